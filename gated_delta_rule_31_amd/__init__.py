@@ -117,6 +117,18 @@ def _load():
     lib.kda_chunk_bwd.restype = i32
     lib.kda_bounded_decay_bwd.argtypes = [vp, i32, vp, vp, f32, i64, i32, i32, vp, i32, vp, i32, vp, vp, vp]
     lib.kda_bounded_decay_bwd.restype = i32
+    lib.kda_gdr_chunk_fwd_workspace_size.argtypes = [i32, i32, i64, i32, i32, i32, i32, i32, i32]
+    lib.kda_gdr_chunk_fwd_workspace_size.restype = sz
+    lib.kda_gdr_chunk_fwd.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, vp, i32, i32, i64, i32, i32, i32, i32, f32, vp,
+                                      i32, vp, sz, vp]
+    lib.kda_gdr_chunk_fwd.restype = i32
+    lib.kda_gdr_recurrent_step.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp, i64, vp, i32, vp, vp, i32, i32, i32, i32,
+                                           i32, i32, f32, vp, i32, vp]
+    lib.kda_gdr_recurrent_step.restype = i32
+    lib.kda_draft_verify_workspace_size.argtypes = [i32, i32]
+    lib.kda_draft_verify_workspace_size.restype = sz
+    lib.kda_draft_verify.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, sz, vp]
+    lib.kda_draft_verify.restype = i32
     lib.kda_status_string.argtypes = [i32]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_abi_version.argtypes = []
@@ -670,3 +682,9 @@ def recurrent_kda(q, k, v, alpha, beta, initial_state=None, chunk_size: int = 32
         return chunk_fwd(q, k, v, alpha, beta, initial_state=initial_state, output_final_state=True,
                          chunk_size=chunk_size, scale=scale)
     return recurrent_fwd(q, k, v, alpha, beta, initial_state=initial_state, output_final_state=True, scale=scale)
+
+
+from .gdr import (draft_verify, gdr_chunk_fwd, gdr_chunk_fwd_workspace_size,  # noqa: E402
+                  gdr_recurrent_step)
+
+__all__ += ["gdr_chunk_fwd", "gdr_chunk_fwd_workspace_size", "gdr_recurrent_step", "draft_verify"]

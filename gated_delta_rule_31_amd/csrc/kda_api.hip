@@ -10,10 +10,22 @@ namespace {
 
 thread_local char g_last_hip_error[256] = "";
 
-kda_status hip_fail(hipError_t e) {
+}  // namespace
+
+namespace kda {
+
+void record_hip_error(hipError_t e) {
     const char *msg = hipGetErrorString(e);
     strncpy(g_last_hip_error, msg ? msg : "unknown HIP error", sizeof(g_last_hip_error) - 1);
     g_last_hip_error[sizeof(g_last_hip_error) - 1] = 0;
+}
+
+}  // namespace kda
+
+namespace {
+
+kda_status hip_fail(hipError_t e) {
+    kda::record_hip_error(e);
     return e == hipErrorNotSupported ? KDA_ERR_UNSUPPORTED : KDA_ERR_HIP;
 }
 

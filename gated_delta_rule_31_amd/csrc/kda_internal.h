@@ -182,6 +182,8 @@ hipError_t launch_recurrent_fwd(const RecurrentArgs &a, bool fp32_inputs, int K,
 hipError_t launch_bounded_decay(const GateArgs &a, bool fp32_logits, hipStream_t stream);
 // dst[i] = src ? src[i] : 0 for i < n
 hipError_t launch_fill_copy(float *dst, const float *src, int64_t n, hipStream_t stream);
+// keeps the text of a launch error for kda_last_hip_error (per thread)
+void record_hip_error(hipError_t e);
 // compute units of the current device (queried once per device; 256 if the query fails)
 int device_cu_count();
 

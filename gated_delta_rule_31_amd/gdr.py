@@ -1,0 +1,191 @@
+"""The gated delta rule with one decay per value head, and decoding with drafted tokens.
+
+* ``gdr_chunk_fwd(q, k, v, g, beta, ...)`` -- prefill: g and beta per value head, q and k
+  shared by the HV / HK value heads of a group; packed sequences, initial and final states.
+* ``gdr_recurrent_step(q, k, v, g, beta, states, ...)`` -- decode: one or several tokens a
+  request over a pool of states, the state after every drafted token in a slot of its own;
+  a decay per value head, or per channel as KDA has it.
+* ``draft_verify(target_probs, draft_tokens, uniforms, ...)`` -- which drafted tokens hold
+  against the target's probabilities, and the token behind them; its ``accepted`` is the
+  next ``gdr_recurrent_step``'s ``start``.
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+from . import _check, _dev, _dtype_code, _load, _ptr, _stream
+
+
+def _input(x: Optional[torch.Tensor], name: str, like: Optional[torch.Tensor] = None, dtype=None) -> Optional[torch.Tensor]:
+    """A dense tensor on the device of ``like``, on a 16-byte border (copied to one if need be)."""
+    x = _dev(x, name, dtype)
+    if x is None:
+        return None
+    if like is not None and x.device != like.device:
+        raise ValueError("%s is on %s, but q is on %s" % (name, x.device, like.device))
+    return x.clone() if x.data_ptr() % 16 else x
+
+
+def _output(x: torch.Tensor, name: str, shape, dtype, device) -> torch.Tensor:
+    """A caller's buffer that is written in place: it has to be what the kernels write as it is."""
+    if (not isinstance(x, torch.Tensor) or tuple(x.shape) != tuple(shape) or x.dtype != dtype or x.device != device
+            or not x.is_contiguous()):
+        raise ValueError("%s must be a contiguous %s tensor %s on %s" % (name, dtype, list(shape), device))
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError("%s requires grad: it is written in place" % name)
+    return x
+
+
+def _workspace(x: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
+    if x is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    if x.device != device or x.dtype != torch.uint8 or not x.is_contiguous() or x.numel() < need:
+        raise ValueError("workspace must be a contiguous uint8 tensor of at least %d bytes on %s" % (need, device))
+    return x
+
+
+def _chunk_inputs(q, k, v, g, beta, initial_state, cu_seqlens):
+    q = _input(q, "q")
+    if q is None:
+        raise TypeError("q must be a torch.Tensor")
+    k, v = _input(k, "k", q, q.dtype), _input(v, "v", q, q.dtype)
+    g, beta = _input(g, "g", q, torch.float32), _input(beta, "beta", q, torch.float32)
+    initial_state = _input(initial_state, "initial_state", q, torch.float32)
+    cu_seqlens = _input(cu_seqlens, "cu_seqlens", q, torch.int32)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k must be [B, T, HK, K] and v [B, T, HV, V]")
+    B, T, HK, K = q.shape
+    HV, V = v.shape[2:]
+    if k.shape != q.shape or v.shape[:2] != (B, T) or g.shape != (B, T, HV) or beta.shape != (B, T, HV):
+        raise ValueError("inconsistent shapes: q %s k %s v %s g %s beta %s" % tuple(tuple(x.shape) for x in (q, k, v, g, beta)))
+    if cu_seqlens is not None and (cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1):
+        raise ValueError("cu_seqlens must be int32 [N + 1]")
+    N = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    if initial_state is not None and initial_state.shape != (N, HV, K, V):
+        raise ValueError("initial_state must be %s" % [N, HV, K, V])
+    return q, k, v, g, beta, initial_state, cu_seqlens, (B, T, HK, HV, K, V, N)
+
+
+def gdr_chunk_fwd_workspace_size(dtype: torch.dtype, B: int, T: int, HK: int, HV: int, K: int, V: int, num_seqs: int = 0,
+                                 varlen: bool = False) -> int:
+    """Bytes of device workspace ``gdr_chunk_fwd`` needs for this shape (0: unsupported or empty)."""
+    return int(_load().kda_gdr_chunk_fwd_workspace_size(_dtype_code(dtype), int(B), int(T), int(num_seqs), 1 if varlen else 0, int(HK),
+                                                        int(HV), int(K), int(V)))
+
+
+def gdr_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                  initial_state: Optional[torch.Tensor] = None, output_final_state: bool = True,
+                  cu_seqlens: Optional[torch.Tensor] = None, scale: float = 1.0, out_dtype: Optional[torch.dtype] = None,
+                  out: Optional[torch.Tensor] = None, final_state: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Prefill of the gated delta rule.  q, k [B,T,HK,K]; v [B,T,HV,V] (one dtype, float32 or
+    bfloat16; HV a multiple of HK); g [B,T,HV] float32 log decays (<= 0, -inf allowed); beta
+    [B,T,HV] float32; initial_state [N,HV,K,V] float32 or None (zeros); cu_seqlens int32 [N+1]
+    (B == 1) or None.  Returns (out [B,T,HV,V], final_state [N,HV,K,V] or None).  ``final_state``
+    may be passed in (it may be ``initial_state``).  Rows of ``out`` behind the last packed
+    sequence are left as they were (zeros in an ``out`` made here)."""
+    q, k, v, g, beta, initial_state, cu_seqlens, (B, T, HK, HV, K, V, N) = _chunk_inputs(q, k, v, g, beta, initial_state, cu_seqlens)
+    od, dev = out_dtype or v.dtype, q.device
+    if out is None:
+        out = (torch.empty if cu_seqlens is None else torch.zeros)((B, T, HV, V), dtype=od, device=dev)
+    out = _output(out, "out", (B, T, HV, V), od, dev)
+    if output_final_state and final_state is None:
+        final_state = torch.empty((N, HV, K, V), dtype=torch.float32, device=dev)
+    if final_state is not None:
+        final_state = _output(final_state, "final_state", (N, HV, K, V), torch.float32, dev)
+    workspace = _workspace(workspace, gdr_chunk_fwd_workspace_size(q.dtype, B, T, HK, HV, K, V, N, cu_seqlens is not None), dev)
+    with torch.cuda.device(dev):
+        st = _load().kda_gdr_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q.dtype), _ptr(g), _ptr(beta), _ptr(initial_state),
+                                       _ptr(final_state), _ptr(cu_seqlens), N, B, T, HK, HV, K, V, float(scale), _ptr(out),
+                                       _dtype_code(od), _ptr(workspace), workspace.numel(), _stream(q))
+    _check("kda_gdr_chunk_fwd", st)
+    return out, final_state
+
+
+def gdr_recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, states: torch.Tensor,
+                       slots: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None,
+                       lengths: Optional[torch.Tensor] = None, scale: float = 1.0, out_dtype: Optional[torch.dtype] = None,
+                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Up to S tokens for each of B requests over a pool of states.  q, k [B,S,HK,K]; v
+    [B,S,HV,V]; g [B,S,HV] float32 log decays, or [B,S,HV,K], one per channel; beta [B,S,HV]
+    float32; states [pool,HV,K,V] float32 contiguous, updated in place.
+
+    slots int32 [B, S]: the state after each token goes to a slot of its own (a slot outside the
+    pool keeps none), and a request starts from ``slots[b, start[b]]``, ``start`` int32 [B] being
+    the number of drafts that held (None: column 0).  slots [B] or [B, 1]: a request starts from
+    its slot and leaves the state after its last token there; None: slot b.  A slot that one
+    request writes must not be named by another.  lengths int32 [B]: tokens of each request
+    (None: S); rows of ``out`` behind them are left as they were (zeros in an ``out`` made here).
+    Returns out [B,S,HV,V]."""
+    q = _input(q, "q")
+    if q is None:
+        raise TypeError("q must be a torch.Tensor")
+    k, v = _input(k, "k", q, q.dtype), _input(v, "v", q, q.dtype)
+    g, beta = _input(g, "g", q, torch.float32), _input(beta, "beta", q, torch.float32)
+    slots, start, lengths = (_input(x, n, q, torch.int32) for x, n in ((slots, "slots"), (start, "start"), (lengths, "lengths")))
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k must be [B, S, HK, K] and v [B, S, HV, V]")
+    B, S, HK, K = q.shape
+    HV, V = v.shape[2:]
+    if k.shape != q.shape or v.shape[:2] != (B, S) or beta.shape != (B, S, HV) or tuple(g.shape) not in ((B, S, HV), (B, S, HV, K)):
+        raise ValueError("inconsistent shapes: q %s k %s v %s g %s beta %s" % tuple(tuple(x.shape) for x in (q, k, v, g, beta)))
+    dev = q.device
+    if not isinstance(states, torch.Tensor) or states.dim() != 4:
+        raise ValueError("states must be [pool, HV, K, V]")
+    pool = states.shape[0]
+    states = _output(states, "states", (pool, HV, K, V), torch.float32, dev)
+    cols = 1
+    if slots is not None:
+        cols = 1 if slots.dim() == 1 else slots.shape[-1]
+        if slots.dim() not in (1, 2) or slots.shape[0] != B or cols not in (1, S):
+            raise ValueError("slots must be [B], [B, 1] or [B, S]")
+    if slots is None and (start is not None or pool < B):
+        raise ValueError("without slots every request has a state of its own, states[b], and starts from it")
+    if any(x is not None and x.shape != (B,) for x in (start, lengths)):
+        raise ValueError("start and lengths must be [B]")
+    od = out_dtype or v.dtype
+    if out is None:
+        out = (torch.empty if lengths is None else torch.zeros)((B, S, HV, V), dtype=od, device=dev)
+    out = _output(out, "out", (B, S, HV, V), od, dev)
+    with torch.cuda.device(dev):
+        st = _load().kda_gdr_recurrent_step(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q.dtype), _ptr(g), 1 if g.dim() == 4 else 0, _ptr(beta),
+                                            _ptr(states), pool, _ptr(slots), cols, _ptr(start), _ptr(lengths), B, S, HK, HV, K, V,
+                                            float(scale), _ptr(out), _dtype_code(od), _stream(q))
+    _check("kda_gdr_recurrent_step", st)
+    return out
+
+
+def draft_verify(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uniforms: torch.Tensor,
+                 draft_probs: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None
+                 ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The drafted tokens of B requests against the target's probabilities.  target_probs
+    [B,D+1,vocab] float32; draft_tokens int32 [B,D]; draft_probs [B,D,vocab] float32, what the
+    drafts were drawn from (None: each was certain); uniforms [B,D+1] float32 in [0, 1): one for
+    each draft, and one to draw with; lengths int32 [B]: drafts of each request (None: D).
+
+    Draft i holds while u_i q_i(x_i) < p_i(x_i).  Behind the last that holds one token is drawn,
+    from max(p - q, 0) where a draft was refused (from p if that is nothing), from p where none
+    was; in whole weights of 2^-44, so that no order of summation changes it.  Returns (tokens
+    int32 [B,D+1]: the drafts that hold, the token drawn, then -1; accepted int32 [B])."""
+    p = _input(target_probs, "target_probs", None, torch.float32)
+    if p is None:
+        raise TypeError("target_probs must be a torch.Tensor")
+    x, u = _input(draft_tokens, "draft_tokens", p, torch.int32), _input(uniforms, "uniforms", p, torch.float32)
+    q, lengths = _input(draft_probs, "draft_probs", p, torch.float32), _input(lengths, "lengths", p, torch.int32)
+    if p.dim() != 3 or p.shape[1] < 1:
+        raise ValueError("target_probs must be [B, D + 1, vocab]")
+    B, D, vocab = p.shape[0], p.shape[1] - 1, p.shape[2]
+    if x.shape != (B, D) or u.shape != (B, D + 1) or (q is not None and q.shape != (B, D, vocab)) or (
+            lengths is not None and lengths.shape != (B,)):
+        raise ValueError("draft_tokens must be [B, D], uniforms [B, D + 1], draft_probs [B, D, vocab] and lengths [B]")
+    dev = p.device
+    tokens = torch.empty((B, D + 1), dtype=torch.int32, device=dev)
+    accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+    workspace = _workspace(None, int(_load().kda_draft_verify_workspace_size(B, vocab)), dev)
+    with torch.cuda.device(dev):
+        st = _load().kda_draft_verify(_ptr(p), _ptr(x), _ptr(q), _ptr(u), _ptr(lengths), B, D, vocab, _ptr(tokens), _ptr(accepted),
+                                      _ptr(workspace), workspace.numel(), _stream(p))
+    _check("kda_draft_verify", st)
+    return tokens, accepted

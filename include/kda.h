@@ -341,6 +341,90 @@ kda_status kda_chunk_fwd_fused_gate_noalloc(const void *q, const void *k, const 
 /* bytes of that device array (KDA_NOALLOC_SCRATCH_BYTES) */
 size_t kda_noalloc_scratch_bytes(void);
 
+/*
+ * The gated delta rule with one decay per value head (cheat sheet "Lineage" table, the
+ * Gated DeltaNet row, of which KDA is the form with a decay per channel):
+ *     S_t = e^{g_t} S_{t-1} + beta_t k_t (v_t - e^{g_t} S_{t-1}^T k_t)^T,   o_t = scale S_t^T q_t
+ * for every value head, with q and k shared by the HV / HK value heads of a group (value
+ * head h uses key head h / (HV / HK)).  Conventions of every kda_gdr_* call:
+ *   q, k   [B, T, HK, K] and v [B, T, HV, V] in in_dtype; HV a multiple of HK
+ *   g      [B, T, HV] float32 log decays, g <= 0; -inf forgets the state.  No lower bound.
+ *   beta   [B, T, HV] float32 write strengths, any finite value
+ *   states [N, HV, K, V] float32
+ * K and V in {16, 32, 64, 128} (KDA_ERR_UNSUPPORTED otherwise).  q, k, v, states, gradients,
+ * workspaces must be 16-byte aligned, out too (KDA_ERR_BAD_ARGUMENT otherwise).  The other
+ * conventions of this file hold.
+ *
+ * kda_gdr_chunk_fwd -- prefill, 64 tokens at a time.  initial_state, final_state, cu_seqlens,
+ * num_seqs, scale and the empty-sequence rule are those of kda_chunk_fwd; cu_seqlens[num_seqs]
+ * may be below T: rows of `out` behind the last sequence are left as they were.  Offsets
+ * outside [0, T] or out of order are brought into range on the device (no access outside the
+ * tensors; the results are then unspecified).  The workspace is scratch as in kda_chunk_fwd
+ * (required; at least kda_gdr_chunk_fwd_workspace_size bytes, which is 0 for a shape that is
+ * not supported).  bf16 inputs are exact on the matrix cores; states and corrected values
+ * enter them with 16 mantissa bits (24 with float32 inputs) and float32 sums, so the
+ * relative error of out and of final_state is about 1e-5 at most, before `out` is rounded to
+ * its type.
+ */
+size_t kda_gdr_chunk_fwd_workspace_size(kda_dtype in_dtype, int B, int64_t T, int num_seqs, int varlen, int HK,
+                                        int HV, int K, int V);
+kda_status kda_gdr_chunk_fwd(const void *q, const void *k, const void *v, kda_dtype in_dtype, const float *g,
+                             const float *beta, const float *initial_state, float *final_state,
+                             const int32_t *cu_seqlens, int num_seqs, int B, int64_t T, int HK, int HV, int K, int V,
+                             float scale, void *out, kda_dtype out_dtype, void *workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
+/*
+ * kda_gdr_recurrent_step -- decode: up to S tokens for each of B requests over a pool of kept
+ * states, token by token in float32, so that drafted tokens can be checked (kda_draft_verify)
+ * and the state after any of them taken up again.
+ *   q, k   [B, S, HK, K], v [B, S, HV, V], beta [B, S, HV], out [B, S, HV, V]
+ *   g      [B, S, HV], or with g_channels != 0 [B, S, HV, K]: a decay per channel (KDA)
+ *   states [pool, HV, K, V] float32, updated in place
+ *   slots  [B, slot_cols] int32: with slot_cols == S > 1 the state after token t of request b
+ *          is written to slot slots[b, t]; with slot_cols == 1 the state after the last token
+ *          to slots[b, 0].  NULL: slot b (slot_cols must be 1, pool >= B).
+ *   start  [B] int32 or NULL: request b starts from the state in slots[b, start[b]] (NULL: from
+ *          slots[b, 0]) -- after a round of drafting, the number of drafts that held.
+ *   lengths [B] int32 or NULL: tokens of request b, 0..S (brought into that range; NULL: S).
+ *          Rows of `out` and slots behind a request's last token are left as they were.
+ * A slot outside 0..pool-1 holds no state: nothing is written to it, and a request that starts
+ * from one (or from a column outside 0..slot_cols-1) starts from zeros.  A request may read and
+ * write the same slot, and may name a slot twice (the later token's state stays); a slot that
+ * one request writes must not be named by another.  B == 0 or S == 0 enqueues nothing.
+ */
+kda_status kda_gdr_recurrent_step(const void *q, const void *k, const void *v, kda_dtype in_dtype, const float *g,
+                                  int g_channels, const float *beta, float *states, int64_t pool,
+                                  const int32_t *slots, int slot_cols, const int32_t *start, const int32_t *lengths,
+                                  int B, int S, int HK, int HV, int K, int V, float scale, void *out,
+                                  kda_dtype out_dtype, hipStream_t stream);
+
+/*
+ * kda_draft_verify -- the drafted tokens of B requests against the target's probabilities.
+ *   target_probs [B, D + 1, vocab] float32: row i is the target's distribution of the token
+ *                that draft i stands for, row D (or row lengths[b]) of the one behind them
+ *   draft_tokens [B, D] int32
+ *   draft_probs  [B, D, vocab] float32, what the drafts were drawn from, or NULL: each draft
+ *                was certain
+ *   uniforms     [B, D + 1] float32 in [0, 1): one for each draft, and one to draw with
+ *   lengths      [B] int32 or NULL: drafts of request b, 0..D (brought into that range; NULL: D)
+ *   tokens       [B, D + 1] int32: the drafts that hold, the token drawn, then -1
+ *   accepted     [B] int32: how many drafts hold
+ * Draft i holds while u_i q_i(x_i) < p_i(x_i) (compared exactly; a draft outside the vocabulary
+ * does not hold).  Behind the last that holds one token is drawn: from max(p - q, 0) of the
+ * first draft that does not hold (from p if that is nothing), or from p behind all of them.
+ * The token drawn is the first whose running sum of weights passes floor(u * sum), the weights
+ * being whole numbers of 2^-44 (clamped to [0, 1], cut, NaN as 0): the result does not depend
+ * on any order of summation.  A row without any weight gives token 0; a uniform of 1 or more
+ * the last token that has weight.
+ * D >= 0, 1 <= vocab <= 2^19.  `workspace`: 8-byte aligned scratch of at least
+ * kda_draft_verify_workspace_size bytes.  B == 0 enqueues nothing.
+ */
+size_t kda_draft_verify_workspace_size(int B, int vocab);
+kda_status kda_draft_verify(const float *target_probs, const int32_t *draft_tokens, const float *draft_probs,
+                            const float *uniforms, const int32_t *lengths, int B, int D, int vocab, int32_t *tokens,
+                            int32_t *accepted, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* A static, human-readable name for a status code. */
 const char *kda_status_string(kda_status s);
 

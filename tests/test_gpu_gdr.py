@@ -1,0 +1,393 @@
+"""GPU parity of the gated delta rule with one decay per value head (gdr_chunk_fwd) and of
+decoding with drafted tokens (gdr_recurrent_step, draft_verify) against plain 64-bit forms.
+
+Tolerances, set from the roundings that the kernels make:
+
+* float32 inputs: operands are sums of three bf16 parts, off by at most 2^-24 of the value,
+  and float32 sums of at most 128 + 64 terms: sqrt(192) 2^-24 is 8e-7 of a sum's terms; a
+  dozen such sums follow one another in a chunk: 1e-5.
+* bfloat16 inputs: state, M, beta X, Vn enter as two parts, each off by at most 2^-16 of the
+  value; five such roundings in a chunk, which fade or are corrected like the state itself,
+  give at most 5 2^-16 = 7.6e-5 of the terms, and terms reach about 6 times the rms: 5e-4 of
+  the rms for the largest element, and (as they are independent, with an rms of 2^-18 each)
+  2^-16 in the 2-norm.
+* an output in bfloat16 is rounded once more, by at most half a step, 2^-8 of the value.
+* the decode step is float32 throughout, sums of at most 128 terms: 128 2^-24 = 8e-6 of them.
+"""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_31_amd as kda
+from tests import gdr_reference as ref
+from tests.helpers import err_bf16, err_fp32, f64
+
+pytestmark = pytest.mark.gpu
+
+
+def _gpu(i):
+    return {n: x.cuda() if isinstance(x, torch.Tensor) else x for n, x in i.items()}
+
+
+def _norm(got, want):
+    return float(np.linalg.norm(f64(got) - want) / max(np.linalg.norm(want), 1e-300))
+
+
+def _fwd(i, scale=1.0, **kw):
+    d = _gpu(i)
+    return kda.gdr_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["beta"], initial_state=d["s0"], cu_seqlens=d["cu"], scale=scale, **kw)
+
+
+def _check(out, final, i, scale, dtype, what=""):
+    eo, ef = ref.scan(i, scale)
+    for name, got, want in (("out", out, eo), ("state", final, ef)):
+        assert np.all(np.isfinite(f64(got))), "%s %s is not finite" % (what, name)
+        if dtype == torch.float32:
+            e = err_fp32(got, want)
+            assert e <= 1e-5, "%s %s: %.2e" % (what, name, e)
+        elif got.dtype == torch.float32:
+            e, n = err_bf16(got, want), _norm(got, want)
+            assert e <= 5e-4 and n <= 2.0 ** -16, "%s %s: %.2e of the rms, %.2e in norm" % (what, name, e, n)
+        else:
+            rms = np.sqrt(np.mean(want ** 2))
+            assert np.all(np.abs(f64(got) - want) <= 2.0 ** -8 * np.abs(want) + 5e-4 * rms), "%s %s" % (what, name)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("K,V", [(16, 16), (32, 128), (64, 32), (128, 64), (128, 128), (16, 128)])
+def test_fwd_widths(dtype, K, V):
+    i = ref.make(2, 150, 2, 6, K, V, dtype, seed=K + V)
+    out, final = _fwd(i, 0.7, out_dtype=torch.float32)
+    _check(out, final, i, 0.7, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 63, 64, 65, 128, 129, 300])
+def test_fwd_lengths(dtype, T):
+    i = ref.make(1, T, 1, 2, 64, 64, dtype, seed=T, state=T % 2 == 0)
+    out, final = _fwd(i)
+    _check(out, final, i, 1.0, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lens", [[70, 0, 1, 64, 130], [0, 0, 3], [1, 1, 1, 1], [65, 63, 0], [200]])
+def test_fwd_packed(dtype, lens):
+    i = ref.make(1, sum(lens), 2, 4, 32, 48 - 16, dtype, seed=sum(lens), seqlens=lens)
+    out, final = _fwd(i, 0.5, out_dtype=torch.float32)
+    _check(out, final, i, 0.5, dtype)
+
+
+def test_fwd_rows_behind_the_last_sequence_stay():
+    i = _gpu(ref.make(1, 200, 2, 4, 32, 32, torch.bfloat16, seed=3, seqlens=[90, 40]))
+    full = {n: i[n] for n in ("q", "k", "v", "g", "beta")}
+    pad = {n: torch.cat([x[:, :130], torch.full_like(x[:, :70], float("nan"))], 1) for n, x in full.items()}
+    out = torch.full((1, 200, 4, 32), 7.0, device="cuda", dtype=torch.bfloat16)
+    got, fin = kda.gdr_chunk_fwd(**pad, initial_state=i["s0"], cu_seqlens=i["cu"], out=out)
+    want, wfin = kda.gdr_chunk_fwd(**{n: x[:, :130] for n, x in full.items()}, initial_state=i["s0"], cu_seqlens=i["cu"])
+    assert got is out and torch.equal(got[:, :130], want) and torch.equal(fin, wfin) and bool((got[:, 130:] == 7).all())
+
+
+@pytest.mark.parametrize("what", ["no decay", "forgets", "forgets within", "repeated key", "no writes", "far decays"])
+def test_fwd_regimes(what):
+    i = ref.make(1, 140, 1, 3, 64, 32, torch.float32, seed=11)
+    if what == "no decay":
+        i["g"].zero_()
+    elif what == "forgets":
+        i["g"].fill_(-np.inf)
+    elif what == "forgets within":  # a state, and the tokens before, gone at some tokens only
+        i["g"][0, [0, 5, 63, 64, 100]] = -np.inf
+    elif what == "far decays":  # sums far below what float32 keeps apart
+        i["g"][0, 3] = -900.0
+        i["g"][0, 70:75] = -300.0
+    elif what == "repeated key":
+        i["k"] = i["k"][:, :1].expand_as(i["k"]).contiguous()
+        i["g"].zero_()
+        i["beta"].fill_(1.0)
+    else:
+        i["beta"].zero_()
+    out, final = _fwd(i)
+    _check(out, final, i, 1.0, torch.float32, what)
+
+
+def test_fwd_large_values_and_strengths():
+    i = ref.make(1, 130, 1, 2, 32, 32, torch.bfloat16, seed=5)
+    i["v"] = (i["v"].float() * 3e18).to(torch.bfloat16)
+    i["s0"] = i["s0"] * 1e18
+    i["beta"] = 2 * i["beta"]
+    out, final = _fwd(i, out_dtype=torch.float32)
+    _check(out, final, i, 1.0, torch.bfloat16)
+
+
+def test_fwd_resumes_and_stays_deterministic():
+    i = ref.make(2, 230, 2, 4, 128, 64, torch.float32, seed=21)
+    d = _gpu(i)
+    args = [d[n] for n in ("q", "k", "v", "g", "beta")]
+    keep = [x.clone() for x in args]
+    out, fin = kda.gdr_chunk_fwd(*args, initial_state=d["s0"])
+    again, fin2 = kda.gdr_chunk_fwd(*args, initial_state=d["s0"])
+    assert torch.equal(out, again) and torch.equal(fin, fin2) and all(torch.equal(x, y) for x, y in zip(args, keep))
+    o1, s = kda.gdr_chunk_fwd(*[x[:, :101] for x in args], initial_state=d["s0"])
+    o2, s2 = kda.gdr_chunk_fwd(*[x[:, 101:] for x in args], initial_state=s, final_state=s)  # in place
+    assert s2 is s
+    _check(torch.cat([o1, o2], 1), s, i, 1.0, torch.float32, "two parts")
+
+
+def test_fwd_takes_views_and_misaligned_tensors():
+    i = ref.make(1, 70, 2, 2, 32, 32, torch.bfloat16, seed=8)
+    d = _gpu(i)
+    wide = torch.cat([d["q"], d["k"], d["v"]], -1)  # q, k, v as parts of one projection
+    flat = torch.empty(d["v"].numel() + 3, device="cuda", dtype=torch.bfloat16)
+    flat[3:] = d["v"].reshape(-1)
+    a = kda.gdr_chunk_fwd(wide[..., :32], wide[..., 32:64], wide[..., 64:], d["g"], d["beta"], initial_state=d["s0"])
+    b = kda.gdr_chunk_fwd(d["q"], d["k"], flat[3:].reshape(d["v"].shape), d["g"], d["beta"], initial_state=d["s0"])
+    c = kda.gdr_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["beta"], initial_state=d["s0"])
+    assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(a, b, c))
+
+
+def test_fwd_empty():
+    s0 = torch.randn(2, 4, 16, 32, device="cuda")
+    z = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    out, fin = kda.gdr_chunk_fwd(z(2, 0, 2, 16), z(2, 0, 2, 16), z(2, 0, 4, 32), z(2, 0, 4), z(2, 0, 4), initial_state=s0)
+    assert out.shape == (2, 0, 4, 32) and torch.equal(fin, s0)
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    out, fin = kda.gdr_chunk_fwd(z(1, 9, 2, 16), z(1, 9, 2, 16), z(1, 9, 4, 32), z(1, 9, 4), z(1, 9, 4), cu_seqlens=cu)
+    assert not fin.any() and not out.any()
+
+
+def test_fwd_graph_and_other_stream():
+    """Captured and replayed with new inputs in place, between eager calls on another stream."""
+    d = _gpu(ref.make(1, 200, 2, 4, 64, 64, torch.bfloat16, seed=31))
+    args = [d[n] for n in ("q", "k", "v", "g", "beta")]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        kda.gdr_chunk_fwd(*args, initial_state=d["s0"])
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, fin = kda.gdr_chunk_fwd(*args, initial_state=d["s0"])
+    for seed in (32, 33, 34):
+        n = _gpu(ref.make(1, 200, 2, 4, 64, 64, torch.bfloat16, seed=seed))
+        for x, name in zip(args, ("q", "k", "v", "g", "beta")):
+            x.copy_(n[name])
+        d["s0"].copy_(n["s0"])
+        graph.replay()
+        want, wfin = kda.gdr_chunk_fwd(*args, initial_state=d["s0"])
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(fin, wfin)
+
+
+# ------------------------------------------------------------------------------ decode
+
+def _step_case(B, S, HK, HV, K, V, dtype, seed, channels=False, pool=None):
+    i = ref.make(B, S, HK, HV, K, V, dtype, seed=seed, state=False)
+    gen = torch.Generator().manual_seed(seed + 1)
+    if channels:
+        i["g"] = -torch.nn.functional.softplus(torch.randn(B, S, HV, K, generator=gen))
+    pool = pool or B * S + 2
+    i["states"] = 0.3 * torch.randn(pool, HV, K, V, generator=gen)
+    i["slots"] = torch.randperm(max(pool, B * S), generator=gen)[: B * S].reshape(B, S).to(torch.int32)
+    return i
+
+
+def _step_check(i, start, lengths, scale, dtype, slots=None, out_dtype=torch.float32):
+    d = _gpu(i)
+    slots = i["slots"] if slots is None else slots
+    B, S, HV = i["beta"].shape
+    out = torch.full((B, S, HV, i["v"].shape[-1]), float("nan"), device="cuda", dtype=out_dtype)
+    up = lambda x: None if x is None else x.cuda()  # noqa: E731
+    kda.gdr_recurrent_step(d["q"], d["k"], d["v"], d["g"], d["beta"], d["states"], slots=up(slots), start=up(start), lengths=up(lengths),
+                           scale=scale, out_dtype=out_dtype, out=out)
+    wo, ws = ref.step(i["q"], i["k"], i["v"], i["g"], i["beta"], i["states"], slots.reshape(B, -1), start, lengths, scale)
+    out = f64(out)
+    assert np.array_equal(np.isnan(out), np.isnan(wo))
+    there = ~np.isnan(wo)
+    assert err_fp32(out[there], wo[there]) <= (1e-5 if out_dtype == torch.float32 else 2.0 ** -8 + 1e-5)
+    assert err_fp32(d["states"], ws) <= 1e-5
+    # slots that nothing is written to keep their bits
+    same = np.array([np.array_equal(ws[p], f64(i["states"][p])) for p in range(len(ws))])
+    assert torch.equal(d["states"].cpu()[same], i["states"][same])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("channels", [False, True])
+@pytest.mark.parametrize("K,V", [(16, 16), (16, 64), (32, 32), (64, 16), (64, 128), (128, 32), (128, 128), (128, 16)])
+def test_step_widths(dtype, channels, K, V):
+    i = _step_case(3, 3, 2, 4, K, V, dtype, K + V, channels)
+    _step_check(i, torch.tensor([0, 2, 1], dtype=torch.int32), torch.tensor([3, 1, 2], dtype=torch.int32), 0.6, dtype)
+
+
+@pytest.mark.parametrize("B,HV", [(1, 1), (5, 6), (70, 32)])
+def test_step_single_token_in_place(B, HV):
+    i = _step_case(B, 1, HV, HV, 64, 64, torch.bfloat16, B, pool=B + 1)
+    _step_check(i, None, None, 1.0, torch.bfloat16, out_dtype=torch.bfloat16)
+    one = _step_case(B, 1, HV, HV, 64, 64, torch.float32, B, pool=B)
+    d = _gpu(one)
+    a, b = d["states"].clone(), d["states"].clone()
+    args = [d[n] for n in ("q", "k", "v", "g", "beta")]
+    x = kda.gdr_recurrent_step(*args, a)
+    y = kda.gdr_recurrent_step(*args, b, slots=torch.arange(B, dtype=torch.int32, device="cuda"))
+    assert torch.equal(x, y) and torch.equal(a, b)
+
+
+def test_step_slots_outside_the_pool_and_named_twice():
+    i = _step_case(4, 3, 1, 2, 32, 32, torch.float32, 9, pool=10)
+    i["slots"] = torch.tensor([[-1, 0, 1], [2, 2, 2], [99, 3, -7], [4, 5, 4]], dtype=torch.int32)
+    _step_check(i, torch.tensor([0, 1, 0, 3], dtype=torch.int32), torch.tensor([3, 3, 9, -2], dtype=torch.int32), 1.0, torch.float32)
+    _step_check(i, torch.tensor([2, -1, 1, 0], dtype=torch.int32), None, 1.0, torch.float32)
+
+
+def test_step_one_slot_for_several_tokens():
+    i = _step_case(3, 4, 2, 2, 32, 64, torch.bfloat16, 10, pool=6)
+    _step_check(i, None, torch.tensor([4, 0, 2], dtype=torch.int32), 1.0, torch.bfloat16, slots=torch.tensor([5, 0, 2], dtype=torch.int32))
+
+
+def test_step_forgets():
+    i = _step_case(2, 2, 1, 2, 16, 16, torch.float32, 12)
+    i["g"][0, 0] = -np.inf
+    _step_check(i, None, None, 1.0, torch.float32)
+
+
+def test_step_follows_the_prefill():
+    """Prefill, then the rest token by token: the same states and outputs as one prefill."""
+    i = ref.make(2, 90, 2, 4, 64, 64, torch.float32, seed=13)
+    d = _gpu(i)
+    args = [d[n] for n in ("q", "k", "v", "g", "beta")]
+    _, states = kda.gdr_chunk_fwd(*[x[:, :86] for x in args], initial_state=d["s0"])
+    outs = [kda.gdr_recurrent_step(*[x[:, t : t + 1] for x in args], states) for t in (86, 87)]
+    outs.append(kda.gdr_recurrent_step(*[x[:, 88:] for x in args], states))
+    eo, ef = ref.scan(i)
+    assert err_fp32(torch.cat(outs, 1), eo[:, 86:]) <= 1e-5 and err_fp32(states, ef) <= 1e-5
+
+
+def test_step_with_kda_decays_matches_recurrent_step():
+    B, H, K, V = 3, 4, 64, 32
+    i = _step_case(B, 1, H, H, K, V, torch.bfloat16, 15, channels=True, pool=B)
+    d = _gpu(i)
+    mine, theirs = d["states"].clone(), d["states"].clone()
+    o = kda.gdr_recurrent_step(d["q"], d["k"], d["v"], d["g"], d["beta"], mine, out_dtype=torch.float32)
+    p = kda.recurrent_step(d["q"][:, 0], d["k"][:, 0], d["v"][:, 0], d["g"][:, 0], d["beta"][:, 0], theirs, gate_is_log=True,
+                           out_dtype=torch.float32)
+    assert err_fp32(o[:, 0], f64(p)) <= 2e-5 and err_fp32(mine, f64(theirs)) <= 2e-5
+
+
+# ------------------------------------------------------------------------------ verification
+
+def _probs(gen, *shape, sharp=2.0):
+    return torch.softmax(sharp * torch.randn(*shape, generator=gen), -1)
+
+
+def _verify(p, x, u, q=None, lengths=None):
+    up = lambda t: None if t is None else t.cuda()  # noqa: E731
+    tokens, accepted = kda.draft_verify(up(p), up(x), up(u), draft_probs=up(q), lengths=up(lengths))
+    wt, wa = ref.verify(p, x, u, q, lengths)
+    assert np.array_equal(accepted.cpu().numpy(), wa)
+    assert np.array_equal(tokens.cpu().numpy(), wt)
+    return tokens, accepted
+
+
+@pytest.mark.parametrize("vocab", [1, 2, 63, 1000, 1024, 1025, 5003, 70001, 300001])
+@pytest.mark.parametrize("drawn", [True, False])
+def test_verify_vocabularies(vocab, drawn):
+    gen = torch.Generator().manual_seed(vocab)
+    B, D = 5, 3
+    q = _probs(gen, B, D, vocab)
+    p = torch.cat([0.5 * q + 0.5 * _probs(gen, B, D, vocab), _probs(gen, B, 1, vocab)], 1)
+    x = torch.multinomial(q.reshape(-1, vocab)[:, : 1 << 20], 1, generator=gen).reshape(B, D).to(torch.int32)
+    _verify(p, x, torch.rand(B, D + 1, generator=gen), q if drawn else None, torch.tensor([3, 0, 1, 2, 3], dtype=torch.int32))
+
+
+@pytest.mark.parametrize("D", [0, 1, 5, 63, 64, 65, 130])
+def test_verify_numbers_of_drafts(D):
+    gen = torch.Generator().manual_seed(D)
+    B, vocab = 9, 40
+    p, q = _probs(gen, B, D + 1, vocab), None
+    x = torch.randint(0, vocab, (B, D), generator=gen).to(torch.int32)
+    u = 0.02 * torch.rand(B, D + 1, generator=gen)  # most drafts hold
+    _verify(p, x, u, q)
+    _verify(p, x, u, _probs(gen, B, D, vocab) if D else None, torch.randint(-1, D + 2, (B,), generator=gen).to(torch.int32))
+
+
+def test_verify_borders():
+    """Equal sides do not hold; a residual of nothing falls back to p; no weight at all is token 0; tokens outside
+    the vocabulary do not hold; u = 0 draws the first token that has weight, and one just below 1 the last."""
+    vocab = 6
+    p = torch.tensor([[0, 0.5, 0.25, 0.25, 0, 0], [0, 0, 0.5, 0.25, 0.25, 0]]).expand(8, 2, vocab).contiguous()
+    q = p[:, :1].clone()
+    x = torch.tensor([1, 1, 1, -1, 6, 0, 2, 1], dtype=torch.int32)[:, None]
+    u = torch.tensor([[1.0, 0.0], [0.999, 0.0], [1.0, 1 - 2.0 ** -24], [0, 0.6], [0, 0.6], [0.0, 0.3], [0.5, 0.5], [1.0, 0.7]])
+    _verify(p, x, u, q)
+    _verify(p, x, u, None)
+    p[1] = 0
+    q[7] *= 0.5
+    q[2, 0, 2] = 1.0
+    _verify(p, x, u, q)
+
+
+def test_verify_odd_values():
+    """NaN and infinite probabilities: comparisons with NaN do not hold, weights are clamped, NaN weighs nothing."""
+    gen = torch.Generator().manual_seed(4)
+    p, q = _probs(gen, 4, 3, 2000), _probs(gen, 4, 2, 2000)
+    p[0, 0, :50] = float("nan")
+    p[1, 0, 7] = float("inf")
+    q[2, 0, ::3] = float("nan")
+    q[3, 1, 5] = float("inf")
+    x = torch.tensor([[3, 1], [8, 1], [0, 2], [4, 5]], dtype=torch.int32)
+    _verify(p, x, torch.rand(4, 3, generator=gen), q)
+
+
+def test_verify_draws_what_it_should():
+    """Over many requests the first tokens are distributed as the target's row, whatever the drafts."""
+    gen = torch.Generator().manual_seed(6)
+    B, vocab = 20000, 8
+    p, q = _probs(gen, 1, 2, vocab).expand(B, 2, vocab).contiguous(), _probs(gen, 1, 1, vocab).expand(B, 1, vocab).contiguous()
+    x = torch.multinomial(q[:, 0], 1, generator=gen).to(torch.int32)
+    tokens, _ = _verify(p, x, torch.rand(B, 2, generator=gen), q)
+    share = np.bincount(tokens[:, 0].cpu().numpy(), minlength=vocab) / B
+    want = f64(p[0, 0])
+    assert np.all(np.abs(share - want) <= 6 * np.sqrt(want * (1 - want) / B) + 1e-9)  # six standard deviations
+
+
+def test_drafted_decoding_end_to_end():
+    """Prefill, then rounds of drafting and verification: the states that a round starts from are those after the
+    last draft that held, so the tokens and states are the ones of decoding token by token with the same choices."""
+    torch.manual_seed(7)
+    B, S, HK, HV, K, V, vocab = 3, 4, 2, 4, 32, 32, 97
+    gen = torch.Generator().manual_seed(17)
+    emb = {n: torch.randn(vocab, *s, generator=gen) for n, s in (("q", (HK, K)), ("k", (HK, K)), ("v", (HV, V)), ("g", (HV,)), ("b", (HV,)))}
+    head = torch.randn(HV * V, vocab, generator=gen)
+
+    def layer(x):  # a token's inputs of the layer
+        unit = lambda y: y / y.norm(dim=-1, keepdim=True)  # noqa: E731
+        return (unit(emb["q"][x]), unit(emb["k"][x]), emb["v"][x], -torch.nn.functional.softplus(emb["g"][x]), torch.sigmoid(emb["b"][x]))
+
+    prompt = torch.randint(0, vocab, (B, 70), generator=gen)
+    up = [t.cuda() for t in layer(prompt)]
+    _, first = kda.gdr_chunk_fwd(*up)
+    states = torch.zeros(B * S + 1, HV, K, V, device="cuda")
+    slots = torch.arange(1, B * S + 1, dtype=torch.int32).reshape(B, S).cuda()
+    states[slots[:, 0].long()] = first
+    start, last = torch.zeros(B, dtype=torch.int32, device="cuda"), prompt[:, -1]
+    history, seen = [list(p.tolist()) for p in prompt], [0] * B
+    last = torch.randint(0, vocab, (B,), generator=gen)
+    for b in range(B):
+        history[b].append(int(last[b]))
+    for _ in range(5):
+        drafts = torch.randint(0, vocab, (B, S - 1), generator=gen)
+        x = torch.cat([last[:, None], drafts], 1)
+        out = kda.gdr_recurrent_step(*[t.cuda() for t in layer(x)], states, slots=slots, start=start)
+        p = torch.softmax(3.0 * out.reshape(B, S, -1) @ head.cuda(), -1)
+        p[:, :-1].scatter_add_(-1, drafts.cuda()[..., None], torch.full((B, S - 1, 1), 0.7, device="cuda"))
+        p = p / p.sum(-1, keepdim=True)
+        tokens, start = kda.draft_verify(p, drafts.to(torch.int32).cuda(), torch.rand(B, S, generator=gen).cuda())
+        for b in range(B):
+            new = [t for t in tokens[b].tolist() if t >= 0]
+            assert len(new) == int(start[b]) + 1
+            history[b] += new
+            last[b] = new[-1]
+            seen[b] += int(start[b])
+    assert sum(seen) > 0
+    for b in range(B):  # all but the newest token are in the state that the next round starts from
+        i = dict(zip(("q", "k", "v", "g", "beta"), layer(torch.tensor([history[b][:-1]]))), s0=None, cu=None)
+        _, want = ref.scan(i)
+        assert err_fp32(states[int(slots[b, int(start[b])])], want[0]) <= 1e-4  # 20 rounds of steps of 1e-5 behind a prefill of 1e-5
