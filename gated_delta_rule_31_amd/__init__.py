@@ -31,6 +31,9 @@ Entry points (same names as the C ABI, minus the ``kda_`` prefix where noted):
   (output, final_state) form of the pages' operator contract, on ``chunk_fwd``; it is
   differentiable (autograd through ``chunk_bwd``), and so is ``bounded_decay`` when its
   inputs require grad (through ``bounded_decay_bwd``).
+* ``gated_delta_rule`` / ``gdr_chunk_fwd`` / ``gdr_chunk_bwd`` -- the same recurrence with one
+  decay per value head and key heads shared by groups of value heads; ``gdr_recurrent_step``
+  and ``draft_verify`` -- decoding over a pool of states with drafted tokens (``gdr.py``).
 """
 from __future__ import annotations
 
@@ -122,6 +125,11 @@ def _load():
     lib.kda_gdr_chunk_fwd.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, vp, i32, i32, i64, i32, i32, i32, i32, f32, vp,
                                       i32, vp, sz, vp]
     lib.kda_gdr_chunk_fwd.restype = i32
+    lib.kda_gdr_chunk_bwd_workspace_size.argtypes = [i32, i32, i64, i32, i32, i32, i32, i32, i32]
+    lib.kda_gdr_chunk_bwd_workspace_size.restype = sz
+    lib.kda_gdr_chunk_bwd.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, i32, i32, i64, i32, i32, i32, i32, f32, vp, i32,
+                                      vp, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]
+    lib.kda_gdr_chunk_bwd.restype = i32
     lib.kda_gdr_recurrent_step.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp, i64, vp, i32, vp, vp, i32, i32, i32, i32,
                                            i32, i32, f32, vp, i32, vp]
     lib.kda_gdr_recurrent_step.restype = i32
@@ -684,7 +692,8 @@ def recurrent_kda(q, k, v, alpha, beta, initial_state=None, chunk_size: int = 32
     return recurrent_fwd(q, k, v, alpha, beta, initial_state=initial_state, output_final_state=True, scale=scale)
 
 
-from .gdr import (draft_verify, gdr_chunk_fwd, gdr_chunk_fwd_workspace_size,  # noqa: E402
-                  gdr_recurrent_step)
+from .gdr import (draft_verify, gated_delta_rule, gdr_chunk_bwd, gdr_chunk_bwd_workspace_size,  # noqa: E402
+                  gdr_chunk_fwd, gdr_chunk_fwd_workspace_size, gdr_recurrent_step)
 
-__all__ += ["gdr_chunk_fwd", "gdr_chunk_fwd_workspace_size", "gdr_recurrent_step", "draft_verify"]
+__all__ += ["gated_delta_rule", "gdr_chunk_fwd", "gdr_chunk_fwd_workspace_size", "gdr_chunk_bwd",
+            "gdr_chunk_bwd_workspace_size", "gdr_recurrent_step", "draft_verify"]

@@ -44,6 +44,24 @@ size_t carve_fwd(kda::GdrArgs &a, void *base, bool fp32, int K) {
     return w.used;
 }
 
+size_t carve_bwd(kda::GdrArgs &a, void *base, bool fp32, int K) {
+    const int C = kda::GDR_C, parts = 3, input_parts = fp32 ? 3 : 1;
+    const int64_t units = a.slots * a.HV;
+    Carver w{static_cast<char *>(base)};
+    w.take(a.M, units * parts * C * C);
+    w.take(a.Mt, units * parts * C * C);
+    w.take(a.P, units * parts * C * C);
+    w.take(a.Kt, a.slots * a.HK * input_parts * K * C);
+    w.take(a.Qt, a.slots * a.HK * input_parts * K * C);
+    w.take(a.dec, units * 4 * C);
+    w.take(a.G, units * C);
+    w.take(a.h, units * K * a.V);
+    w.take(a.dh, units * K * a.V);
+    w.take(a.delta, units * C * a.V);
+    w.take(a.dY, units * C * a.V);
+    return w.used;
+}
+
 bool heads_ok(int HK, int HV) { return HK > 0 && HV > 0 && HV % HK == 0; }
 
 // What the prefill and its backward pass share.  KDA_OK with *empty set: nothing to scan.
@@ -81,19 +99,31 @@ kda_status chunk_args(kda::GdrArgs &a, const void *q, const void *k, const void 
     return KDA_OK;
 }
 
+// What a workspace's size depends on; false if the shape is not supported.
+bool size_args(kda::GdrArgs &a, kda_dtype in_dtype, int B, int64_t T, int num_seqs, int varlen, int HK, int HV, int K, int V) {
+    a = kda::GdrArgs{};
+    if (B < 0 || T < 0 || num_seqs < 0 || !heads_ok(HK, HV) || !type_ok(in_dtype) || !width_ok(K) || !width_ok(V)) return false;
+    a.HK = HK;
+    a.HV = HV;
+    a.V = V;
+    a.slots = T == 0 ? 0 : chunk_slots(B, T, num_seqs, varlen != 0);
+    return a.slots <= (int64_t)INT32_MAX / HV;
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t kda_gdr_chunk_fwd_workspace_size(kda_dtype in_dtype, int B, int64_t T, int num_seqs, int varlen, int HK, int HV,
                                         int K, int V) {
-    if (B < 0 || T < 0 || num_seqs < 0 || !heads_ok(HK, HV) || !type_ok(in_dtype) || !width_ok(K) || !width_ok(V)) return 0;
-    kda::GdrArgs a = {};
-    a.HK = HK;
-    a.HV = HV;
-    a.slots = chunk_slots(B, T, num_seqs, varlen != 0);
-    if (a.slots > (int64_t)INT32_MAX / HV) return 0;
-    return carve_fwd(a, nullptr, in_dtype == KDA_F32, K);
+    kda::GdrArgs a;
+    return size_args(a, in_dtype, B, T, num_seqs, varlen, HK, HV, K, V) ? carve_fwd(a, nullptr, in_dtype == KDA_F32, K) : 0;
+}
+
+size_t kda_gdr_chunk_bwd_workspace_size(kda_dtype in_dtype, int B, int64_t T, int num_seqs, int varlen, int HK, int HV,
+                                        int K, int V) {
+    kda::GdrArgs a;
+    return size_args(a, in_dtype, B, T, num_seqs, varlen, HK, HV, K, V) ? carve_bwd(a, nullptr, in_dtype == KDA_F32, K) : 0;
 }
 
 kda_status kda_gdr_chunk_fwd(const void *q, const void *k, const void *v, kda_dtype in_dtype, const float *g,
@@ -128,6 +158,49 @@ kda_status kda_gdr_chunk_fwd(const void *q, const void *k, const void *v, kda_dt
     a.out_bf16 = out_dtype == KDA_BF16;
     const hipError_t e = kda::launch_gdr_prep(a, in_dtype == KDA_F32, K, false, stream);
     return done(e != hipSuccess ? e : kda::launch_gdr_fwd_chain(a, in_dtype == KDA_F32, K, false, stream));
+}
+
+kda_status kda_gdr_chunk_bwd(const void *q, const void *k, const void *v, kda_dtype in_dtype, const float *g,
+                             const float *beta, const float *initial_state, const int32_t *cu_seqlens, int num_seqs,
+                             int B, int64_t T, int HK, int HV, int K, int V, float scale, const void *d_out,
+                             kda_dtype dout_dtype, const float *d_final_state, void *dq, void *dk, void *dv,
+                             kda_dtype grad_dtype, float *dg, float *dbeta, float *d_initial_state, void *workspace,
+                             size_t workspace_bytes, hipStream_t stream) {
+    kda::GdrArgs a;
+    bool empty;
+    const kda_status st = chunk_args(a, q, k, v, in_dtype, g, beta, initial_state, cu_seqlens, num_seqs, B, T, HK, HV, K, V, scale, &empty);
+    if (st != KDA_OK) return st;
+    if (!type_ok(dout_dtype) || !type_ok(grad_dtype)) return KDA_ERR_BAD_DTYPE;
+    if (empty) {
+        if (d_initial_state && a.N > 0 && (const float *)d_initial_state != d_final_state)
+            return done(kda::launch_fill_copy(d_initial_state, d_final_state, (int64_t)a.N * HV * K * V, stream));
+        return KDA_OK;
+    }
+    if (!d_out || !dq || !dk || !dv || !dg || !dbeta || !workspace) return KDA_ERR_NULL_POINTER;
+    const void *ins[] = {q, k, v, g, beta, initial_state, cu_seqlens, d_out, d_final_state};
+    const void *outs[] = {dq, dk, dv, dg, dbeta, d_initial_state, workspace};
+    for (int i = 0; i < 7; ++i) {
+        if (!outs[i]) continue;
+        for (const void *p : ins)
+            if (p == outs[i]) return KDA_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (outs[j] == outs[i]) return KDA_ERR_ALIAS;
+    }
+    const void *vec[] = {q, k, v, initial_state, d_out, d_final_state, dq, dk, dv, d_initial_state, workspace};
+    for (const void *p : vec)
+        if (!aligned(p)) return KDA_ERR_BAD_ARGUMENT;
+    if (workspace_bytes < carve_bwd(a, workspace, in_dtype == KDA_F32, K)) return KDA_ERR_BAD_ARGUMENT;
+    a.d_out = d_out;
+    a.dout_bf16 = dout_dtype == KDA_BF16;
+    a.d_sf = d_final_state;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.grad_bf16 = grad_dtype == KDA_BF16;
+    a.dg = dg;
+    a.dbeta = dbeta;
+    a.ds0 = d_initial_state;
+    return done(kda::launch_gdr_bwd(a, in_dtype == KDA_F32, K, stream));
 }
 
 kda_status kda_gdr_recurrent_step(const void *q, const void *k, const void *v, kda_dtype in_dtype, const float *g,

@@ -2,6 +2,8 @@
 
 * ``gdr_chunk_fwd(q, k, v, g, beta, ...)`` -- prefill: g and beta per value head, q and k
   shared by the HV / HK value heads of a group; packed sequences, initial and final states.
+* ``gdr_chunk_bwd(q, k, v, g, beta, d_out, ...)`` -- its gradients; ``gated_delta_rule(q, k, v,
+  g, beta, ...)`` -- the prefill recorded for autograd through them.
 * ``gdr_recurrent_step(q, k, v, g, beta, states, ...)`` -- decode: one or several tokens a
   request over a pool of states, the state after every drafted token in a slot of its own;
   a decay per value head, or per channel as KDA has it.
@@ -15,7 +17,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _check, _dev, _dtype_code, _load, _ptr, _stream
+from . import _check, _dev, _dtype_code, _load, _needs_grad, _ptr, _stream
 
 
 def _input(x: Optional[torch.Tensor], name: str, like: Optional[torch.Tensor] = None, dtype=None) -> Optional[torch.Tensor]:
@@ -102,6 +104,76 @@ def gdr_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
                                        _dtype_code(od), _ptr(workspace), workspace.numel(), _stream(q))
     _check("kda_gdr_chunk_fwd", st)
     return out, final_state
+
+
+def gdr_chunk_bwd_workspace_size(dtype: torch.dtype, B: int, T: int, HK: int, HV: int, K: int, V: int, num_seqs: int = 0,
+                                 varlen: bool = False) -> int:
+    """Bytes of device workspace ``gdr_chunk_bwd`` needs for this shape (0: unsupported or empty)."""
+    return int(_load().kda_gdr_chunk_bwd_workspace_size(_dtype_code(dtype), int(B), int(T), int(num_seqs), 1 if varlen else 0, int(HK),
+                                                        int(HV), int(K), int(V)))
+
+
+def gdr_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, d_out: torch.Tensor,
+                  initial_state: Optional[torch.Tensor] = None, d_final_state: Optional[torch.Tensor] = None,
+                  cu_seqlens: Optional[torch.Tensor] = None, scale: float = 1.0, grad_dtype: Optional[torch.dtype] = None,
+                  want_d_initial_state: bool = True, workspace: Optional[torch.Tensor] = None):
+    """Gradients of ``gdr_chunk_fwd`` (same q, k, v, g, beta, initial_state, cu_seqlens, scale) for
+    L = <d_out, out> + <d_final_state, final_state>.  Returns (dq, dk, dv, dg, dbeta,
+    d_initial_state): dq, dk (summed over the value heads of a group) and dv in ``grad_dtype``
+    (default: the dtype of q), dg and dbeta [B,T,HV] float32, d_initial_state [N,HV,K,V] float32
+    or None.  Rows behind the last packed sequence get zeros.  ``workspace``: a uint8 CUDA tensor
+    of at least ``gdr_chunk_bwd_workspace_size`` bytes, allocated here if not given."""
+    q, k, v, g, beta, initial_state, cu_seqlens, (B, T, HK, HV, K, V, N) = _chunk_inputs(q, k, v, g, beta, initial_state, cu_seqlens)
+    d_out, d_final_state = _input(d_out, "d_out", q), _input(d_final_state, "d_final_state", q, torch.float32)
+    if d_out is None or d_out.shape != v.shape:
+        raise ValueError("d_out must be shaped like v")
+    if d_final_state is not None and d_final_state.shape != (N, HV, K, V):
+        raise ValueError("d_final_state must be %s" % [N, HV, K, V])
+    gd, dev = grad_dtype or q.dtype, q.device
+    new = torch.empty if cu_seqlens is None else torch.zeros
+    dq, dk, dv = (new(x.shape, dtype=gd, device=dev) for x in (q, k, v))
+    dg, dbeta = (new(g.shape, dtype=torch.float32, device=dev) for _ in range(2))
+    ds0 = torch.empty((N, HV, K, V), dtype=torch.float32, device=dev) if want_d_initial_state else None
+    workspace = _workspace(workspace, gdr_chunk_bwd_workspace_size(q.dtype, B, T, HK, HV, K, V, N, cu_seqlens is not None), dev)
+    with torch.cuda.device(dev):
+        st = _load().kda_gdr_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q.dtype), _ptr(g), _ptr(beta), _ptr(initial_state),
+                                       _ptr(cu_seqlens), N, B, T, HK, HV, K, V, float(scale), _ptr(d_out), _dtype_code(d_out.dtype),
+                                       _ptr(d_final_state), _ptr(dq), _ptr(dk), _ptr(dv), _dtype_code(gd), _ptr(dg), _ptr(dbeta),
+                                       _ptr(ds0), _ptr(workspace), workspace.numel(), _stream(q))
+    _check("kda_gdr_chunk_bwd", st)
+    return dq, dk, dv, dg, dbeta, ds0
+
+
+class _GatedDeltaRuleFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, initial_state, cu_seqlens, scale):
+        d = lambda x: None if x is None else x.detach()  # noqa: E731
+        with torch.no_grad():
+            out, fin = gdr_chunk_fwd(d(q), d(k), d(v), d(g), d(beta), initial_state=d(initial_state), cu_seqlens=cu_seqlens, scale=scale)
+        ctx.save_for_backward(q, k, v, g, beta, initial_state, cu_seqlens)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return out, fin
+
+    @staticmethod
+    def backward(ctx, d_out, d_fin):
+        q, k, v, g, beta, s0, cu = ctx.saved_tensors
+        if d_out is None:
+            d_out = torch.zeros(v.shape, dtype=v.dtype, device=v.device)
+        d = lambda x: None if x is None else x.detach()  # noqa: E731
+        with torch.no_grad():
+            dq, dk, dv, dg, db, ds0 = gdr_chunk_bwd(d(q), d(k), d(v), d(g), d(beta), d_out, initial_state=d(s0), d_final_state=d_fin,
+                                                    cu_seqlens=cu, scale=ctx.scale, want_d_initial_state=ctx.needs_input_grad[5])
+        return dq, dk, dv, dg, db, ds0, None, None
+
+
+def gated_delta_rule(q, k, v, g, beta, initial_state=None, cu_seqlens=None, scale: float = 1.0):
+    """``gdr_chunk_fwd`` as a function of its inputs: (out in the inputs' dtype, final_state), recorded
+    for autograd when any of q, k, v, g, beta or initial_state requires grad (through
+    ``gdr_chunk_bwd``)."""
+    if _needs_grad(q, k, v, g, beta, initial_state):
+        return _GatedDeltaRuleFn.apply(q, k, v, g, beta, initial_state, cu_seqlens, float(scale))
+    return gdr_chunk_fwd(q, k, v, g, beta, initial_state=initial_state, cu_seqlens=cu_seqlens, scale=scale)
 
 
 def gdr_recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, states: torch.Tensor,

@@ -375,6 +375,30 @@ kda_status kda_gdr_chunk_fwd(const void *q, const void *k, const void *v, kda_dt
                              hipStream_t stream);
 
 /*
+ * kda_gdr_chunk_bwd -- gradients of kda_gdr_chunk_fwd for L = <d_out, out> + <d_final_state,
+ * final_state>, written for the inputs exactly as given to the forward:
+ *   dq, dk [B, T, HK, K] (summed over the value heads of a group, in a fixed order) and
+ *   dv     [B, T, HV, V] in grad_dtype;  dg, dbeta [B, T, HV] float32
+ *   d_initial_state [N, HV, K, V] float32, or NULL (not wanted); with initial_state NULL it is
+ *          the gradient at the zero state
+ * from d_out [B, T, HV, V] in dout_dtype and d_final_state [N, HV, K, V] float32 or NULL (zeros).
+ * Rows behind the last packed sequence are left as they were.  The forward is computed again,
+ * chunk by chunk; its intermediates live in the workspace (about 0.27 MB per chunk and value
+ * head at K = V = 128), scratch as in the forward.  Float32 precision throughout (computed
+ * operands enter the matrix cores with 24 mantissa bits).  A token with g = -inf gets dg = 0.
+ * No output may overlap an input or another output.  T == 0 (or B == 0): no token gradients,
+ * d_initial_state = d_final_state (or zeros).
+ */
+size_t kda_gdr_chunk_bwd_workspace_size(kda_dtype in_dtype, int B, int64_t T, int num_seqs, int varlen, int HK,
+                                        int HV, int K, int V);
+kda_status kda_gdr_chunk_bwd(const void *q, const void *k, const void *v, kda_dtype in_dtype, const float *g,
+                             const float *beta, const float *initial_state, const int32_t *cu_seqlens, int num_seqs,
+                             int B, int64_t T, int HK, int HV, int K, int V, float scale, const void *d_out,
+                             kda_dtype dout_dtype, const float *d_final_state, void *dq, void *dk, void *dv,
+                             kda_dtype grad_dtype, float *dg, float *dbeta, float *d_initial_state, void *workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
+/*
  * kda_gdr_recurrent_step -- decode: up to S tokens for each of B requests over a pool of kept
  * states, token by token in float32, so that drafted tokens can be checked (kda_draft_verify)
  * and the state after any of them taken up again.

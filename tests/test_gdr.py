@@ -46,6 +46,29 @@ def test_chunk_fwd_workspace(lib):
     assert _fwd(lib, wsz=need - 1) == 5
 
 
+def _bwd(lib, q=0x1000, k=0x2000, v=0x3000, dt=1, g=0x4000, beta=0x5000, s0=None, cu=None, N=0, B=1, T=64, HK=2, HV=4, K=16, V=16, do=0x6000,
+         dd=1, dsf=None, dq=0x7000, dk=0x8000, dv=0x9000, gd=1, dg=0xa000, db=0xb000, ds0=None, ws=0xc000, wsz=1 << 30):
+    return lib.kda_gdr_chunk_bwd(q, k, v, dt, g, beta, s0, cu, N, B, T, HK, HV, K, V, 1.0, do, dd, dsf, dq, dk, dv, gd, dg, db, ds0, ws, wsz,
+                                 None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(K=8), 4), (dict(HV=5), 2), (dict(dt=4), 3), (dict(dd=4), 3), (dict(gd=4), 3), (dict(do=None), 1), (dict(dg=None), 1), (dict(ws=None), 1),
+    (dict(cu=0x900, B=2), 5), (dict(dq=0x2000), 6), (dict(dg=0x7000), 6), (dict(ds0=0x6000), 6), (dict(ws=0x6000), 6), (dict(do=0x6008), 5),
+    (dict(wsz=4096), 5), (dict(T=0, q=None, ws=None), 0),
+])
+def test_chunk_bwd_refusals(lib, kw, status):
+    assert _bwd(lib, **kw) == status
+
+
+def test_chunk_bwd_workspace(lib):
+    size = lambda **kw: kda.gdr_chunk_bwd_workspace_size(**{**dict(dtype=torch.bfloat16, B=1, T=64, HK=2, HV=4, K=16, V=32), **kw})  # noqa: E731
+    # three bf16 parts of M, M^T and P^T; decays (float) and their sums (double); two states and two sets of rows; K^T, Q^T
+    assert size() == 4 * (3 * 3 * 64 * 64 * 2 + 4 * 64 * 4 + 64 * 8 + 2 * 16 * 32 * 4 + 2 * 64 * 32 * 4) + 2 * 2 * 16 * 64 * 2
+    assert size(T=130, num_seqs=4, varlen=True) == 6 * size() and size(K=24) == 0 and size(T=0, num_seqs=3, varlen=True) == 0
+    assert _bwd(lib, V=32, wsz=size() - 1) == 5
+
+
 def _step(lib, q=0x1000, k=0x2000, v=0x3000, dt=1, g=0x4000, ch=0, beta=0x5000, st=0x6000, pool=8, slots=0x900, cols=3, start=None, lens=None,
           B=2, S=3, HK=2, HV=4, K=16, V=16, out=0x7000, od=1):
     return lib.kda_gdr_recurrent_step(q, k, v, dt, g, ch, beta, st, pool, slots, cols, start, lens, B, S, HK, HV, K, V, 1.0, out, od, None)

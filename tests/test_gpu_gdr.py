@@ -177,6 +177,158 @@ def test_fwd_graph_and_other_stream():
         assert torch.equal(out, want) and torch.equal(fin, wfin)
 
 
+# ------------------------------------------------------------------------------ gradients
+
+NAMES = ("dq", "dk", "dv", "dg", "dbeta", "ds0")
+
+
+def _cotangents(i, seed, dtype=torch.float32, final=True):
+    gen = torch.Generator().manual_seed(seed)
+    K, (HV, V) = i["q"].shape[3], i["v"].shape[2:]
+    return torch.randn(*i["v"].shape, generator=gen).to(dtype), 0.5 * torch.randn(i["N"], HV, K, V, generator=gen) if final else None
+
+
+def _bwd_check(i, seed, scale=1.0, dout_dtype=torch.float32, final=True, what="", **kw):
+    """Three bf16 parts: 24 bits, as with float32 inputs above.  A gradient's chunk passes two more sums of 64 + 128
+    terms than an output's, and dg sums a chunk's 64 rows and its pairs in float32: 5e-5 of the larger of a
+    gradient's rms and the element (a tenth of that in the 2-norm)."""
+    d_out, d_fin = _cotangents(i, seed, dout_dtype, final)
+    d = _gpu(i)
+    got = kda.gdr_chunk_bwd(d["q"], d["k"], d["v"], d["g"], d["beta"], d_out.cuda(), initial_state=d["s0"],
+                            d_final_state=None if d_fin is None else d_fin.cuda(), cu_seqlens=d["cu"], scale=scale, grad_dtype=torch.float32, **kw)
+    want = ref.scan_bwd(i, d_out, d_fin, scale)
+    for name, x, y in zip(NAMES, got, want):
+        if x is None:
+            continue
+        assert np.all(np.isfinite(f64(x))), "%s %s is not finite" % (what, name)
+        e, n = err_fp32(x, y), _norm(x, y)
+        assert e <= 5e-5 and (n <= 5e-6 or np.linalg.norm(y) < 1e-12), "%s %s: %.2e, %.2e in norm" % (what, name, e, n)
+    return got
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("K,V", [(16, 16), (32, 128), (64, 32), (128, 64), (128, 128), (16, 128)])
+def test_bwd_widths(dtype, K, V):
+    _bwd_check(ref.make(2, 150, 2, 6, K, V, dtype, seed=K + V), K, 0.7, dtype)
+
+
+@pytest.mark.parametrize("T", [1, 2, 16, 17, 63, 64, 65, 129, 200])
+def test_bwd_lengths(T):
+    _bwd_check(ref.make(1, T, 1, 2, 32, 32, torch.bfloat16, seed=T, state=T % 2 == 0), T, final=T % 3 != 0)
+
+
+@pytest.mark.parametrize("lens", [[70, 0, 1, 64, 130], [0, 0, 3], [1, 1, 1, 1], [65, 63, 0]])
+def test_bwd_packed(lens):
+    _bwd_check(ref.make(1, sum(lens), 2, 4, 32, 16, torch.float32, seed=sum(lens), seqlens=lens), 7, 0.5)
+
+
+@pytest.mark.parametrize("what", ["no decay", "forgets within", "fast decay", "repeated key", "no writes"])
+def test_bwd_regimes(what):
+    i = ref.make(1, 140, 1, 3, 32, 32, torch.float32, seed=11)
+    if what == "no decay":
+        i["g"].zero_()
+    elif what == "forgets within":
+        i["g"][0, [0, 5, 63, 64, 100]] = -1000.0  # the oracle's e^g is 0, and so is dg
+    elif what == "fast decay":
+        i["g"] = i["g"] * 20
+    elif what == "repeated key":
+        i["k"] = i["k"][:, :1].expand_as(i["k"]).contiguous()
+    else:
+        i["beta"].zero_()
+    got = _bwd_check(i, 12, what=what)
+    if what == "forgets within":
+        assert not got[3][0, [0, 5, 63, 64, 100]].any()
+        i["g"][0, [0, 5, 63, 64, 100]] = -np.inf
+        d_out, d_fin = _cotangents(i, 12)
+        d = _gpu(i)
+        again = kda.gdr_chunk_bwd(d["q"], d["k"], d["v"], d["g"], d["beta"], d_out.cuda(), initial_state=d["s0"], d_final_state=d_fin.cuda())
+        assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
+def test_bwd_rows_behind_the_last_sequence_are_zero():
+    i = ref.make(1, 130, 1, 2, 16, 16, torch.float32, seed=3, seqlens=[90, 40])
+    d_out, d_fin = (x.cuda() for x in _cotangents(i, 4))
+    d = _gpu(i)
+    nan = lambda x: torch.cat([x, torch.full_like(x[:, :30], float("nan"))], 1)  # noqa: E731
+    a = kda.gdr_chunk_bwd(*[nan(d[n]) for n in ("q", "k", "v", "g", "beta")], nan(d_out), initial_state=d["s0"], d_final_state=d_fin, cu_seqlens=d["cu"])
+    b = kda.gdr_chunk_bwd(*[d[n] for n in ("q", "k", "v", "g", "beta")], d_out, initial_state=d["s0"], d_final_state=d_fin, cu_seqlens=d["cu"])
+    assert all(torch.equal(x[:, :130], y) and not x[:, 130:].any() for x, y in zip(a[:5], b[:5])) and torch.equal(a[5], b[5])
+
+
+def test_bwd_against_differences():
+    """Central differences of the forward along each gradient, with steps of 0.003 of the input's norm.  The quotient's
+    own error falls with the step's square: for these inputs the 64-bit form's quotient along g is 5.4e-2 off its
+    gradient at a step of 0.01 and 5.3e-4 at 0.001, so 4.9e-3 at 0.003; that and the forward's error give 1e-2."""
+    i = ref.make(1, 70, 1, 2, 16, 16, torch.float32, seed=9)
+    d_out, d_fin = _cotangents(i, 5)
+    d = _gpu(i)
+    got = kda.gdr_chunk_bwd(d["q"], d["k"], d["v"], d["g"], d["beta"], d_out.cuda(), initial_state=d["s0"], d_final_state=d_fin.cuda())
+
+    def loss(x):
+        out, fin = ref.scan(x)  # the 64-bit form, to which the forward is held
+        o, f = _fwd(x)
+        assert err_fp32(o, out) <= 1e-5
+        return float((f64(o) * f64(d_out)).sum() + (f64(f) * f64(d_fin)).sum())
+    for name, grad in zip(("q", "k", "v", "g", "beta", "s0"), got):
+        grad = grad.cpu()
+        step = 0.003 * float(i[name].norm() / grad.norm())
+        plus, minus = ({**i, name: i[name] + s * step * grad} for s in (1, -1))
+        num, want = (loss(plus) - loss(minus)) / (2 * step), float(f64(grad.norm()) ** 2)
+        assert abs(num - want) <= 1e-2 * want, (name, num, want)
+
+
+def test_bwd_deterministic_and_workspace_contents_do_not_matter():
+    i = ref.make(1, 200, 2, 6, 64, 32, torch.bfloat16, seed=23)
+    d_out, d_fin = (x.cuda() for x in _cotangents(i, 24, torch.bfloat16))
+    d = _gpu(i)
+    args = ([d[n] for n in ("q", "k", "v", "g", "beta")] + [d_out], dict(initial_state=d["s0"], d_final_state=d_fin.float()))
+    n = kda.gdr_chunk_bwd_workspace_size(torch.bfloat16, 1, 200, 2, 6, 64, 32)
+    runs = [kda.gdr_chunk_bwd(*args[0], **args[1], workspace=torch.full((n,), f, dtype=torch.uint8, device="cuda")) for f in (0, 255, 127)]
+    assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(*runs))
+    nf = kda.gdr_chunk_fwd_workspace_size(torch.bfloat16, 1, 200, 2, 6, 64, 32)
+    fw = [kda.gdr_chunk_fwd(*args[0][:5], workspace=torch.full((nf,), f, dtype=torch.uint8, device="cuda")) for f in (0, 255)]
+    assert all(torch.equal(x, y) for x, y in zip(*fw))
+
+
+def test_autograd_matches_bwd():
+    i = ref.make(2, 100, 2, 4, 32, 32, torch.bfloat16, seed=25)
+    d = _gpu(i)
+    leaves = [d[n].clone().requires_grad_() for n in ("q", "k", "v", "g", "beta", "s0")]
+    d_out, d_fin = (x.cuda() for x in _cotangents(i, 26, torch.bfloat16))
+    out, fin = kda.gated_delta_rule(*leaves[:5], initial_state=leaves[5], scale=0.5)
+    torch.autograd.backward([out, fin], [d_out, d_fin.float()])
+    want = kda.gdr_chunk_bwd(*[x.detach() for x in leaves[:5]], d_out, initial_state=d["s0"], d_final_state=d_fin.float(), scale=0.5)
+    assert all(torch.equal(x.grad, y) for x, y in zip(leaves, want))
+    only = d["q"].clone().requires_grad_()  # the final state unused, no initial state
+    out, _ = kda.gated_delta_rule(only, d["k"], d["v"], d["g"], d["beta"])
+    out.float().sum().backward()
+    want = kda.gdr_chunk_bwd(d["q"], d["k"], d["v"], d["g"], d["beta"], torch.ones_like(d["v"]))
+    assert torch.equal(only.grad, want[0])
+    with pytest.raises(ValueError):
+        kda.gdr_chunk_fwd(only, d["k"], d["v"], d["g"], d["beta"])
+
+
+def test_bwd_graph():
+    i = ref.make(1, 130, 1, 2, 32, 32, torch.bfloat16, seed=27)
+    d = _gpu(i)
+    d_out, d_fin = (x.cuda() for x in _cotangents(i, 28, torch.bfloat16))
+    args = [d[n] for n in ("q", "k", "v", "g", "beta")] + [d_out]
+    call = lambda: kda.gdr_chunk_bwd(*args, initial_state=d["s0"], d_final_state=d_fin.float())  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for seed in (29, 30, 31):
+        n = _gpu(ref.make(1, 130, 1, 2, 32, 32, torch.bfloat16, seed=seed))
+        for x, name in zip(args, ("q", "k", "v", "g", "beta")):
+            x.copy_(n[name])
+        graph.replay()
+        want = call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 # ------------------------------------------------------------------------------ decode
 
 def _step_case(B, S, HK, HV, K, V, dtype, seed, channels=False, pool=None):
