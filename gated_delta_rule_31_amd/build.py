@@ -20,7 +20,8 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
 # per-source extra flags: the DMA-fed chain kernel keeps its matrix-core accumulators in
 # ordinary vector registers (the float32 state is rescaled by vector instructions every
 # chunk; accumulation registers would need a move each way)
-EXTRA = {"kda_chunk_chain.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+EXTRA = {"kda_chunk_chain.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "kda_gdr_fwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def build(verbose: bool = False) -> str:

@@ -28,6 +28,7 @@
 namespace kda {
 
 constexpr int GDR_C = 64;  // tokens per chunk
+constexpr int GDR_STATE_PARTS = 3;
 
 // Workspace of one call; the matrices are stored in the order in which a wave loads its
 // matrix-core fragments: [.., 16-row tile][32-column step][part][lane][8].
@@ -69,39 +70,54 @@ struct Parts {
     bf16x8 v[P];
 };
 
+// Two float32 numbers as pairs of bf16 parts, part p of both in one register.
 template <int P>
-__device__ __forceinline__ void cut(float x, __bf16 (&o)[P]) {
+__device__ __forceinline__ void cut2(float x, float y, unsigned (&o)[P]) {
+    typedef __attribute__((ext_vector_type(2))) float f2;
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-        o[p] = (__bf16)x;
-        x -= (float)o[p];
+        o[p] = __builtin_bit_cast(unsigned, __builtin_convertvector((f2{x, y}), bf16x2));
+        if (p + 1 < P) {
+            x -= __builtin_bit_cast(float, o[p] << 16);
+            y -= __builtin_bit_cast(float, o[p] & 0xffff0000u);
+        }
     }
 }
+
+typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
+typedef __attribute__((ext_vector_type(2))) unsigned u32x2;
 
 template <int P>
 __device__ __forceinline__ Parts<P> cut8(const float *x) {
-    Parts<P> r;
+    u32x4 r[P];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        __bf16 o[P];
-        cut<P>(x[i], o);
+    for (int i = 0; i < 4; ++i) {
+        unsigned o[P];
+        cut2<P>(x[2 * i], x[2 * i + 1], o);
 #pragma unroll
-        for (int p = 0; p < P; ++p) r.v[p][i] = o[p];
+        for (int p = 0; p < P; ++p) r[p][i] = o[p];
     }
-    return r;
+    Parts<P> f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) f.v[p] = __builtin_bit_cast(bf16x8, r[p]);
+    return f;
 }
 
-// acc += A B for operands given in parts; the part products below the last part of the
-// finer operand are left out.
-template <int NA, int NB>
-__device__ __forceinline__ void mma(f4 &acc, const Parts<NA> &a, const Parts<NB> &b) {
-    constexpr int L = NA > NB ? NA : NB;
+// acc += A B for operands given in parts: the part products i + j < L, smallest first (by
+// default all that matter beside the finer operand's last part).
+template <int L, int NA, int NB>
+__device__ __forceinline__ void mma_to(f4 &acc, const Parts<NA> &a, const Parts<NB> &b) {
 #pragma unroll
     for (int s = L - 1; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i < NA; ++i)
             if (s - i >= 0 && s - i < NB)
                 acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[s - i], acc, 0, 0, 0);
+}
+template <int NA, int NB>
+__device__ __forceinline__ void mma(f4 &acc, const Parts<NA> &a, const Parts<NB> &b) {
+    mma_to<(NA > NB ? NA : NB)>(acc, a, b);
 }
 
 // Eight consecutive elements of an input as parts; zeros where !there.
@@ -125,9 +141,9 @@ __device__ __forceinline__ Parts<PK> load8(const float *p, bool there) {
 template <int P>
 __device__ __forceinline__ Parts<P> load_frag(const __bf16 *m, int r, int s, int lane) {
     Parts<P> f;
+    const char *from = reinterpret_cast<const char *>(m) + (r * 2 + s) * P * 1024;
 #pragma unroll
-    for (int p = 0; p < P; ++p)
-        f.v[p] = *reinterpret_cast<const bf16x8 *>(m + ((((r * 2 + s) * P + p) * 64) + lane) * 8);
+    for (int p = 0; p < P; ++p) f.v[p] = *reinterpret_cast<const bf16x8 *>(from + (unsigned)(lane * 16) + p * 1024);
     return f;
 }
 template <int P>
@@ -136,29 +152,56 @@ __device__ __forceinline__ void store_frag(__bf16 *m, int r, int s, int lane, co
     for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x8 *>(m + ((((r * 2 + s) * P + p) * 64) + lane) * 8) = f.v[p];
 }
 
-// A fragment out of LDS: part p of row `row` at element `col`, rows of `ld` elements, parts
-// `ps` elements apart.
-template <int P>
-__device__ __forceinline__ Parts<P> lds_frag(const __bf16 *m, int ps, int ld, int row, int col) {
+// Operands in LDS: parts of an R x N matrix (N a multiple of 32), rows of N elements without
+// padding.  A row's 16-byte pieces are placed by piece XOR row (for rows shorter than the 64
+// banks, XOR of the row's place among those that share a line of banks), so that the sixteen
+// rows of a fragment, and the rows that a store writes, fall on different banks.
+template <int N>
+__device__ __forceinline__ int lds_at(int row, int col) {
+    constexpr int PIECES = N / 8, SHARE = 16 / PIECES;  // pieces of a row; rows on one line of banks
+    static_assert(N == 32 || N == 64 || N == 128, "rows of at most one line");
+    const int turn = N == 32 ? (PIECES - row / SHARE % PIECES) % PIECES : row / SHARE % PIECES;
+    return row * N + ((col / 8) ^ turn) * 8 + col % 8;
+}
+template <int P, int R, int N>
+__device__ __forceinline__ Parts<P> lds_frag(const __bf16 *m, int row, int col) {
     Parts<P> f;
 #pragma unroll
-    for (int p = 0; p < P; ++p) f.v[p] = *reinterpret_cast<const bf16x8 *>(m + p * ps + row * ld + col);
+    for (int p = 0; p < P; ++p) f.v[p] = *reinterpret_cast<const bf16x8 *>(m + p * R * N + lds_at<N>(row, col));
     return f;
 }
-// Four consecutive float32 numbers into LDS as parts.
-template <int P>
-__device__ __forceinline__ void lds_put4(__bf16 *m, int ps, int ld, int row, int col, const f4 &x) {
-    typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
-    bf16x4 r[P];
+// Four consecutive float32 numbers of a row into LDS as parts.
+template <int P, int R, int N>
+__device__ __forceinline__ void lds_put4(__bf16 *m, int row, int col, const f4 &x) {
+    unsigned a[P], b[P];
+    cut2<P>(x[0], x[1], a);
+    cut2<P>(x[2], x[3], b);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        __bf16 o[P];
-        cut<P>(x[i], o);
+    for (int p = 0; p < P; ++p) *reinterpret_cast<u32x2 *>(m + p * R * N + lds_at<N>(row, col)) = u32x2{a[p], b[p]};
+}
+
+// The transpose of a fragment: eight rows (from row) of column col + lane % 16, out of R x N
+// matrices in the same layout.  The instruction turns 4 x 16 tiles: in each sixteen lanes, lane
+// 4 i + j gives the address of row i's columns 4 j .. + 3 and receives the rows of its column.
+template <int P, int R, int N>
+__device__ __forceinline__ Parts<P> lds_frag_turned(const __bf16 *m, int row, int col, int lane) {
+    typedef __attribute__((ext_vector_type(4))) short s4;
+    typedef __attribute__((address_space(3))) s4 *lds4;
+    const int r = row + lane % 16 / 4, c = col + lane % 4 * 4;
+    Parts<P> f;
 #pragma unroll
-        for (int p = 0; p < P; ++p) r[p][i] = o[p];
+    for (int p = 0; p < P; ++p) {
+        const s4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(m + p * R * N + lds_at<N>(r, c)));
+        const s4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(m + p * R * N + lds_at<N>(r + 4, c)));
+        f.v[p] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     }
-#pragma unroll
-    for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x4 *>(m + p * ps + row * ld + col) = r[p];
+    return f;
+}
+
+// A load or store at a 32-bit byte offset from an address that the whole wave shares.
+template <typename V>
+__device__ __forceinline__ V at_offset(const void *base, unsigned bytes) {
+    return *reinterpret_cast<const V *>(static_cast<const char *>(base) + bytes);
 }
 
 // Workgroup barrier for LDS traffic only: the waves exchange data through LDS alone, so
@@ -205,12 +248,39 @@ __device__ __forceinline__ bool gdr_chunk(const GdrArgs &a, int64_t slot, int64_
     return true;
 }
 
-// Block index to unit: consecutive blocks go to the eight XCDs in turn, so units of one
-// eighth of the range run on one XCD and share its L2.
-__device__ __forceinline__ int gdr_xcd_unit(int b, int total) {
-    const int per = total / 8, left = total % 8, x = b % 8, i = b / 8;
-    return x * per + (x < left ? x : left) + i;
+// The chains' grids: block b of 8 VB ceil(N HV / 8) takes value block b / 8 % VB of pair
+// (b / 8 / VB) 8 + b % 8.  Blocks go to the eight XCDs in turn, so a pair's value blocks, which
+// read the same keys, share one XCD's L2, and a long sequence's heads spread over all of them.
+// Packed sequences (up to 64) are taken longest first, so that none is left to run alone.
+// False for a block without a pair.
+__device__ __forceinline__ bool gdr_pair(const GdrArgs &a, int VB, int &vb, int &hv, int &n) {
+    const int i = blockIdx.x / 8;
+    const int64_t pair = (int64_t)(i / VB) * 8 + blockIdx.x % 8;
+    vb = i % VB;
+    hv = (int)(pair % a.HV);
+    n = (int)(pair / a.HV);
+    if (pair >= (int64_t)a.N * a.HV) return false;
+    if (a.cu && a.N > 1 && a.N <= 64) {
+        const int lane = threadIdx.x & 63;
+        int64_t row, len = -1, slot;
+        if (lane < a.N) gdr_sequence(a, lane, row, len, slot);
+        int rank = 0;
+        for (int m = 0; m < a.N; ++m) {
+            const int other = __builtin_amdgcn_readlane((int)len, m);
+            rank += other > (int)len || (other == (int)len && m < lane);
+        }
+        n = __builtin_ctzll(__ballot(lane < a.N && rank == n));
+    }
+    return true;
 }
+// Tiles of 16 value columns that one workgroup of a chain takes: one while that gives a compute
+// unit no more than one workgroup (8192 tokens x 32 heads of 128 columns: 291 us, two tiles 361),
+// two from two workgroups a unit on, as a chunk's operands are then loaded half as often (64
+// heads: 412 us, one tile 498; 96 heads 634, 767).
+inline int gdr_column_tiles(const GdrArgs &a) {
+    return a.V >= 32 && (int64_t)a.N * a.HV * (a.V / 16) >= 2 * device_cu_count() ? 2 : 1;
+}
+inline int64_t gdr_pair_blocks(const GdrArgs &a, int VB) { return ((int64_t)a.N * a.HV + 7) / 8 * 8 * VB; }
 
 // the products that do not depend on the state, for every (chunk slot, value head)
 hipError_t launch_gdr_prep(const GdrArgs &a, bool fp32, int K, bool bwd, hipStream_t stream);

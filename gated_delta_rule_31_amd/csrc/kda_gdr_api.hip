@@ -33,13 +33,12 @@ struct Carver {
     }
 };
 
-size_t carve_fwd(kda::GdrArgs &a, void *base, bool fp32, int K) {
-    const int C = kda::GDR_C, parts = fp32 ? 3 : 2, input_parts = fp32 ? 3 : 1;
+size_t carve_fwd(kda::GdrArgs &a, void *base, bool fp32) {
+    const int C = kda::GDR_C, parts = fp32 ? 3 : kda::GDR_STATE_PARTS, out_parts = fp32 ? 3 : 2;
     const int64_t units = a.slots * a.HV;
     Carver w{static_cast<char *>(base)};
     w.take(a.M, units * parts * C * C);
-    w.take(a.P, units * parts * C * C);
-    w.take(a.Kt, a.slots * a.HK * input_parts * K * C);
+    w.take(a.P, units * out_parts * C * C);
     w.take(a.dec, units * 4 * C);
     return w.used;
 }
@@ -93,8 +92,10 @@ kda_status chunk_args(kda::GdrArgs &a, const void *q, const void *k, const void 
     if (*empty) return KDA_OK;
     a.slots = chunk_slots(B, T, num_seqs, cu != nullptr);
     a.chunks = (int)((T + kda::GDR_C - 1) / kda::GDR_C);
+    // a chunk's rows are addressed by 32-bit offsets
+    if (HK > 65535 || HV > 65535) return KDA_ERR_UNSUPPORTED;
     // (chunk slot, value head) and (sequence, value head, column block) index grids as int
-    if (a.slots > (int64_t)INT32_MAX / HV || N > (int64_t)INT32_MAX / HV / (V / 16)) return KDA_ERR_UNSUPPORTED;
+    if (a.slots > (int64_t)INT32_MAX / HV / 2 || N > (int64_t)INT32_MAX / HV / (V / 16) - 8) return KDA_ERR_UNSUPPORTED;
     if (!q || !k || !v || !g || !beta) return KDA_ERR_NULL_POINTER;
     return KDA_OK;
 }
@@ -107,7 +108,7 @@ bool size_args(kda::GdrArgs &a, kda_dtype in_dtype, int B, int64_t T, int num_se
     a.HV = HV;
     a.V = V;
     a.slots = T == 0 ? 0 : chunk_slots(B, T, num_seqs, varlen != 0);
-    return a.slots <= (int64_t)INT32_MAX / HV;
+    return a.slots <= (int64_t)INT32_MAX / HV / 2;
 }
 
 }  // namespace
@@ -117,7 +118,7 @@ extern "C" {
 size_t kda_gdr_chunk_fwd_workspace_size(kda_dtype in_dtype, int B, int64_t T, int num_seqs, int varlen, int HK, int HV,
                                         int K, int V) {
     kda::GdrArgs a;
-    return size_args(a, in_dtype, B, T, num_seqs, varlen, HK, HV, K, V) ? carve_fwd(a, nullptr, in_dtype == KDA_F32, K) : 0;
+    return size_args(a, in_dtype, B, T, num_seqs, varlen, HK, HV, K, V) ? carve_fwd(a, nullptr, in_dtype == KDA_F32) : 0;
 }
 
 size_t kda_gdr_chunk_bwd_workspace_size(kda_dtype in_dtype, int B, int64_t T, int num_seqs, int varlen, int HK, int HV,
@@ -152,7 +153,7 @@ kda_status kda_gdr_chunk_fwd(const void *q, const void *k, const void *v, kda_dt
     const void *vec[] = {q, k, v, initial_state, final_state, out, workspace};
     for (const void *p : vec)
         if (!aligned(p)) return KDA_ERR_BAD_ARGUMENT;
-    if (workspace_bytes < carve_fwd(a, workspace, in_dtype == KDA_F32, K)) return KDA_ERR_BAD_ARGUMENT;
+    if (workspace_bytes < carve_fwd(a, workspace, in_dtype == KDA_F32)) return KDA_ERR_BAD_ARGUMENT;
     a.sf = final_state;
     a.out = out;
     a.out_bf16 = out_dtype == KDA_BF16;

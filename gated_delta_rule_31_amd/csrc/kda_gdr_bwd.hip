@@ -31,17 +31,18 @@ __device__ __forceinline__ float ld_any(const void *p, int bf16, int64_t i) {
 // The chain of gradients: workgroups and waves as in the forward chain.
 template <typename T, int K>
 __global__ __launch_bounds__(256) void gdr_bwd_chain_kernel(const GdrArgs a) {
-    constexpr int PK = gdr_input_parts<T>(), KP = K < 32 ? 32 : K, KS = KP / 32, NC = (K / 16 + 3) / 4, LS = KP + 8, LT = C + 8;
-    __shared__ __attribute__((aligned(16))) __bf16 sS[P * 16 * LS], sO[P * 16 * LT], sX[P * 16 * LT], sB[P * 16 * LT], sE[P * 16 * LT];
-    const int VB = a.V / 16, unit = gdr_xcd_unit(blockIdx.x, gridDim.x);
-    const int vb = unit % VB, hv = unit / VB % a.HV, n = unit / VB / a.HV, hk = hv / a.group;
+    constexpr int PK = gdr_input_parts<T>(), KP = K < 32 ? 32 : K, KS = KP / 32, NC = (K / 16 + 3) / 4;
+    __shared__ __attribute__((aligned(16))) __bf16 sS[P * 16 * KP], sO[P * 16 * C], sX[P * 16 * C], sB[P * 16 * C], sE[P * 16 * C];
+    int vb, hv, n;
+    if (!gdr_pair(a, a.V / 16, vb, hv, n)) return;
+    const int hk = hv / a.group;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15, lg = lane >> 4;
     const int col = 16 * vb + lr;
     int64_t row, len, slot;
     gdr_sequence(a, n, row, len, slot);
     const int64_t state = ((int64_t)n * a.HV + hv) * K * a.V;
     if (K < 32) {
-        for (int i = threadIdx.x; i < P * 16 * LS; i += 256) sS[i] = (__bf16)0.f;
+        for (int i = threadIdx.x; i < P * 16 * KP; i += 256) sS[i] = (__bf16)0.f;
         __syncthreads();
     }
     f4 S[NC];
@@ -53,7 +54,7 @@ __global__ __launch_bounds__(256) void gdr_bwd_chain_kernel(const GdrArgs a) {
             if (a.d_sf)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) S[c][e] = a.d_sf[state + (int64_t)(ch + e) * a.V + col];
-            lds_put4<P>(sS, 16 * LS, LS, lr, ch, S[c]);
+            lds_put4<P, 16, KP>(sS, lr, ch, S[c]);
         }
     }
     const int64_t chunks = (len + C - 1) / C;
@@ -101,23 +102,23 @@ __global__ __launch_bounds__(256) void gdr_bwd_chain_kernel(const GdrArgs a) {
             if (w + 4 * c < K / 16)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) dh[(int64_t)(16 * (w + 4 * c) + 4 * lg + e) * a.V + col] = S[c][e];
-        lds_put4<P>(sO, 16 * LT, LT, lr, 16 * w + 4 * lg, dO);
+        lds_put4<P, 16, C>(sO, lr, 16 * w + 4 * lg, dO);
         gdr_lds_barrier();
         f4 x = {}, y = {};
 #pragma unroll
-        for (int s = 0; s < KS; ++s) mma(x, k[s], lds_frag<P>(sS, 16 * LS, LS, lr, 32 * s + 8 * lg));
+        for (int s = 0; s < KS; ++s) mma(x, k[s], lds_frag<P, 16, KP>(sS, lr, 32 * s + 8 * lg));
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (s >= w / 2) mma(y, p[s], lds_frag<P>(sO, 16 * LT, LT, lr, 32 * s + 8 * lg));
+            if (s >= w / 2) mma(y, p[s], lds_frag<P, 16, C>(sO, lr, 32 * s + 8 * lg));
         x = end * x + y;
-        lds_put4<P>(sX, 16 * LT, LT, lr, 16 * w + 4 * lg, beta * x);
-        lds_put4<P>(sB, 16 * LT, LT, lr, 16 * w + 4 * lg, b * dO);
+        lds_put4<P, 16, C>(sX, lr, 16 * w + 4 * lg, beta * x);
+        lds_put4<P, 16, C>(sB, lr, 16 * w + 4 * lg, b * dO);
         gdr_lds_barrier();
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (s >= w / 2) mma(x, m[s], lds_frag<P>(sX, 16 * LT, LT, lr, 32 * s + 8 * lg));
+            if (s >= w / 2) mma(x, m[s], lds_frag<P, 16, C>(sX, lr, 32 * s + 8 * lg));
         const f4 E = beta * x;
-        lds_put4<P>(sE, 16 * LT, LT, lr, 16 * w + 4 * lg, -(b * E));
+        lds_put4<P, 16, C>(sE, lr, 16 * w + 4 * lg, -(b * E));
         gdr_lds_barrier();
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -125,10 +126,10 @@ __global__ __launch_bounds__(256) void gdr_bwd_chain_kernel(const GdrArgs a) {
                 S[c] *= last;
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    mma(S[c], qt[c][s], lds_frag<P>(sB, 16 * LT, LT, lr, 32 * s + 8 * lg));
-                    mma(S[c], kt[c][s], lds_frag<P>(sE, 16 * LT, LT, lr, 32 * s + 8 * lg));
+                    mma(S[c], qt[c][s], lds_frag<P, 16, C>(sB, lr, 32 * s + 8 * lg));
+                    mma(S[c], kt[c][s], lds_frag<P, 16, C>(sE, lr, 32 * s + 8 * lg));
                 }
-                lds_put4<P>(sS, 16 * LS, LS, lr, 16 * (w + 4 * c) + 4 * lg, S[c]);
+                lds_put4<P, 16, KP>(sS, lr, 16 * (w + 4 * c) + 4 * lg, S[c]);
             }
         float *dY = a.dY + at * ((int64_t)C * a.V);
 #pragma unroll
@@ -164,11 +165,11 @@ __device__ __forceinline__ void row8(float (&x)[8], const float *p, bool there) 
 // The products over V go through LDS in slices of 32 columns.
 template <typename T, int K>
 __global__ __launch_bounds__(256, 1) void gdr_grads_kernel(const GdrArgs a) {
-    constexpr int PK = gdr_input_parts<T>(), KS = K < 32 ? 1 : K / 32, CT = K / 16, LV = 40, LA = C + 4, LH = C + 1;
-    __shared__ __attribute__((aligned(16))) __bf16 sS[P * K * LV], sH[P * K * LV], sV[P * C * LV];
+    constexpr int PK = gdr_input_parts<T>(), KS = K < 32 ? 1 : K / 32, CT = K / 16, LA = C + 4, LH = C + 1;
+    __shared__ __attribute__((aligned(16))) __bf16 sS[P * K * 32], sH[P * K * 32], sV[P * C * 32];
     __shared__ __attribute__((aligned(16))) float sP[C * LA], sA[C * LA], sT[C * LH], sReads[C], sEnds[C], sKeep[4];
     __shared__ double sG[C];
-    const int unit = gdr_xcd_unit(blockIdx.x, gridDim.x), hk = unit % a.HK;
+    const int unit = blockIdx.x, hk = unit % a.HK;
     const int64_t slot = unit / a.HK;
     int64_t row;
     int len;
@@ -217,7 +218,7 @@ __global__ __launch_bounds__(256, 1) void gdr_grads_kernel(const GdrArgs a) {
             const Parts<P> fo = cut8<P>(xo), fv = cut8<P>(xv), fe = cut8<P>(xe);
             __syncthreads();  // the last slice has been read
 #pragma unroll
-            for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x8 *>(sV + (p * C + r) * LV + 8 * lg) = fv.v[p];
+            for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x8 *>(sV + p * C * 32 + lds_at<32>(r, 8 * lg)) = fv.v[p];
             for (int i = tid; i < K * 4; i += 256) {
                 const int ch = i / 4, c = i % 4 * 8;
                 float x[8], y[8];
@@ -228,14 +229,14 @@ __global__ __launch_bounds__(256, 1) void gdr_grads_kernel(const GdrArgs a) {
                 const Parts<P> fx = cut8<P>(x), fy = cut8<P>(y);
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
-                    *reinterpret_cast<bf16x8 *>(sS + (p * K + ch) * LV + c) = fx.v[p];
-                    *reinterpret_cast<bf16x8 *>(sH + (p * K + ch) * LV + c) = fy.v[p];
+                    *reinterpret_cast<bf16x8 *>(sS + p * K * 32 + lds_at<32>(ch, c)) = fx.v[p];
+                    *reinterpret_cast<bf16x8 *>(sH + p * K * 32 + lds_at<32>(ch, c)) = fy.v[p];
                 }
             }
             __syncthreads();
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
-                const Parts<P> s = lds_frag<P>(sS, K * LV, LV, 16 * c + lr, 8 * lg), d = lds_frag<P>(sH, K * LV, LV, 16 * c + lr, 8 * lg);
+                const Parts<P> s = lds_frag<P, K, 32>(sS, 16 * c + lr, 8 * lg), d = lds_frag<P, K, 32>(sH, 16 * c + lr, 8 * lg);
                 mma(r1[c], fo, s);
                 mma(r2[c], fe, s);
                 mma(r3[c], fv, d);
@@ -243,7 +244,7 @@ __global__ __launch_bounds__(256, 1) void gdr_grads_kernel(const GdrArgs a) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
                 if (c <= w) {
-                    const Parts<P> f = lds_frag<P>(sV, C * LV, LV, 16 * c + lr, 8 * lg);
+                    const Parts<P> f = lds_frag<P, C, 32>(sV, 16 * c + lr, 8 * lg);
                     mma(dP[c], fo, f);
                     mma(dA[c], fe, f);
                 }
@@ -377,7 +378,7 @@ __global__ __launch_bounds__(256, 1) void gdr_grads_kernel(const GdrArgs a) {
 
 template <typename T, int K>
 hipError_t launch(const GdrArgs &a, hipStream_t stream) {
-    hipLaunchKernelGGL((gdr_bwd_chain_kernel<T, K>), dim3((unsigned)((int64_t)a.N * a.HV * (a.V / 16))), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((gdr_bwd_chain_kernel<T, K>), dim3((unsigned)gdr_pair_blocks(a, a.V / 16)), dim3(256), 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((gdr_grads_kernel<T, K>), dim3((unsigned)(a.slots * a.HK)), dim3(256), 0, stream, a);

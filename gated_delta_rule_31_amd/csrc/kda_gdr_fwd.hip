@@ -9,7 +9,6 @@ namespace kda {
 namespace {
 
 constexpr int C = GDR_C;
-constexpr int LA = C + 4;  // row stride of the C x C float32 matrices in LDS
 
 // Eight elements down a column of an LDS tile, as parts.
 template <int P, typename T>
@@ -20,287 +19,401 @@ __device__ __forceinline__ Parts<P> column8(const T *m, int ld, int row, int col
     return cut8<P>(x);
 }
 
-// One workgroup of four waves per (chunk slot, value head); wave w owns token rows 16w..16w+15.
-template <typename T, int K, int P, bool BWD>
+// The lower 16 x 16 blocks of a C x C float32 matrix in LDS, rows of 20.
+constexpr int BLOCKS = 10, LB = 20;
+__device__ __forceinline__ int block_at(int p, int r) { return (p * (p + 1) / 2 + r) * 16 * LB; }
+
+// One workgroup of four waves per (chunk slot, value head), and in the backward pass one per
+// (chunk slot, key head) that writes K^T and Q^T.  Wave w owns token rows 16w..16w+15 until A
+// is there, then the column blocks w of M.  33 KB of LDS, so that four workgroups share a
+// compute unit: a workgroup mostly waits (for its rows, for substitution and products that
+// follow one another), and what it writes, 30 KB, is more than it reads.
+template <typename T, int K, int P, int PO, bool BWD>
 __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
     constexpr int PK = gdr_input_parts<T>(), KP = K < 32 ? 32 : K, LK = KP + 8, KS = KP / 32, VEC = 16 / sizeof(T);
-    __shared__ __attribute__((aligned(16))) T sK[C * LK], sQ[C * LK];
-    __shared__ __attribute__((aligned(16))) float sA[C * LA], sM[C * LA], sD[4 * 16 * 20], sB[C];
-    __shared__ double sG[C];
-    const int unit = blockIdx.x, hv = unit % a.HV, hk = hv / a.group;
-    const int64_t slot = unit / a.HV;
+    constexpr int WORK = 2 * BLOCKS * 16 * LB * 4, BYTES = BWD && C * LK * (int)sizeof(T) > WORK ? C * LK * (int)sizeof(T) : WORK;
+    __shared__ __attribute__((aligned(16))) char shared[BYTES];
+    __shared__ __attribute__((aligned(16))) float sD[4][16 * LB], sP[BWD ? BLOCKS * 16 * LB : 4];
+    __shared__ double sG[4][C];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), lr = lane & 15, lg = lane >> 4;
+    const T *q = static_cast<const T *>(a.q), *k = static_cast<const T *>(a.k);
+    // blocks go to the eight XCDs in turn: a key head's blocks, which read the same rows, are 8
+    // apart and share an L2
+    const int i8 = blockIdx.x / 8, each = a.group + BWD, which_head = i8 % each;
+    const int64_t key = (int64_t)(i8 / each) * 8 + blockIdx.x % 8, slot = key / a.HK;
+    const int hk = (int)(key % a.HK);
+    if (key >= a.slots * a.HK) return;
     int64_t row;
     int len;
     if (!gdr_chunk(a, slot, row, len)) return;
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), lr = lane & 15, lg = lane >> 4;
-
-    // k and q rows into LDS, zeros behind the sequence's end and beside a width of 16
-    const T *q = static_cast<const T *>(a.q), *k = static_cast<const T *>(a.k);
-    for (int i = tid; i < C * KP / VEC; i += 256) {
-        const int r = i / (KP / VEC), c = i % (KP / VEC) * VEC;
-        f4 x = {}, y = {};
-        if (r < len && c < K) {
-            const int64_t at = ((row + r) * a.HK + hk) * K + c;
-            x = *reinterpret_cast<const f4 *>(k + at);
-            y = *reinterpret_cast<const f4 *>(q + at);
+    if (BWD && which_head == a.group) {  // K^T, Q^T through LDS
+        T *tile = reinterpret_cast<T *>(shared);
+        for (int which = 0; which < 2; ++which) {
+            const T *from = which ? q : k;
+            if (which) __syncthreads();
+            for (int i = tid; i < C * K / VEC; i += 256) {
+                const int r = i / (K / VEC), c = i % (K / VEC) * VEC;
+                f4 x = {};
+                if (r < len) x = *reinterpret_cast<const f4 *>(from + ((row + r) * a.HK + hk) * K + c);
+                *reinterpret_cast<f4 *>(tile + r * LK + c) = x;
+            }
+            __syncthreads();
+            __bf16 *to = (which ? a.Qt : a.Kt) + key * (PK * K * C);
+            for (int i = w; i < K / 16 * 2; i += 4)
+                store_frag<PK>(to, i / 2, i % 2, lane, column8<PK>(tile, LK, 32 * (i % 2) + 8 * lg, 16 * (i / 2) + lr));
         }
-        *reinterpret_cast<f4 *>(sK + r * LK + c) = x;
-        *reinterpret_cast<f4 *>(sQ + r * LK + c) = y;
+        return;
     }
-    if (w == 0) {
-        const int64_t at = (row + lane) * a.HV + hv;
-        // log2 units in float64; beyond 2^-1000 a decay is 0 in float32 whatever follows, and
-        // the bound keeps -inf out of the differences
-        double g = lane < len ? (double)a.g[at] * 1.4426950408889634 : 0.0;
-        g = g < -1000.0 ? -1000.0 : g;
+    const int hv = hk * a.group + which_head;
+    const int64_t unit = slot * a.HV + hv;
+    float *sA = reinterpret_cast<float *>(shared), *sM = sA + BLOCKS * 16 * LB;
+
+    // log decays in log2 units, summed in float64, lane = token; beyond 2^-1000 a decay is 0 in
+    // float32 whatever follows, and the bound keeps -inf out of the differences
+    const int64_t at = (row + (lane < len ? lane : 0)) * a.HV + hv;
+    double g = (double)a.g[at] * 1.4426950408889634;
+    float beta = a.beta[at];
+    Parts<PK> fk[KS], fq[KS];
+    auto rows8 = [&](const T *x, int r, int s) {
+        const bool there = r < len && 32 * s + 8 * lg < K;
+        return load8<PK>(x + ((row + (there ? r : 0)) * a.HK + hk) * K + (there ? 32 * s + 8 * lg : 0), there);
+    };
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const double up = __shfl_up(g, d);
-            if (lane >= d) g += up;
-        }
+    for (int s = 0; s < KS; ++s) {
+        fk[s] = rows8(k, 16 * w + lr, s);
+        fq[s] = rows8(q, 16 * w + lr, s);
+    }
+    if (lane >= len) g = 0.0, beta = 0.f;
+    g = g < -1000.0 ? -1000.0 : g;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const double up = __shfl_up(g, d);
+        if (lane >= d) g += up;
+    }
+    sG[w][lane] = g;  // every wave has its own copy: no barrier
+    if (w == 0) {
         const double last = __shfl(g, 63);
-        const float beta = lane < len ? a.beta[at] : 0.f;
-        sG[lane] = g;
-        sB[lane] = beta;
-        float *dec = a.dec + (int64_t)unit * 4 * C;
+        float *dec = a.dec + unit * 4 * C;
         dec[lane] = exp2f((float)g);
         dec[C + lane] = exp2f((float)(last - g));
         dec[2 * C + lane] = beta;
-        if (BWD) a.G[(int64_t)unit * C + lane] = g;
+        if (BWD) a.G[unit * C + lane] = g;
     }
-    __syncthreads();
-
-    // A and P, tile by tile (P goes to sM until M takes its place)
+    double gi[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        f4 kk = {}, qk = {};
+    for (int e = 0; e < 4; ++e) gi[e] = sG[w][16 * w + 4 * lg + e];
+
+    // A and P of the wave's rows; P goes through the wave's rows of sM (BWD: of sP)
+    float *rowsP = BWD ? sP : sM;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
         if (c <= w) {
+            f4 kk = {}, qk = {};
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                const Parts<PK> b = load8<PK>(sK + (16 * c + lr) * LK + 32 * s + 8 * lg, true);
-                mma(kk, load8<PK>(sK + (16 * w + lr) * LK + 32 * s + 8 * lg, true), b);
-                mma(qk, load8<PK>(sQ + (16 * w + lr) * LK + 32 * s + 8 * lg, true), b);
+                const Parts<PK> f = c == w ? fk[s] : rows8(k, 16 * c + lr, s);
+                mma(kk, fk[s], f);
+                mma(qk, fq[s], f);
             }
-        }
+            const double gj = sG[w][16 * c + lr];
+            const float bj = __shfl(beta, 16 * c + lr);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = 16 * w + 4 * lg + e, j = 16 * c + lr;
-            const float d = j <= i ? exp2f((float)(sG[i] - sG[j])) : 0.f;
-            sA[i * LA + j] = j < i ? kk[e] * d : 0.f;
-            sM[i * LA + j] = j <= i ? qk[e] * d : 0.f;
-        }
-    }
-    __syncthreads();
-
-    // P (or P^T) leaves; K^T (and Q^T) leave once for the value heads of a group
-    {
-        __bf16 *to = a.P + (int64_t)unit * P * C * C;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            if (BWD) store_frag<P>(to, w, s, lane, column8<P>(sM, LA, 32 * s + 8 * lg, 16 * w + lr));
-            else store_frag<P>(to, w, s, lane, cut8<P>(sM + (16 * w + lr) * LA + 32 * s + 8 * lg));
-        }
-        if (hv % a.group == 0) {
-            const int64_t at = (slot * a.HK + hk) * (PK * K * C);
-            for (int i = w; i < K / 16 * 2; i += 4) {
-                store_frag<PK>(a.Kt + at, i / 2, i % 2, lane, column8<PK>(sK, LK, 32 * (i % 2) + 8 * lg, 16 * (i / 2) + lr));
-                if (BWD) store_frag<PK>(a.Qt + at, i / 2, i % 2, lane, column8<PK>(sQ, LK, 32 * (i % 2) + 8 * lg, 16 * (i / 2) + lr));
+            for (int e = 0; e < 4; ++e) {
+                const int i = 4 * lg + e;
+                const float d = c < w || lr <= i ? __builtin_amdgcn_exp2f((float)(gi[e] - gj)) : 0.f;
+                kk[e] = c < w || lr < i ? kk[e] * d : 0.f;
+                qk[e] = c < w || lr <= i ? qk[e] * d : 0.f;
+                sA[block_at(w, c) + i * LB + lr] = kk[e];
+                rowsP[block_at(w, c) + i * LB + lr] = qk[e];
             }
+            if (c == w) *reinterpret_cast<f4 *>(sD[w] + lr * LB + 4 * lg) = bj * kk;  // A beta, columns first
         }
-    }
-    // the inverse of block w of 1 + A beta on the diagonal, a column a lane, by substitution
+    // eight elements of a row, or of a column, of a matrix held by blocks; zeros above the diagonal
+    auto row8f = [&](const float *m, int s, float (&x)[8]) {
+        const int c = 2 * s + lg / 2;
+        const float *from = m + block_at(w, c <= w ? c : w) + lr * LB + lg % 2 * 8;
+        const f4 u = *reinterpret_cast<const f4 *>(from), v = *reinterpret_cast<const f4 *>(from + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = c <= w ? (i < 4 ? u[i % 4] : v[i % 4]) : 0.f;
+    };
+    auto column8f = [&](const float *m, int s, float (&x)[8]) {
+        const int p = 2 * s + lg / 2;
+        const float *from = m + block_at(p >= w ? p : w, w) + lg % 2 * 8 * LB + lr;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = p >= w ? from[i * LB] : 0.f;
+    };
+    float x8[8];
+    if (!BWD)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            if (s <= w / 2) {
+                row8f(sM, s, x8);
+                store_frag<PO>(a.P + unit * (PO * C * C), w, s, lane, cut8<PO>(x8));
+            }
+    // the inverse of block w of 1 + A beta on the diagonal by substitution, a column a lane: as
+    // soon as row m of the inverse is there its part is taken off all rows below
     {
-        float x[16];
+        f4 x[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float s = i == lr ? 1.f : 0.f;
+        for (int i = 0; i < 16; ++i) x[i / 4][i % 4] = i == lr ? 1.f : 0.f;
 #pragma unroll
-            for (int m = 0; m < i; ++m) s -= sA[(16 * w + i) * LA + 16 * w + m] * (sB[16 * w + m] * x[m]);
-            x[i] = s;
+        for (int m = 0; m < 15; ++m) {
+            const float xm = x[m / 4][m % 4];
+#pragma unroll
+            for (int i4 = (m + 1) / 4; i4 < 4; ++i4) {
+                const f4 l = *reinterpret_cast<const f4 *>(sD[w] + m * LB + 4 * i4);  // 0 up to the diagonal
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (4 * i4 + e > m) x[i4][e] -= l[e] * xm;
+            }
         }
         if (lg == 0) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sD[(16 * w + i) * 20 + lr] = x[i];
+            for (int i = 0; i < 16; ++i) sD[w][i * LB + lr] = x[i / 4][i % 4];
         }
     }
-    __syncthreads();
+    gdr_lds_barrier();
 
     // M by columns of blocks, wave w column w: (1 + A_pp beta_p) M_pw = -(A_pw + sum_r A_pr beta_r M_rw).
     // Step e of a product takes k = 4 (lane / 16) + e, which is how an accumulator holds its rows.
-    {
-        f4 m[4];
+    f4 m[4];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            f4 acc = {};
-            if (p >= w) {
+    for (int p = 0; p < 4; ++p)
+        if (p >= w) {
+            f4 acc;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[e] = sA[(16 * p + 4 * lg + e) * LA + 16 * w + lr];
+            for (int e = 0; e < 4; ++e) acc[e] = sA[block_at(p, w) + (4 * lg + e) * LB + lr];
 #pragma unroll
-                for (int r = 0; r < p; ++r)
-                    if (r >= w) {
-                        const f4 x = *reinterpret_cast<const f4 *>(sA + (16 * p + lr) * LA + 16 * r + 4 * lg);
+            for (int r = 0; r < p; ++r)
+                if (r >= w) {
+                    const f4 x = *reinterpret_cast<const f4 *>(sA + block_at(p, r) + lr * LB + 4 * lg);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], m[r][e], acc, 0, 0, 0);
-                    }
-                const f4 d = *reinterpret_cast<const f4 *>(sD + (16 * p + lr) * 20 + 4 * lg);
-                f4 y = {};
+                    for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], m[r][e], acc, 0, 0, 0);
+                }
+            const f4 d = *reinterpret_cast<const f4 *>(sD[p] + lr * LB + 4 * lg);
+            f4 y = {};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y = __builtin_amdgcn_mfma_f32_16x16x4f32(d[e], -acc[e], y, 0, 0, 0);
-                acc = y;
-            }
+            for (int e = 0; e < 4; ++e) y = __builtin_amdgcn_mfma_f32_16x16x4f32(d[e], -acc[e], y, 0, 0, 0);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                sM[(16 * p + 4 * lg + e) * LA + 16 * w + lr] = acc[e];
-                m[p][e] = acc[e] * sB[16 * p + 4 * lg + e];
+                sM[block_at(p, w) + (4 * lg + e) * LB + lr] = y[e];
+                m[p][e] = y[e] * __shfl(beta, 16 * p + 4 * lg + e);
             }
         }
-    }
-    __syncthreads();
-    {
-        const int64_t at = (int64_t)unit * P * C * C;
+    gdr_lds_barrier();
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            store_frag<P>(a.M + at, w, s, lane, cut8<P>(sM + (16 * w + lr) * LA + 32 * s + 8 * lg));
-            if (BWD) store_frag<P>(a.Mt + at, w, s, lane, column8<P>(sM, LA, 32 * s + 8 * lg, 16 * w + lr));
+    for (int s = 0; s < 2; ++s) {
+        if (s <= w / 2) {
+            row8f(sM, s, x8);
+            store_frag<P>(a.M + unit * (P * C * C), w, s, lane, cut8<P>(x8));
+        }
+        if (BWD && s >= w / 2) {
+            column8f(sM, s, x8);
+            store_frag<P>(a.Mt + unit * (P * C * C), w, s, lane, cut8<P>(x8));
+            column8f(sP, s, x8);
+            store_frag<P>(a.P + unit * (P * C * C), w, s, lane, cut8<P>(x8));
         }
     }
 }
 
-// What a wave needs of one chunk beside the state: its 16 rows of K, Q, M and P, its channel
-// rows of K^T, its values and decays.
-template <typename T, int K, int P, bool TRAIN>
-struct ChainOps {
-    static constexpr int PK = gdr_input_parts<T>(), KS = K < 32 ? 1 : K / 32, NC = (K / 16 + 3) / 4;
-    Parts<PK> k[KS], q[TRAIN ? 1 : KS], kt[NC][2];
-    Parts<P> m[2], p[TRAIN ? 1 : 2];
-    f4 v, b, end, beta;
-    float last;
-
-    __device__ __forceinline__ void load(const GdrArgs &a, int64_t slot, int64_t row, int len, int hv, int col, int w, int lane) {
-        const int lr = lane & 15, lg = lane >> 4, hk = hv / a.group;
-        const int64_t unit = slot * a.HV + hv;
-        const int64_t at = ((row + 16 * w + lr) * a.HK + hk) * K + 8 * lg;
-        const bool there = 16 * w + lr < len;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            k[s] = load8<PK>(static_cast<const T *>(a.k) + at + 32 * s, there && 32 * s + 8 * lg < K);
-            if (!TRAIN) q[s] = load8<PK>(static_cast<const T *>(a.q) + at + 32 * s, there && 32 * s + 8 * lg < K);
-        }
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-            if (s <= w / 2) {
-                m[s] = load_frag<P>(a.M + unit * (P * C * C), w, s, lane);
-                if (!TRAIN) p[s] = load_frag<P>(a.P + unit * (P * C * C), w, s, lane);
-            }
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (w + 4 * c < K / 16)
-#pragma unroll
-                for (int s = 0; s < 2; ++s) kt[c][s] = load_frag<PK>(a.Kt + (slot * a.HK + hk) * (PK * K * C), w + 4 * c, s, lane);
-        const float *dec = a.dec + unit * 4 * C + 16 * w + 4 * lg;
-        b = *reinterpret_cast<const f4 *>(dec);
-        end = *reinterpret_cast<const f4 *>(dec + C);
-        beta = *reinterpret_cast<const f4 *>(dec + 2 * C);
-        last = a.dec[unit * 4 * C + C - 1];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int r = 16 * w + 4 * lg + e;
-            v[e] = r < len ? to_f32(static_cast<const T *>(a.v)[((row + r) * a.HV + hv) * a.V + col]) : 0.f;
-        }
-    }
-};
-
-// One workgroup of four waves per (sequence, value head, 16 value columns).  Wave w owns
-// token rows 16w..16w+15 of the chunk and the state's channel tiles w, w + 4, ..; what the
-// waves exchange (beta X, Vn, the state) goes through LDS as bf16 parts, columns first.
-template <typename T, int K, int P, bool TRAIN>
+// The chain.  One workgroup of four waves per (sequence, value head, 16 NV value columns).
+// Wave w owns token rows 16w..16w+15 of the chunk and the state's channel tiles w, w + 4, ..;
+// what the waves exchange (beta X, Vn, the state) goes through LDS as bf16 parts, columns first.
+// The operands come from memory straight into the registers of the wave that uses them, each
+// for the next chunk as soon as this chunk's product has read it, so that they are in flight
+// over most of a chunk.  Rows behind the sequence's end read its last row: their beta is 0, so
+// nothing of them reaches the state.
+//
+// P: parts of what reaches the state, PO: parts of what reaches the output alone.
+template <typename T, typename OT, int K, int P, int PO, int NV, bool TRAIN>
 __global__ __launch_bounds__(256) void gdr_chain_kernel(const GdrArgs a) {
-    using Ops = ChainOps<T, K, P, TRAIN>;
-    constexpr int KP = K < 32 ? 32 : K, LS = KP + 8, LT = C + 8, KS = Ops::KS, NC = Ops::NC;
-    __shared__ __attribute__((aligned(16))) __bf16 sS[P * 16 * LS], sX[P * 16 * LT], sV[P * 16 * LT], sE[P * 16 * LT];
-    const int VB = a.V / 16, unit = gdr_xcd_unit(blockIdx.x, gridDim.x);
-    const int vb = unit % VB, hv = unit / VB % a.HV, n = unit / VB / a.HV;
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15, lg = lane >> 4;
-    const int col = 16 * vb + lr;
+    constexpr int PK = gdr_input_parts<T>(), KP = K < 32 ? 32 : K, KS = KP / 32, NC = (K / 16 + 3) / 4, W = 16 * NV, SZ = sizeof(T);
+    __shared__ __attribute__((aligned(16))) __bf16 sS[P * W * KP], sX[P * W * C], sE[P * W * C], sV[TRAIN ? 8 : PO * W * C], sK[PK * C * KP];
+    int vb, hv, n;
+    if (!gdr_pair(a, a.V / W, vb, hv, n)) return;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15, lg = lane >> 4, hk = hv / a.group;
     int64_t row, len, slot;
     gdr_sequence(a, n, row, len, slot);
-    const int64_t state = ((int64_t)n * a.HV + hv) * K * a.V;
+    const int64_t state = ((int64_t)n * a.HV + hv) * K * a.V + W * vb;
 
-    if (K < 32)
-        for (int i = threadIdx.x; i < P * 16 * LS; i += 256) sS[i] = (__bf16)0.f;
-    if (K < 32) __syncthreads();
-    f4 S[NC];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        S[c] = f4{};
-        if (w + 4 * c < K / 16) {
-            const int ch = 16 * (w + 4 * c) + 4 * lg;
-            if (a.s0)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S[c][e] = a.s0[state + (int64_t)(ch + e) * a.V + col];
-            lds_put4<P>(sS, 16 * LS, LS, lr, ch, S[c]);
-        }
+    if (K < 32) {
+        for (int i = threadIdx.x; i < P * W * KP; i += 256) sS[i] = (__bf16)0.f;
+        __syncthreads();
     }
-    Ops o;
-    for (int64_t t = 0; t < len; t += C, ++slot) {
-        const int here = (int)(len - t < C ? len - t : C);
-        o.load(a, slot, row + t, here, hv, col, w, lane);
-        if (TRAIN) {
-            float *h = a.h + (slot * a.HV + hv) * ((int64_t)K * a.V);
+    f4 S[NC][NV];
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-                if (w + 4 * c < K / 16)
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) h[(int64_t)(16 * (w + 4 * c) + 4 * lg + e) * a.V + col] = S[c][e];
+        for (int u = 0; u < NV; ++u) {
+            S[c][u] = f4{};
+            if (w + 4 * c < K / 16) {
+                const int ch = 16 * (w + 4 * c) + 4 * lg;
+                if (a.s0)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[c][u][e] = a.s0[state + (int64_t)(ch + e) * a.V + lr + 16 * u];
+                lds_put4<P, W, KP>(sS, 16 * u + lr, ch, S[c][u]);
+            }
         }
-        gdr_lds_barrier();
-        f4 x = {}, y = {};
+
+    const int chunks = (int)((len + C - 1) / C);
+    // byte strides of a token, and this lane's offsets from a chunk's first token
+    const unsigned kstep = (unsigned)a.HK * K * SZ, vstep = (unsigned)a.HV * a.V * SZ, ostep = (unsigned)a.HV * a.V * sizeof(OT);
+    const char *kbase = static_cast<const char *>(a.k) + (row * a.HK + hk) * (K * SZ), *qbase = static_cast<const char *>(a.q) + (row * a.HK + hk) * (K * SZ);
+    const char *vbase = static_cast<const char *>(a.v) + ((row * a.HV + hv) * a.V + W * vb) * SZ;
+    char *obase = static_cast<char *>(a.out) + ((row * a.HV + hv) * a.V + W * vb) * sizeof(OT);
+    const unsigned kcol = (K < 32 ? lg % 2 * 8 : 8 * lg) * SZ;  // beside a width of 16 the state's parts are zero
+    const unsigned krow = (16 * w + lr) * kstep + kcol, r0 = 16 * w + 4 * lg;
+    Parts<PK> k[KS], q[KS];
+    Parts<P> m[2];
+    Parts<PO> p[2];
+    f4 b, end, beta, nb, nend, nbeta;
+    Parts<PK> v, nv;
+    bf16x8 one[NV];
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) one[u][i] = (__bf16)(8 * lg + i == 16 * u + lr ? 1.f : 0.f);
+    const unsigned vcol = (NV == 1 ? lg % 2 * 8 : 8 * lg) * SZ;
+    float last, nlast, blr, nblr;
+    auto load_kq = [&](int c) {
+        const int64_t t = (int64_t)c * C;
+        unsigned at = krow;
+        if (t + C > len) at = (unsigned)(16 * w + lr < len - t ? 16 * w + lr : len - t - 1) * kstep + kcol;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const Parts<P> f = lds_frag<P>(sS, 16 * LS, LS, lr, 32 * s + 8 * lg);
-            mma(x, o.k[s], f);
-            if (!TRAIN) mma(y, o.q[s], f);
+            k[s] = load8<PK>(reinterpret_cast<const T *>(kbase + t * kstep + at + 32 * s * SZ), true);
+            if (!TRAIN) q[s] = load8<PK>(reinterpret_cast<const T *>(qbase + t * kstep + at + 32 * s * SZ), true);
         }
-        x = o.v - o.b * x;
-        lds_put4<P>(sX, 16 * LT, LT, lr, 16 * w + 4 * lg, o.beta * x);
+    };
+    auto load_m = [&](int c) {
+        const __bf16 *from = a.M + ((slot + c) * a.HV + hv) * (P * C * C);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            if (s <= w / 2) m[s] = load_frag<P>(from, w, s, lane);
+    };
+    auto load_p = [&](int c) {
+        const __bf16 *from = a.P + ((slot + c) * a.HV + hv) * (PO * C * C);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            if (!TRAIN && s <= w / 2) p[s] = load_frag<PO>(from, w, s, lane);
+    };
+    auto load_rows = [&](int c) {  // into the second set
+        const float *dec = a.dec + ((slot + c) * a.HV + hv) * (4 * C);
+        nb = at_offset<f4>(dec, r0 * 4);
+        nend = at_offset<f4>(dec + C, r0 * 4);
+        nbeta = at_offset<f4>(dec + 2 * C, r0 * 4);
+        nlast = dec[C - 1];
+        nblr = at_offset<float>(dec, (16 * w + lr) * 4);
+        const int64_t t = (int64_t)c * C;
+        const unsigned r = 16 * w + lr < len - t ? 16 * w + lr : (unsigned)(len - t - 1);
+        nv = load8<PK>(reinterpret_cast<const T *>(vbase + t * vstep + (r * vstep + vcol)), true);
+    };
+    if (chunks > 0) {
+        load_rows(0);
+        load_kq(0);
+        load_m(0);
+        load_p(0);
+    }
+    for (int c = 0; c < chunks; ++c) {
+        const int next = c + 1 < chunks ? c + 1 : c;
+        b = nb, end = nend, beta = nbeta, last = nlast, blr = nblr;
+        v = nv;
+        load_rows(next);
+        if (TRAIN) {
+            float *h = a.h + ((slot + c) * a.HV + hv) * ((int64_t)K * a.V) + W * vb;
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                if (w + 4 * i < K / 16)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int u = 0; u < NV; ++u) h[(16 * (w + 4 * i) + 4 * lg + e) * a.V + lr + 16 * u] = S[i][u][e];
+        }
+        gdr_lds_barrier();
+        // K's rows also go to LDS, where the state's update reads them by columns
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int i = 0; i < PK; ++i) *reinterpret_cast<bf16x8 *>(sK + i * C * KP + lds_at<KP>(16 * w + lr, 32 * s + 8 * lg)) = k[s].v[i];
+        f4 x[NV], y[NV];
+#pragma unroll
+        for (int u = 0; u < NV; ++u) x[u] = y[u] = f4{};
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int u = 0; u < NV; ++u) {
+                const Parts<P> f = lds_frag<P, W, KP>(sS, 16 * u + lr, 32 * s + 8 * lg);
+                mma(x[u], k[s], f);
+                if (!TRAIN) mma_to<PO>(y[u], f, q[s]);  // columns by tokens: a lane gets four columns of a token
+            }
+        load_kq(next);
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            x[u] *= -b;
+            mma(x[u], v, Parts<1>{{one[u]}});
+            lds_put4<P, W, C>(sX, 16 * u + lr, r0, beta * x[u]);
+        }
         gdr_lds_barrier();
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (s <= w / 2) mma(x, o.m[s], lds_frag<P>(sX, 16 * LT, LT, lr, 32 * s + 8 * lg));
-        const f4 vn = o.beta * x;
-        if (!TRAIN) lds_put4<P>(sV, 16 * LT, LT, lr, 16 * w + 4 * lg, vn);
-        lds_put4<P>(sE, 16 * LT, LT, lr, 16 * w + 4 * lg, o.end * vn);
+            if (s <= w / 2)
+#pragma unroll
+                for (int u = 0; u < NV; ++u) mma(x[u], m[s], lds_frag<P, W, C>(sX, 16 * u + lr, 32 * s + 8 * lg));
+        load_m(next);
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            const f4 vn = beta * x[u];
+            lds_put4<P, W, C>(sE, 16 * u + lr, r0, end * vn);
+            if (!TRAIN) lds_put4<PO, W, C>(sV, 16 * u + lr, r0, vn);
+        }
         gdr_lds_barrier();
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (w + 4 * c < K / 16) {
-                S[c] *= o.last;
+        for (int i = 0; i < NC; ++i)
+            if (w + 4 * i < K / 16) {
+                Parts<PK> kt[2];
 #pragma unroll
-                for (int s = 0; s < 2; ++s) mma(S[c], o.kt[c][s], lds_frag<P>(sE, 16 * LT, LT, lr, 32 * s + 8 * lg));
-                lds_put4<P>(sS, 16 * LS, LS, lr, 16 * (w + 4 * c) + 4 * lg, S[c]);
+                for (int s = 0; s < 2; ++s) kt[s] = lds_frag_turned<PK, C, KP>(sK, 32 * s + 8 * lg, 16 * (w + 4 * i), lane);
+#pragma unroll
+                for (int u = 0; u < NV; ++u) {
+                    S[i][u] *= last;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) mma(S[i][u], kt[s], lds_frag<P, W, C>(sE, 16 * u + lr, 32 * s + 8 * lg));
+                    lds_put4<P, W, KP>(sS, 16 * u + lr, 16 * (w + 4 * i) + 4 * lg, S[i][u]);
+                }
             }
+        const int64_t t = (int64_t)c * C;
         if (TRAIN) {
-            float *d = a.delta + (slot * a.HV + hv) * ((int64_t)C * a.V);
+            float *d = a.delta + ((slot + c) * a.HV + hv) * ((int64_t)C * a.V) + W * vb;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) d[(int64_t)(16 * w + 4 * lg + e) * a.V + col] = x[e];
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int u = 0; u < NV; ++u) d[(r0 + e) * a.V + lr + 16 * u] = x[u][e];
         } else {
-            y *= o.b;
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-                if (s <= w / 2) mma(y, o.p[s], lds_frag<P>(sV, 16 * LT, LT, lr, 32 * s + 8 * lg));
+            for (int u = 0; u < NV; ++u) {
+                y[u] *= blr;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = 16 * w + 4 * lg + e;
-                if (r < here) st_out(a.out, a.out_bf16, ((row + t + r) * a.HV + hv) * a.V + col, a.scale * y[e]);
+                for (int s = 0; s < 2; ++s)
+                    if (s <= w / 2) mma_to<PO>(y[u], lds_frag<PO, W, C>(sV, 16 * u + lr, 32 * s + 8 * lg), p[s]);
+                y[u] *= a.scale;
             }
+            load_p(next);
+            char *to = obase + t * ostep;
+            typedef __attribute__((ext_vector_type(4))) OT ot4;
+            if (16 * w + lr < len - t)
+#pragma unroll
+                for (int u = 0; u < NV; ++u)
+                    *reinterpret_cast<ot4 *>(to + ((16 * w + lr) * ostep + (16 * u + 4 * lg) * (unsigned)sizeof(OT))) = __builtin_convertvector(y[u], ot4);
         }
     }
     if (!TRAIN && a.sf)
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (w + 4 * c < K / 16)
+        for (int i = 0; i < NC; ++i)
+            if (w + 4 * i < K / 16)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) a.sf[state + (int64_t)(16 * (w + 4 * c) + 4 * lg + e) * a.V + col] = S[c][e];
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int u = 0; u < NV; ++u) a.sf[state + (int64_t)(16 * (w + 4 * i) + 4 * lg + e) * a.V + lr + 16 * u] = S[i][u][e];
 }
 
 template <typename F>
@@ -314,18 +427,20 @@ hipError_t by_width(int K, F f) {
     return hipErrorNotSupported;
 }
 
-template <typename T, int P, bool BWD>
+template <typename T, int P, int PO, bool BWD>
 hipError_t prep(const GdrArgs &a, int K, hipStream_t stream) {
     return by_width(K, [&](auto k) {
-        hipLaunchKernelGGL((gdr_prep_kernel<T, decltype(k)::value, P, BWD>), dim3((unsigned)(a.slots * a.HV)), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((gdr_prep_kernel<T, decltype(k)::value, P, PO, BWD>), dim3((unsigned)((a.slots * a.HK + 7) / 8 * 8 * (a.group + BWD))), dim3(256), 0, stream, a);
         return hipGetLastError();
     });
 }
-template <typename T, int P, bool TRAIN>
+template <typename T, typename OT, int P, int PO, bool TRAIN>
 hipError_t chain(const GdrArgs &a, int K, hipStream_t stream) {
     return by_width(K, [&](auto k) {
-        hipLaunchKernelGGL((gdr_chain_kernel<T, decltype(k)::value, P, TRAIN>), dim3((unsigned)((int64_t)a.N * a.HV * (a.V / 16))), dim3(256), 0,
-                           stream, a);
+        constexpr int KK = decltype(k)::value;
+        const int nv = gdr_column_tiles(a);
+        if (nv == 2) hipLaunchKernelGGL((gdr_chain_kernel<T, OT, KK, P, PO, 2, TRAIN>), dim3((unsigned)gdr_pair_blocks(a, a.V / 32)), dim3(256), 0, stream, a);
+        else hipLaunchKernelGGL((gdr_chain_kernel<T, OT, KK, P, PO, 1, TRAIN>), dim3((unsigned)gdr_pair_blocks(a, a.V / 16)), dim3(256), 0, stream, a);
         return hipGetLastError();
     });
 }
@@ -333,13 +448,14 @@ hipError_t chain(const GdrArgs &a, int K, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_gdr_prep(const GdrArgs &a, bool fp32, int K, bool bwd, hipStream_t stream) {
-    if (bwd) return fp32 ? prep<float, 3, true>(a, K, stream) : prep<__bf16, 3, true>(a, K, stream);
-    return fp32 ? prep<float, 3, false>(a, K, stream) : prep<__bf16, 2, false>(a, K, stream);
+    if (bwd) return fp32 ? prep<float, 3, 3, true>(a, K, stream) : prep<__bf16, 3, 3, true>(a, K, stream);
+    return fp32 ? prep<float, 3, 3, false>(a, K, stream) : prep<__bf16, GDR_STATE_PARTS, 2, false>(a, K, stream);
 }
 
 hipError_t launch_gdr_fwd_chain(const GdrArgs &a, bool fp32, int K, bool train, hipStream_t stream) {
-    if (train) return fp32 ? chain<float, 3, true>(a, K, stream) : chain<__bf16, 3, true>(a, K, stream);
-    return fp32 ? chain<float, 3, false>(a, K, stream) : chain<__bf16, 2, false>(a, K, stream);
+    if (train) return fp32 ? chain<float, float, 3, 3, true>(a, K, stream) : chain<__bf16, float, 3, 3, true>(a, K, stream);
+    if (a.out_bf16) return fp32 ? chain<float, __bf16, 3, 3, false>(a, K, stream) : chain<__bf16, __bf16, GDR_STATE_PARTS, 2, false>(a, K, stream);
+    return fp32 ? chain<float, float, 3, 3, false>(a, K, stream) : chain<__bf16, float, GDR_STATE_PARTS, 2, false>(a, K, stream);
 }
 
 }  // namespace kda

@@ -37,8 +37,8 @@ def test_chunk_fwd_refusals(lib, kw, status):
 def test_chunk_fwd_workspace(lib):
     size = lambda dt=torch.bfloat16, B=1, T=64, HK=2, HV=4, K=16, V=16, N=0, packed=False: kda.gdr_chunk_fwd_workspace_size(  # noqa: E731
         dt, B, T, HK, HV, K, V, N, packed)
-    # two bf16 parts of M and of P, four rows of 64 floats, and one part of K^T for a key head
-    assert size() == 4 * (2 * 2 * 64 * 64 * 2 + 4 * 64 * 4) + 2 * 16 * 64 * 2
+    # three bf16 parts of M and two of P (three with float32 inputs), and four rows of 64 floats
+    assert size() == 4 * ((3 + 2) * 64 * 64 * 2 + 4 * 64 * 4) and size(torch.float32) == 4 * ((3 + 3) * 64 * 64 * 2 + 4 * 64 * 4)
     assert size(T=65) == 2 * size() == size(B=2) and size(T=64 * 7) == 7 * size()
     assert size(T=130, N=4, packed=True) == 6 * size()  # T // 64 + N chunk slots
     assert size(K=24) == 0 and size(HV=3) == 0 and size(T=0) == 0
