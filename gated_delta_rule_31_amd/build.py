@@ -21,7 +21,7 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
 # ordinary vector registers (the float32 state is rescaled by vector instructions every
 # chunk; accumulation registers would need a move each way)
 EXTRA = {"kda_chunk_chain.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-         "kda_gdr_fwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+         "kda_gdr_fwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"], "kda_gdr_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def build(verbose: bool = False) -> str:

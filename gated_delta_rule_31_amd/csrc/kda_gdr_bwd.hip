@@ -24,135 +24,187 @@ namespace {
 
 constexpr int C = GDR_C, P = 3;
 
-__device__ __forceinline__ float ld_any(const void *p, int bf16, int64_t i) {
-    return bf16 ? (float)static_cast<const __bf16 *>(p)[i] : static_cast<const float *>(p)[i];
-}
-
-// The chain of gradients: workgroups and waves as in the forward chain.
-template <typename T, int K>
+// The chain of gradients: workgroups, waves and operands in flight as in the forward chain.
+// D: the type of d_out, whose parts are exact until the read's scale meets them.
+template <typename T, typename D, int K, int NV>
 __global__ __launch_bounds__(256) void gdr_bwd_chain_kernel(const GdrArgs a) {
-    constexpr int PK = gdr_input_parts<T>(), KP = K < 32 ? 32 : K, KS = KP / 32, NC = (K / 16 + 3) / 4;
-    __shared__ __attribute__((aligned(16))) __bf16 sS[P * 16 * KP], sO[P * 16 * C], sX[P * 16 * C], sB[P * 16 * C], sE[P * 16 * C];
+    constexpr int PK = gdr_input_parts<T>(), PD = gdr_input_parts<D>(), KP = K < 32 ? 32 : K, KS = KP / 32, NC = (K / 16 + 3) / 4, W = 16 * NV;
+    constexpr int SZ = sizeof(T), DZ = sizeof(D);
+    __shared__ __attribute__((aligned(16))) __bf16 sS[P * W * KP], sX[P * W * C], sB[P * W * C], sE[P * W * C], sK[PK * C * KP], sQ[PK * C * KP], sO[PD * C * 32];
     int vb, hv, n;
-    if (!gdr_pair(a, a.V / 16, vb, hv, n)) return;
-    const int hk = hv / a.group;
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15, lg = lane >> 4;
-    const int col = 16 * vb + lr;
+    if (!gdr_pair(a, a.V / W, vb, hv, n)) return;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15, lg = lane >> 4, hk = hv / a.group;
     int64_t row, len, slot;
     gdr_sequence(a, n, row, len, slot);
-    const int64_t state = ((int64_t)n * a.HV + hv) * K * a.V;
+    const int64_t state = ((int64_t)n * a.HV + hv) * K * a.V + W * vb;
     if (K < 32) {
-        for (int i = threadIdx.x; i < P * 16 * KP; i += 256) sS[i] = (__bf16)0.f;
+        for (int i = threadIdx.x; i < P * W * KP; i += 256) sS[i] = (__bf16)0.f;
         __syncthreads();
     }
-    f4 S[NC];
+    f4 S[NC][NV];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        S[c] = f4{};
-        if (w + 4 * c < K / 16) {
-            const int ch = 16 * (w + 4 * c) + 4 * lg;
-            if (a.d_sf)
+    for (int i = 0; i < NC; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) S[c][e] = a.d_sf[state + (int64_t)(ch + e) * a.V + col];
-            lds_put4<P, 16, KP>(sS, lr, ch, S[c]);
-        }
-    }
-    const int64_t chunks = (len + C - 1) / C;
-    for (int64_t j = chunks - 1; j >= 0; --j) {
-        const int64_t t = j * C, at = (slot + j) * a.HV + hv;
-        const int here = (int)(len - t < C ? len - t : C);
-        // this chunk's operands
-        Parts<PK> k[KS], kt[NC][2], qt[NC][2];
-        Parts<P> m[2], p[2];
-        f4 b, end, beta, dO;
-        {
-            const bool there = 16 * w + lr < here;
-            const T *kp = static_cast<const T *>(a.k) + ((row + t + 16 * w + lr) * a.HK + hk) * K + 8 * lg;
+        for (int u = 0; u < NV; ++u) {
+            S[i][u] = f4{};
+            if (w + 4 * i < K / 16) {
+                const int ch = 16 * (w + 4 * i) + 4 * lg;
+                if (a.d_sf)
 #pragma unroll
-            for (int s = 0; s < KS; ++s) k[s] = load8<PK>(kp + 32 * s, there && 32 * s + 8 * lg < K);
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                if (s >= w / 2) {
-                    m[s] = load_frag<P>(a.Mt + at * (P * C * C), w, s, lane);
-                    p[s] = load_frag<P>(a.P + at * (P * C * C), w, s, lane);
-                }
-            const int64_t kq = ((slot + j) * a.HK + hk) * (PK * K * C);
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-                if (w + 4 * c < K / 16)
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        kt[c][s] = load_frag<PK>(a.Kt + kq, w + 4 * c, s, lane);
-                        qt[c][s] = load_frag<PK>(a.Qt + kq, w + 4 * c, s, lane);
-                    }
-            const float *dec = a.dec + at * 4 * C + 16 * w + 4 * lg;
-            b = *reinterpret_cast<const f4 *>(dec);
-            end = *reinterpret_cast<const f4 *>(dec + C);
-            beta = *reinterpret_cast<const f4 *>(dec + 2 * C);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = 16 * w + 4 * lg + e;
-                dO[e] = r < here ? a.scale * ld_any(a.d_out, a.dout_bf16, ((row + t + r) * a.HV + hv) * a.V + col) : 0.f;
+                    for (int e = 0; e < 4; ++e) S[i][u][e] = a.d_sf[state + (int64_t)(ch + e) * a.V + lr + 16 * u];
+                lds_put4<P, W, KP>(sS, 16 * u + lr, ch, S[i][u]);
             }
         }
-        const float last = a.dec[at * 4 * C + C - 1];
-        float *dh = a.dh + at * ((int64_t)K * a.V);
+    const int chunks = (int)((len + C - 1) / C);
+    const unsigned kstep = (unsigned)a.HK * K * SZ, ostep = (unsigned)a.HV * a.V * DZ;
+    const char *kbase = static_cast<const char *>(a.k) + (row * a.HK + hk) * (K * SZ), *qbase = static_cast<const char *>(a.q) + (row * a.HK + hk) * (K * SZ);
+    const char *obase = static_cast<const char *>(a.d_out) + ((row * a.HV + hv) * a.V + W * vb) * DZ;
+    const unsigned kcol = (K < 32 ? lg % 2 * 8 : 8 * lg) * SZ, ocol = (NV == 1 ? lg % 2 * 8 : 8 * lg) * DZ, r0 = 16 * w + 4 * lg;
+    bf16x8 one[NV];  // d_out enters as operands, eight columns of a row a lane: dO = dO 1
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (w + 4 * c < K / 16)
+    for (int u = 0; u < NV; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dh[(int64_t)(16 * (w + 4 * c) + 4 * lg + e) * a.V + col] = S[c][e];
-        lds_put4<P, 16, C>(sO, lr, 16 * w + 4 * lg, dO);
-        gdr_lds_barrier();
-        f4 x = {}, y = {};
+        for (int i = 0; i < 8; ++i) one[u][i] = (__bf16)(8 * lg + i == 16 * u + lr ? 1.f : 0.f);
+    Parts<PK> k[KS], q[KS];
+    Parts<P> m[2], p[2];
+    Parts<PD> o;
+    f4 b, end, beta;
+    float last;
+    // rows behind the sequence's end read its last row: P^T and M^T are 0 there, and so is beta
+    auto load_kqo = [&](int c) {
+        const int64_t t = (int64_t)c * C;
+        const bool there = 16 * w + lr < len - t;
+        const unsigned r = there ? 16 * w + lr : (unsigned)(len - t - 1);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) mma(x, k[s], lds_frag<P, 16, KP>(sS, lr, 32 * s + 8 * lg));
+        for (int s = 0; s < KS; ++s) {
+            k[s] = load8<PK>(reinterpret_cast<const T *>(kbase + t * kstep + (r * kstep + kcol) + 32 * s * SZ), true);
+            q[s] = load8<PK>(reinterpret_cast<const T *>(qbase + t * kstep + (r * kstep + kcol) + 32 * s * SZ), true);
+        }
+        o = load8<PD>(reinterpret_cast<const D *>(obase + t * ostep + (r * ostep + ocol)), there);
+    };
+    auto load_frags = [&](const __bf16 *base, Parts<P> (&f)[2], int c) {
+        const __bf16 *from = base + ((slot + c) * a.HV + hv) * (P * C * C);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (s >= w / 2) mma(y, p[s], lds_frag<P, 16, C>(sO, lr, 32 * s + 8 * lg));
-        x = end * x + y;
-        lds_put4<P, 16, C>(sX, lr, 16 * w + 4 * lg, beta * x);
-        lds_put4<P, 16, C>(sB, lr, 16 * w + 4 * lg, b * dO);
+            if (s >= w / 2) f[s] = load_frag<P>(from, w, s, lane);
+    };
+    auto load_dec = [&](int c) {
+        const float *dec = a.dec + ((slot + c) * a.HV + hv) * (4 * C);
+        b = at_offset<f4>(dec, r0 * 4);
+        end = at_offset<f4>(dec + C, r0 * 4);
+        beta = at_offset<f4>(dec + 2 * C, r0 * 4);
+        last = dec[C - 1];
+    };
+    if (chunks > 0) {
+        load_kqo(chunks - 1);
+        load_frags(a.P, p, chunks - 1);
+        load_dec(chunks - 1);
+        load_frags(a.Mt, m, chunks - 1);
+    }
+    for (int c = chunks - 1; c >= 0; --c) {
+        const int next = c > 0 ? c - 1 : 0;
+        const int64_t at = (slot + c) * a.HV + hv, t = (int64_t)c * C;
+        float *dh = a.dh + at * ((int64_t)K * a.V) + W * vb;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+            if (w + 4 * i < K / 16)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int u = 0; u < NV; ++u) dh[(16 * (w + 4 * i) + 4 * lg + e) * a.V + lr + 16 * u] = S[i][u][e];
+#pragma unroll
+        for (int i = 0; i < PD; ++i) *reinterpret_cast<bf16x8 *>(sO + i * C * 32 + lds_at<32>(16 * w + lr, 8 * lg)) = o.v[i];
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int i = 0; i < PK; ++i) {
+                *reinterpret_cast<bf16x8 *>(sK + i * C * KP + lds_at<KP>(16 * w + lr, 32 * s + 8 * lg)) = k[s].v[i];
+                *reinterpret_cast<bf16x8 *>(sQ + i * C * KP + lds_at<KP>(16 * w + lr, 32 * s + 8 * lg)) = q[s].v[i];
+            }
+        gdr_lds_barrier();
+        f4 x[NV], y[NV], d[NV];
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            x[u] = y[u] = d[u] = f4{};
+            mma(d[u], o, Parts<1>{{one[u]}});
+        }
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int u = 0; u < NV; ++u) mma(x[u], k[s], lds_frag<P, W, KP>(sS, 16 * u + lr, 32 * s + 8 * lg));
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            if (s >= w / 2)
+#pragma unroll
+                for (int u = 0; u < NV; ++u) mma(y[u], p[s], lds_frag_turned<PD, C, 32>(sO, 32 * s + 8 * lg, 16 * u, lane));
+        load_kqo(next);
+        load_frags(a.P, p, next);
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            x[u] = end * x[u] + a.scale * y[u];
+            lds_put4<P, W, C>(sX, 16 * u + lr, r0, beta * x[u]);
+            lds_put4<P, W, C>(sB, 16 * u + lr, r0, a.scale * b * d[u]);
+        }
         gdr_lds_barrier();
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (s >= w / 2) mma(x, m[s], lds_frag<P, 16, C>(sX, lr, 32 * s + 8 * lg));
-        const f4 E = beta * x;
-        lds_put4<P, 16, C>(sE, lr, 16 * w + 4 * lg, -(b * E));
+            if (s >= w / 2)
+#pragma unroll
+                for (int u = 0; u < NV; ++u) mma(x[u], m[s], lds_frag<P, W, C>(sX, 16 * u + lr, 32 * s + 8 * lg));
+        load_frags(a.Mt, m, next);
+        f4 E[NV];
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            E[u] = beta * x[u];
+            lds_put4<P, W, C>(sE, 16 * u + lr, r0, -(b * E[u]));
+        }
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int u = 0; u < NV; ++u) S[i][u] *= last;
+        load_dec(next);
         gdr_lds_barrier();
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (w + 4 * c < K / 16) {
-                S[c] *= last;
+        for (int i = 0; i < NC; ++i)
+            if (w + 4 * i < K / 16) {
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    mma(S[c], qt[c][s], lds_frag<P, 16, C>(sB, lr, 32 * s + 8 * lg));
-                    mma(S[c], kt[c][s], lds_frag<P, 16, C>(sE, lr, 32 * s + 8 * lg));
-                }
-                lds_put4<P, 16, KP>(sS, lr, 16 * (w + 4 * c) + 4 * lg, S[c]);
-            }
-        float *dY = a.dY + at * ((int64_t)C * a.V);
+                    const Parts<PK> qt = lds_frag_turned<PK, C, KP>(sQ, 32 * s + 8 * lg, 16 * (w + 4 * i), lane);
+                    const Parts<PK> kt = lds_frag_turned<PK, C, KP>(sK, 32 * s + 8 * lg, 16 * (w + 4 * i), lane);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int r = 16 * w + 4 * lg + e;
-            dY[(int64_t)r * a.V + col] = x[e];
-            if (r < here) st_out(a.dv, a.grad_bf16, ((row + t + r) * a.HV + hv) * a.V + col, E[e]);
-        }
+                    for (int u = 0; u < NV; ++u) {
+                        mma(S[i][u], qt, lds_frag<P, W, C>(sB, 16 * u + lr, 32 * s + 8 * lg));
+                        mma(S[i][u], kt, lds_frag<P, W, C>(sE, 16 * u + lr, 32 * s + 8 * lg));
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < NV; ++u) lds_put4<P, W, KP>(sS, 16 * u + lr, 16 * (w + 4 * i) + 4 * lg, S[i][u]);
+            }
+        float *dY = a.dY + at * ((int64_t)C * a.V) + W * vb;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int u = 0; u < NV; ++u) {
+                dY[(r0 + e) * a.V + lr + 16 * u] = x[u][e];
+                if (r0 + e < len - t) st_out(a.dv, a.grad_bf16, ((row + t + r0 + e) * a.HV + hv) * a.V + W * vb + lr + 16 * u, E[u][e]);
+            }
     }
     if (a.ds0)
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (w + 4 * c < K / 16)
+        for (int i = 0; i < NC; ++i)
+            if (w + 4 * i < K / 16)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) a.ds0[state + (int64_t)(16 * (w + 4 * c) + 4 * lg + e) * a.V + col] = S[c][e];
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int u = 0; u < NV; ++u) a.ds0[state + (int64_t)(16 * (w + 4 * i) + 4 * lg + e) * a.V + lr + 16 * u] = S[i][u][e];
 }
 
-// Eight float32 numbers of a row, zeros where !there.
-__device__ __forceinline__ void row8(float (&x)[8], const float *p, bool there) {
+// Eight float32 numbers at a byte offset from an address of the wave, zeros where !there.
+__device__ __forceinline__ void row8(float (&x)[8], const float *p, unsigned bytes, bool there) {
     f4 u = {}, v = {};
     if (there) {
-        u = *reinterpret_cast<const f4 *>(p);
-        v = *reinterpret_cast<const f4 *>(p + 4);
+        u = at_offset<f4>(p, bytes);
+        v = at_offset<f4>(p, bytes + 16);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -161,196 +213,230 @@ __device__ __forceinline__ void row8(float (&x)[8], const float *p, bool there) 
     }
 }
 
-// One workgroup of four waves per (chunk slot, key head); wave w owns token rows 16w..16w+15.
-// The products over V go through LDS in slices of 32 columns.
-template <typename T, int K>
-__global__ __launch_bounds__(256, 1) void gdr_grads_kernel(const GdrArgs a) {
-    constexpr int PK = gdr_input_parts<T>(), KS = K < 32 ? 1 : K / 32, CT = K / 16, LA = C + 4, LH = C + 1;
+// One workgroup of eight waves per (chunk slot, key head).  Wave (w, h) owns token rows
+// 16w..16w+15 and the h-th half of the channels; of the C x C products, h = 0 has dP and h = 1
+// dA.  The products over V go through LDS in slices of 32 columns, the next slice's rows on
+// their way meanwhile.
+template <typename T, typename D, int K>
+__global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
+    constexpr int PK = gdr_input_parts<T>(), PD = gdr_input_parts<D>(), KS = K < 32 ? 1 : K / 32, CT = (K / 16 + 1) / 2, LA = C + 4, PIECES = (K * 4 + 511) / 512;
     __shared__ __attribute__((aligned(16))) __bf16 sS[P * K * 32], sH[P * K * 32], sV[P * C * 32];
-    __shared__ __attribute__((aligned(16))) float sP[C * LA], sA[C * LA], sT[C * LH], sReads[C], sEnds[C], sKeep[4];
+    __shared__ __attribute__((aligned(16))) float sP[C * LA], sA[C * LA], sT[C * LA], sSum[4][C], sReads[2][C], sEnds[2][C], sKeep[8];
     __shared__ double sG[C];
     const int unit = blockIdx.x, hk = unit % a.HK;
     const int64_t slot = unit / a.HK;
     int64_t row;
     int len;
     if (!gdr_chunk(a, slot, row, len)) return;
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), lr = lane & 15, lg = lane >> 4;
+    const int w8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = w8 & 3, half = w8 >> 2;
     const int V = a.V, slices = (V + 31) / 32;
-    const T *q = static_cast<const T *>(a.q), *k = static_cast<const T *>(a.k);
+    // addresses are one of the wave's and a lane's 32-bit offset; rows behind the end read the last
+    // row, where dO is taken as 0 and beta is 0
+    const T *q = static_cast<const T *>(a.q) + (row * a.HK + hk) * K, *k = static_cast<const T *>(a.k) + (row * a.HK + hk) * K;
+    const unsigned kstep = (unsigned)a.HK * K * sizeof(T), dstep = (unsigned)a.HV * V * sizeof(D);
+    auto clamped = [&](int i) { return (unsigned)(i < len ? i : len - 1); };
+    auto at8 = [](const T *x, unsigned bytes) { return reinterpret_cast<const T *>(reinterpret_cast<const char *>(x) + bytes); };
     const int64_t kq = (slot * a.HK + hk) * (PK * K * C);
 
     f4 dq[CT], dk[CT];
 #pragma unroll
     for (int c = 0; c < CT; ++c) dq[c] = dk[c] = f4{};
     for (int hv = hk * a.group; hv < (hk + 1) * a.group; ++hv) {
+        // the lane is read anew for each head: what follows from it (a hundred offsets) would else be
+        // formed once ahead of the loop and spilled
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        const int lane = tid & 63, lr = lane & 15, lg = lane >> 4, r = 16 * w + lr;
         const int64_t at = slot * a.HV + hv;
         const float *dec = a.dec + at * 4 * C, *h = a.h + at * ((int64_t)K * V), *dh = a.dh + at * ((int64_t)K * V);
         const float *delta = a.delta + at * ((int64_t)C * V), *dY = a.dY + at * ((int64_t)C * V);
+        const char *dO = static_cast<const char *>(a.d_out) + (row * a.HV + hv) * (V * (int64_t)sizeof(D));
         if (tid < C) sG[tid] = a.G[at * C + tid];
-        f4 r1[CT], r2[CT], r3[CT], dP[4], dA[4];
+        f4 r1[CT], r2[CT], r3[CT], pair[4];
 #pragma unroll
         for (int c = 0; c < CT; ++c) r1[c] = r2[c] = r3[c] = f4{};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) dP[c] = dA[c] = f4{};
-        const float beta_r = dec[2 * C + 16 * w + lr];
+        for (int c = 0; c < 4; ++c) pair[c] = f4{};
+        const float beta_r = dec[2 * C + r];
         float keep = 0.f, db = 0.f;
-        for (int sl = 0; sl < slices; ++sl) {
-            const int r = 16 * w + lr, v0 = 32 * sl + 8 * lg;
-            const bool in = v0 < V;
-            float xo[8], xv[8], xe[8];
-            row8(xv, delta + (int64_t)r * V + v0, in);
-            row8(xe, dY + (int64_t)r * V + v0, in);
-            const int64_t ov = ((row + r) * a.HV + hv) * V + v0;
-            if (a.dout_bf16) {
-                const bf16x8 o = in && r < len ? *reinterpret_cast<const bf16x8 *>(static_cast<const __bf16 *>(a.d_out) + ov) : bf16x8{};
+        float xv[8], xe[8], hx[PIECES][8], hy[PIECES][8];
+        Parts<PD> fo;
+        auto load = [&](int sl) {
+            const int v0 = 32 * sl + 8 * lg;
+            row8(xv, delta, (r * V + v0) * 4u, v0 < V);
+            row8(xe, dY, (r * V + v0) * 4u, v0 < V);
+            fo = load8<PD>(reinterpret_cast<const D *>(dO + (r * dstep + v0 * (unsigned)sizeof(D))), v0 < V && r < len);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) xo[i] = (float)o[i];
-            } else {
-                row8(xo, static_cast<const float *>(a.d_out) + ov, in && r < len);
+            for (int j = 0; j < PIECES; ++j) {
+                const int i = tid + 512 * j, c = 32 * sl + i % 4 * 8;
+                const bool there = i < K * 4 && c < V;
+                row8(hx[j], h, (i / 4 * V + c) * 4u, there);
+                row8(hy[j], dh, (i / 4 * V + c) * 4u, there);
             }
+        };
+        load(0);
+        for (int sl = 0; sl < slices; ++sl) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 db += xe[i] * xv[i];
                 xv[i] *= beta_r;
                 xe[i] *= beta_r;
-                xo[i] *= a.scale;
             }
-            const Parts<P> fo = cut8<P>(xo), fv = cut8<P>(xv), fe = cut8<P>(xe);
-            __syncthreads();  // the last slice has been read
+            const Parts<P> fv = cut8<P>(xv), fe = cut8<P>(xe);
+            const Parts<PD> fd = fo;
+            gdr_lds_barrier();  // the last slice has been read
+            if (half == 0)
 #pragma unroll
-            for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x8 *>(sV + p * C * 32 + lds_at<32>(r, 8 * lg)) = fv.v[p];
-            for (int i = tid; i < K * 4; i += 256) {
-                const int ch = i / 4, c = i % 4 * 8;
-                float x[8], y[8];
-                row8(x, h + (int64_t)ch * V + 32 * sl + c, 32 * sl + c < V);
-                row8(y, dh + (int64_t)ch * V + 32 * sl + c, 32 * sl + c < V);
+                for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x8 *>(sV + p * C * 32 + lds_at<32>(r, 8 * lg)) = fv.v[p];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) keep += x[e] * y[e];
-                const Parts<P> fx = cut8<P>(x), fy = cut8<P>(y);
+            for (int j = 0; j < PIECES; ++j) {
+                const int i = tid + 512 * j;
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    *reinterpret_cast<bf16x8 *>(sS + p * K * 32 + lds_at<32>(ch, c)) = fx.v[p];
-                    *reinterpret_cast<bf16x8 *>(sH + p * K * 32 + lds_at<32>(ch, c)) = fy.v[p];
+                for (int e = 0; e < 8; ++e) keep += hx[j][e] * hy[j][e];
+                const Parts<P> fx = cut8<P>(hx[j]), fy = cut8<P>(hy[j]);
+                if (i < K * 4)
+#pragma unroll
+                    for (int p = 0; p < P; ++p) {
+                        *reinterpret_cast<bf16x8 *>(sS + p * K * 32 + lds_at<32>(i / 4, i % 4 * 8)) = fx.v[p];
+                        *reinterpret_cast<bf16x8 *>(sH + p * K * 32 + lds_at<32>(i / 4, i % 4 * 8)) = fy.v[p];
+                    }
+            }
+            if (sl + 1 < slices) load(sl + 1);
+            gdr_lds_barrier();
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+                if (half * CT + c < K / 16) {
+                    const int ch = 16 * (half * CT + c) + lr;
+                    const Parts<P> s = lds_frag<P, K, 32>(sS, ch, 8 * lg), d = lds_frag<P, K, 32>(sH, ch, 8 * lg);
+                    mma(r1[c], fd, s);
+                    mma(r2[c], fe, s);
+                    mma(r3[c], fv, d);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-            }
-            __syncthreads();
-#pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                const Parts<P> s = lds_frag<P, K, 32>(sS, 16 * c + lr, 8 * lg), d = lds_frag<P, K, 32>(sH, 16 * c + lr, 8 * lg);
-                mma(r1[c], fo, s);
-                mma(r2[c], fe, s);
-                mma(r3[c], fv, d);
-            }
 #pragma unroll
             for (int c = 0; c < 4; ++c)
                 if (c <= w) {
                     const Parts<P> f = lds_frag<P, C, 32>(sV, 16 * c + lr, 8 * lg);
-                    mma(dP[c], fo, f);
-                    mma(dA[c], fe, f);
+                    if (half == 0) mma(pair[c], fd, f);
+                    else mma(pair[c], fe, f);
                 }
         }
         // dbeta: a row's eight-column pieces lie in lanes 16 apart
         db += __shfl_xor(db, 16);
         db += __shfl_xor(db, 32);
-        if (lg == 0 && 16 * w + lr < len) a.dbeta[(row + 16 * w + lr) * a.HV + hv] = db;
+        if (half == 0 && lg == 0 && r < len) a.dbeta[(row + r) * a.HV + hv] = db;
 #pragma unroll
         for (int d = 32; d; d /= 2) keep += __shfl_xor(keep, d);
-        if (lane == 0) sKeep[w] = keep;
+        if (lane == 0) sKeep[w8] = keep;
 
-        // the pairs inside the chunk
-        Parts<PK> fk[KS], fq[KS];
-        const bool there = 16 * w + lr < len;
+        // the pairs inside the chunk: dP and its share of H, then dA and its
+        f4 share[4];
+        Parts<PK> f[KS];
+        auto rows = [&](const T *x, int i, int s) {
+            return load8<PK>(at8(x, clamped(i) * kstep + (K < 32 ? lg % 2 * 8 : 32 * s + 8 * lg) * (unsigned)sizeof(T)), K >= 32 || lg < 2);
+        };
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const int64_t o = ((row + 16 * w + lr) * a.HK + hk) * K + 32 * s + 8 * lg;
-            fk[s] = load8<PK>(k + o, there && 32 * s + 8 * lg < K);
-            fq[s] = load8<PK>(q + o, there && 32 * s + 8 * lg < K);
-        }
+        for (int s = 0; s < KS; ++s) f[s] = rows(half == 0 ? q : k, r, s);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            f4 kk = {}, qk = {};
-            if (c <= w)
+            f4 dot = {};
+            if (c <= w) {
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const Parts<PK> f = load8<PK>(k + ((row + 16 * c + lr) * a.HK + hk) * K + 32 * s + 8 * lg, 16 * c + lr < len && 32 * s + 8 * lg < K);
-                    mma(kk, fk[s], f);
-                    mma(qk, fq[s], f);
-                }
+                for (int s = 0; s < KS; ++s) mma(dot, f[s], rows(k, 16 * c + lr, s));
+            }
+            __builtin_amdgcn_sched_barrier(0);  // else the loads of all tiles are in registers at once
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = 16 * w + 4 * lg + e, j = 16 * c + lr;
-                const float d = j <= i ? exp2f((float)(sG[i] - sG[j])) : 0.f;
-                const float p = dP[c][e] * d, m = j < i ? -dA[c][e] * d : 0.f;
-                sP[i * LA + j] = p;
-                sA[i * LA + j] = m;
-                sT[i * LH + j] = p * qk[e] + m * kk[e];
+                const float d = j < i + (half == 0) ? __builtin_amdgcn_exp2f((float)(sG[i] - sG[j])) : 0.f;
+                const float x = c <= w ? pair[c][e] * (half == 0 ? a.scale * d : -d) : 0.f;
+                (half == 0 ? sP : sA)[i * LA + j] = x;
+                share[c][e] = x * dot[e];
+                if (half == 0) sT[i * LA + j] = share[c][e];
             }
         }
         // rows that read S, and rows that reach S'
         const f4 b = *reinterpret_cast<const f4 *>(dec + 16 * w + 4 * lg), end = *reinterpret_cast<const f4 *>(dec + C + 16 * w + 4 * lg);
         f4 reads = {}, ends = {};
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            f4 qc = {}, kc = {};
+        for (int c = 0; c < CT; ++c)
+            if (half * CT + c < K / 16) {
+                f4 qc, kc;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = 16 * w + 4 * lg + e;
-                if (r < len) {
-                    qc[e] = to_f32(q[((row + r) * a.HK + hk) * K + 16 * c + lr]);
-                    kc[e] = to_f32(k[((row + r) * a.HK + hk) * K + 16 * c + lr]);
+                for (int e = 0; e < 4; ++e) {
+                    const unsigned o = clamped(16 * w + 4 * lg + e) * kstep + (16 * (half * CT + c) + lr) * (unsigned)sizeof(T);
+                    qc[e] = to_f32(*at8(q, o));
+                    kc[e] = to_f32(*at8(k, o));
                 }
+                r1[c] *= a.scale * b;
+                r2[c] *= -b;
+                r3[c] *= end;
+                reads += qc * r1[c] + kc * r2[c];
+                ends += kc * r3[c];
+                dq[c] += r1[c];
+                dk[c] += r2[c] + r3[c];
+                __builtin_amdgcn_sched_barrier(0);
             }
-            r1[c] *= b;
-            r2[c] *= -b;
-            r3[c] *= end;
-            reads += qc * r1[c] + kc * r2[c];
-            ends += kc * r3[c];
-            dq[c] += r1[c];
-            dk[c] += r2[c] + r3[c];
-        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            reads[e] = row16_sum(reads[e]);
-            ends[e] = row16_sum(ends[e]);
+            const float x = row16_sum(reads[e]), y = row16_sum(ends[e]);
             if (lr == 0) {
-                sReads[16 * w + 4 * lg + e] = reads[e];
-                sEnds[16 * w + 4 * lg + e] = ends[e];
+                sReads[half][16 * w + 4 * lg + e] = x;
+                sEnds[half][16 * w + 4 * lg + e] = y;
             }
         }
         __syncthreads();
+        if (half == 1)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sT[(16 * w + 4 * lg + e) * LA + 16 * c + lr] += share[c][e];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             float pr[8], ar[8], pc[8], ac[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                pr[i] = sP[(16 * w + lr) * LA + 32 * s + 8 * lg + i];
-                ar[i] = sA[(16 * w + lr) * LA + 32 * s + 8 * lg + i];
-                pc[i] = sP[(32 * s + 8 * lg + i) * LA + 16 * w + lr];
-                ac[i] = sA[(32 * s + 8 * lg + i) * LA + 16 * w + lr] + ar[i];
+                pr[i] = sP[r * LA + 32 * s + 8 * lg + i];
+                ar[i] = sA[r * LA + 32 * s + 8 * lg + i];
+                pc[i] = sP[(32 * s + 8 * lg + i) * LA + r];
+                ac[i] = sA[(32 * s + 8 * lg + i) * LA + r] + ar[i];
             }
             const Parts<P> fpr = cut8<P>(pr), fpc = cut8<P>(pc), fac = cut8<P>(ac);
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                const Parts<PK> kt = load_frag<PK>(a.Kt + kq, c, s, lane), qt = load_frag<PK>(a.Qt + kq, c, s, lane);
-                mma(dq[c], fpr, kt);
-                mma(dk[c], fac, kt);
-                mma(dk[c], fpc, qt);
-            }
+            for (int c = 0; c < CT; ++c)
+                if (half * CT + c < K / 16) {
+                    const Parts<PK> kt = load_frag<PK>(a.Kt + kq, half * CT + c, s, lane), qt = load_frag<PK>(a.Qt + kq, half * CT + c, s, lane);
+                    mma(dq[c], fpr, kt);
+                    mma(dk[c], fac, kt);
+                    mma(dk[c], fpc, qt);
+                }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        // dg: sums of the pairs in each row before t, then over the rows from t on
-        if (tid < C) {
-            float s = 0.f;
-            for (int j = 0; j < C; ++j) {
-                const float x = sT[tid * LH + j];
-                sT[tid * LH + j] = s;
-                s += x;
+        __syncthreads();
+        // dg.  The pairs: R = H U with U_jt = 1 for j < t sums a row's pairs before t, then the rows
+        // from t on are added up; half 0 has t < 32, half 1 the others
+#pragma unroll
+        for (int c2 = 0; c2 < 2; ++c2) {
+            const int c = 2 * half + c2, t = 16 * c + lr;
+            f4 R = {};
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                Parts<1> U;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) U.v[0][i] = (__bf16)(32 * s + 8 * lg + i < t ? 1.f : 0.f);
+                mma(R, cut8<P>(sT + r * LA + 32 * s + 8 * lg), U);
             }
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum += 16 * w + 4 * lg + e >= t ? R[e] : 0.f;
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (lg == 0) sSum[w][t] = sum;
+            __builtin_amdgcn_sched_barrier(0);
         }
         __syncthreads();
         if (tid < C) {
-            float s = 0.f;
-            for (int i = C - 1; i >= tid; --i) s += sT[i * LH + tid];
-            float from = sReads[tid], upto = sEnds[tid];
+            float from = sReads[0][tid] + sReads[1][tid], upto = sEnds[0][tid] + sEnds[1][tid];
             const float own = upto;
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) {
@@ -358,39 +444,46 @@ __global__ __launch_bounds__(256, 1) void gdr_grads_kernel(const GdrArgs a) {
                 if (tid + d < 64) from += x;
                 if (tid >= d) upto += y;
             }
-            const float last = dec[C - 1];
-            if (tid < len) a.dg[(row + tid) * a.HV + hv] = s + from + (upto - own) + last * (sKeep[0] + sKeep[1] + sKeep[2] + sKeep[3]);
+            float kept = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) kept += sKeep[i];
+            const float sum = (sSum[0][tid] + sSum[1][tid]) + (sSum[2][tid] + sSum[3][tid]);
+            if (tid < len) a.dg[(row + tid) * a.HV + hv] = sum + from + (upto - own) + dec[C - 1] * kept;
         }
         __syncthreads();
     }
+    const int lr = threadIdx.x & 15, lg = threadIdx.x >> 4 & 3;
 #pragma unroll
     for (int c = 0; c < CT; ++c)
+        if (half * CT + c < K / 16)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int r = 16 * w + 4 * lg + e;
-            if (r < len) {
-                const int64_t o = ((row + r) * a.HK + hk) * K + 16 * c + lr;
-                st_out(a.dq, a.grad_bf16, o, dq[c][e]);
-                st_out(a.dk, a.grad_bf16, o, dk[c][e]);
+            for (int e = 0; e < 4; ++e) {
+                const int i = 16 * w + 4 * lg + e;
+                if (i < len) {
+                    const int64_t o = ((row + i) * a.HK + hk) * K + 16 * (half * CT + c) + lr;
+                    st_out(a.dq, a.grad_bf16, o, dq[c][e]);
+                    st_out(a.dk, a.grad_bf16, o, dk[c][e]);
+                }
             }
-        }
 }
 
-template <typename T, int K>
+template <typename T, typename D, int K>
 hipError_t launch(const GdrArgs &a, hipStream_t stream) {
-    hipLaunchKernelGGL((gdr_bwd_chain_kernel<T, K>), dim3((unsigned)gdr_pair_blocks(a, a.V / 16)), dim3(256), 0, stream, a);
+    constexpr bool WIDE = sizeof(T) == 2 || K < 128;  // two tiles of float32 rows of 128 channels do not fit the LDS
+    if (WIDE && gdr_column_tiles(a) == 2) hipLaunchKernelGGL((gdr_bwd_chain_kernel<T, D, K, WIDE ? 2 : 1>), dim3((unsigned)gdr_pair_blocks(a, a.V / 32)), dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((gdr_bwd_chain_kernel<T, D, K, 1>), dim3((unsigned)gdr_pair_blocks(a, a.V / 16)), dim3(256), 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((gdr_grads_kernel<T, K>), dim3((unsigned)(a.slots * a.HK)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((gdr_grads_kernel<T, D, K>), dim3((unsigned)(a.slots * a.HK)), dim3(512), 0, stream, a);
     return hipGetLastError();
 }
-template <typename T>
+template <typename T, typename D>
 hipError_t by_width(const GdrArgs &a, int K, hipStream_t stream) {
     switch (K) {
-        case 16: return launch<T, 16>(a, stream);
-        case 32: return launch<T, 32>(a, stream);
-        case 64: return launch<T, 64>(a, stream);
-        case 128: return launch<T, 128>(a, stream);
+        case 16: return launch<T, D, 16>(a, stream);
+        case 32: return launch<T, D, 32>(a, stream);
+        case 64: return launch<T, D, 64>(a, stream);
+        case 128: return launch<T, D, 128>(a, stream);
     }
     return hipErrorNotSupported;
 }
@@ -402,7 +495,8 @@ hipError_t launch_gdr_bwd(const GdrArgs &a, bool fp32, int K, hipStream_t stream
     if (e != hipSuccess) return e;
     e = launch_gdr_fwd_chain(a, fp32, K, true, stream);
     if (e != hipSuccess) return e;
-    return fp32 ? by_width<float>(a, K, stream) : by_width<__bf16>(a, K, stream);
+    if (a.dout_bf16) return fp32 ? by_width<float, __bf16>(a, K, stream) : by_width<__bf16, __bf16>(a, K, stream);
+    return fp32 ? by_width<float, float>(a, K, stream) : by_width<__bf16, float>(a, K, stream);
 }
 
 }  // namespace kda
