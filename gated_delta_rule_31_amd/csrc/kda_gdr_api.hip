@@ -44,14 +44,14 @@ size_t carve_fwd(kda::GdrArgs &a, void *base, bool fp32) {
 }
 
 size_t carve_bwd(kda::GdrArgs &a, void *base, bool fp32, int K) {
-    const int C = kda::GDR_C, parts = 3, input_parts = fp32 ? 3 : 1;
+    const int C = kda::GDR_C, parts = 3, turned_parts = fp32 ? 3 : 0;
     const int64_t units = a.slots * a.HV;
     Carver w{static_cast<char *>(base)};
     w.take(a.M, units * parts * C * C);
     w.take(a.Mt, units * parts * C * C);
     w.take(a.P, units * parts * C * C);
-    w.take(a.Kt, a.slots * a.HK * input_parts * K * C);
-    w.take(a.Qt, a.slots * a.HK * input_parts * K * C);
+    w.take(a.Kt, a.slots * a.HK * turned_parts * K * C);
+    w.take(a.Qt, a.slots * a.HK * turned_parts * K * C);
     w.take(a.dec, units * 4 * C);
     w.take(a.G, units * C);
     w.take(a.h, units * K * a.V);

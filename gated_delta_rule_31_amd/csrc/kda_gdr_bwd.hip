@@ -199,19 +199,25 @@ __global__ __launch_bounds__(256) void gdr_bwd_chain_kernel(const GdrArgs a) {
                     for (int u = 0; u < NV; ++u) a.ds0[state + (int64_t)(16 * (w + 4 * i) + 4 * lg + e) * a.V + lr + 16 * u] = S[i][u][e];
 }
 
-// Eight float32 numbers at a byte offset from an address of the wave, zeros where !there.
-__device__ __forceinline__ void row8(float (&x)[8], const float *p, unsigned bytes, bool there) {
-    f4 u = {}, v = {};
-    if (there) {
-        u = at_offset<f4>(p, bytes);
-        v = at_offset<f4>(p, bytes + 16);
-    }
+// Columns 4 g .. + 3 and 16 + 4 g .. + 3 of a row's 32-column slice, zeros where !there: lanes next
+// to each other read addresses next to each other, and the products over the slice take their
+// operands' columns in this order (staged_at).
+__device__ __forceinline__ f4 load4(const void *p, unsigned bytes, bool there, const float *) { return there ? at_offset<f4>(p, bytes) : f4{}; }
+__device__ __forceinline__ f4 load4(const void *p, unsigned bytes, bool there, const __bf16 *) {
+    typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
+    return there ? __builtin_convertvector(at_offset<bf16x4>(p, bytes), f4) : f4{};
+}
+template <typename D>
+__device__ __forceinline__ void slice8(float (&x)[8], const void *p, unsigned bytes, int g, int columns) {
+    const f4 u = load4(p, bytes + 4 * g * (unsigned)sizeof(D), 4 * g < columns, (const D *)nullptr);
+    const f4 v = load4(p, bytes + (16 + 4 * g) * (unsigned)sizeof(D), 16 + 4 * g < columns, (const D *)nullptr);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         x[i] = u[i];
         x[4 + i] = v[i];
     }
 }
+__device__ __forceinline__ int staged_at(int row, int quad) { return lds_at<32>(row, quad % 4 * 8 + quad / 4 * 4); }
 
 // One workgroup of eight waves per (chunk slot, key head).  Wave (w, h) owns token rows
 // 16w..16w+15 and the h-th half of the channels; of the C x C products, h = 0 has dP and h = 1
@@ -219,9 +225,11 @@ __device__ __forceinline__ void row8(float (&x)[8], const float *p, unsigned byt
 // their way meanwhile.
 template <typename T, typename D, int K>
 __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
-    constexpr int PK = gdr_input_parts<T>(), PD = gdr_input_parts<D>(), KS = K < 32 ? 1 : K / 32, CT = (K / 16 + 1) / 2, LA = C + 4, PIECES = (K * 4 + 511) / 512;
+    constexpr int PK = gdr_input_parts<T>(), PD = gdr_input_parts<D>(), KS = K < 32 ? 1 : K / 32, CT = (K / 16 + 1) / 2, LA = C + 4, KP = K < 32 ? 32 : K, QUADS = K * 8 / 512 ? K * 8 / 512 : 1;
+    constexpr bool KQ = PK == 1;  // k and q rows stay in LDS over the heads of a group where they fit
     __shared__ __attribute__((aligned(16))) __bf16 sS[P * K * 32], sH[P * K * 32], sV[P * C * 32];
     __shared__ __attribute__((aligned(16))) float sP[C * LA], sA[C * LA], sT[C * LA], sSum[4][C], sReads[2][C], sEnds[2][C], sKeep[8];
+    __shared__ __attribute__((aligned(16))) __bf16 sK[KQ ? C * KP : 8], sQ[KQ ? C * KP : 8];
     __shared__ double sG[C];
     const int unit = blockIdx.x, hk = unit % a.HK;
     const int64_t slot = unit / a.HK;
@@ -238,6 +246,33 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
     auto at8 = [](const T *x, unsigned bytes) { return reinterpret_cast<const T *>(reinterpret_cast<const char *>(x) + bytes); };
     const int64_t kq = (slot * a.HK + hk) * (PK * K * C);
 
+    if constexpr (KQ)
+        for (int i = threadIdx.x; i < C * K / 8; i += 512) {
+            const int j = i / (K / 8), c = i % (K / 8) * 8;
+            *reinterpret_cast<bf16x8 *>(sK + lds_at<KP>(j, c)) = load8<1>(at8(k, clamped(j) * kstep + c * (unsigned)sizeof(T)), true).v[0];
+            *reinterpret_cast<bf16x8 *>(sQ + lds_at<KP>(j, c)) = load8<1>(at8(q, clamped(j) * kstep + c * (unsigned)sizeof(T)), true).v[0];
+        }
+    // a slice's rows on their way: corrections, dY and d_out of this lane's row, four columns each of
+    // rows of the two states
+    float xv[8], xe[8], xo[8];
+    f4 hx[QUADS], hy[QUADS];
+    auto load = [&](int hv, int sl, int tid) {
+        const int64_t at = slot * a.HV + hv;
+        const int lane = tid & 63, r = 16 * w + (lane & 15), lg = lane >> 4, left = V - 32 * sl;
+        const char *dO = static_cast<const char *>(a.d_out) + ((row * a.HV + hv) * V + 32 * sl) * (int64_t)sizeof(D);
+        slice8<float>(xv, a.delta + at * ((int64_t)C * V) + 32 * sl, r * V * 4u, lg, left);
+        slice8<float>(xe, a.dY + at * ((int64_t)C * V) + 32 * sl, r * V * 4u, lg, left);
+        slice8<D>(xo, dO, clamped(r) * dstep, lg, r < len ? left : 0);
+        const float *h = a.h + at * ((int64_t)K * V) + 32 * sl, *dh = a.dh + at * ((int64_t)K * V) + 32 * sl;
+#pragma unroll
+        for (int j = 0; j < QUADS; ++j) {
+            const int i = tid + 512 * j;
+            const bool there = i < K * 8 && i % 8 * 4 < left;
+            hx[j] = load4(h, (i / 8 * V + i % 8 * 4) * 4u, there, (const float *)nullptr);
+            hy[j] = load4(dh, (i / 8 * V + i % 8 * 4) * 4u, there, (const float *)nullptr);
+        }
+    };
+    load(hk * a.group, 0, threadIdx.x);
     f4 dq[CT], dk[CT];
 #pragma unroll
     for (int c = 0; c < CT; ++c) dq[c] = dk[c] = f4{};
@@ -248,9 +283,7 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
         asm volatile("" : "+v"(tid));
         const int lane = tid & 63, lr = lane & 15, lg = lane >> 4, r = 16 * w + lr;
         const int64_t at = slot * a.HV + hv;
-        const float *dec = a.dec + at * 4 * C, *h = a.h + at * ((int64_t)K * V), *dh = a.dh + at * ((int64_t)K * V);
-        const float *delta = a.delta + at * ((int64_t)C * V), *dY = a.dY + at * ((int64_t)C * V);
-        const char *dO = static_cast<const char *>(a.d_out) + (row * a.HV + hv) * (V * (int64_t)sizeof(D));
+        const float *dec = a.dec + at * 4 * C;
         if (tid < C) sG[tid] = a.G[at * C + tid];
         f4 r1[CT], r2[CT], r3[CT], pair[4];
 #pragma unroll
@@ -259,22 +292,6 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
         for (int c = 0; c < 4; ++c) pair[c] = f4{};
         const float beta_r = dec[2 * C + r];
         float keep = 0.f, db = 0.f;
-        float xv[8], xe[8], hx[PIECES][8], hy[PIECES][8];
-        Parts<PD> fo;
-        auto load = [&](int sl) {
-            const int v0 = 32 * sl + 8 * lg;
-            row8(xv, delta, (r * V + v0) * 4u, v0 < V);
-            row8(xe, dY, (r * V + v0) * 4u, v0 < V);
-            fo = load8<PD>(reinterpret_cast<const D *>(dO + (r * dstep + v0 * (unsigned)sizeof(D))), v0 < V && r < len);
-#pragma unroll
-            for (int j = 0; j < PIECES; ++j) {
-                const int i = tid + 512 * j, c = 32 * sl + i % 4 * 8;
-                const bool there = i < K * 4 && c < V;
-                row8(hx[j], h, (i / 4 * V + c) * 4u, there);
-                row8(hy[j], dh, (i / 4 * V + c) * 4u, there);
-            }
-        };
-        load(0);
         for (int sl = 0; sl < slices; ++sl) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -283,25 +300,33 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
                 xe[i] *= beta_r;
             }
             const Parts<P> fv = cut8<P>(xv), fe = cut8<P>(xe);
-            const Parts<PD> fd = fo;
+            const Parts<PD> fd = cut8<PD>(xo);
+            unsigned cx[QUADS][2][P], cy[QUADS][2][P];
+#pragma unroll
+            for (int j = 0; j < QUADS; ++j) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) keep += hx[j][e] * hy[j][e];
+                cut2<P>(hx[j][0], hx[j][1], cx[j][0]);
+                cut2<P>(hx[j][2], hx[j][3], cx[j][1]);
+                cut2<P>(hy[j][0], hy[j][1], cy[j][0]);
+                cut2<P>(hy[j][2], hy[j][3], cy[j][1]);
+            }
+            if (sl + 1 < slices) load(hv, sl + 1, tid);
+            else if (hv + 1 < (hk + 1) * a.group) load(hv + 1, 0, tid);
             gdr_lds_barrier();  // the last slice has been read
             if (half == 0)
 #pragma unroll
                 for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x8 *>(sV + p * C * 32 + lds_at<32>(r, 8 * lg)) = fv.v[p];
 #pragma unroll
-            for (int j = 0; j < PIECES; ++j) {
+            for (int j = 0; j < QUADS; ++j) {
                 const int i = tid + 512 * j;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) keep += hx[j][e] * hy[j][e];
-                const Parts<P> fx = cut8<P>(hx[j]), fy = cut8<P>(hy[j]);
-                if (i < K * 4)
+                if (i < K * 8)
 #pragma unroll
                     for (int p = 0; p < P; ++p) {
-                        *reinterpret_cast<bf16x8 *>(sS + p * K * 32 + lds_at<32>(i / 4, i % 4 * 8)) = fx.v[p];
-                        *reinterpret_cast<bf16x8 *>(sH + p * K * 32 + lds_at<32>(i / 4, i % 4 * 8)) = fy.v[p];
+                        *reinterpret_cast<u32x2 *>(sS + p * K * 32 + staged_at(i / 8, i % 8)) = u32x2{cx[j][0][p], cx[j][1][p]};
+                        *reinterpret_cast<u32x2 *>(sH + p * K * 32 + staged_at(i / 8, i % 8)) = u32x2{cy[j][0][p], cy[j][1][p]};
                     }
             }
-            if (sl + 1 < slices) load(sl + 1);
             gdr_lds_barrier();
 #pragma unroll
             for (int c = 0; c < CT; ++c)
@@ -332,17 +357,21 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
         // the pairs inside the chunk: dP and its share of H, then dA and its
         f4 share[4];
         Parts<PK> f[KS];
-        auto rows = [&](const T *x, int i, int s) {
-            return load8<PK>(at8(x, clamped(i) * kstep + (K < 32 ? lg % 2 * 8 : 32 * s + 8 * lg) * (unsigned)sizeof(T)), K >= 32 || lg < 2);
+        auto rows = [&](const T *x, const __bf16 *tile, int i, int s) {
+            if constexpr (KQ) {
+                const Parts<PK> y = lds_frag<PK, C, KP>(tile, i, K < 32 ? lg % 2 * 8 : 32 * s + 8 * lg);
+                return K < 32 && lg > 1 ? Parts<PK>{} : y;
+            } else
+                return load8<PK>(at8(x, clamped(i) * kstep + (K < 32 ? lg % 2 * 8 : 32 * s + 8 * lg) * (unsigned)sizeof(T)), K >= 32 || lg < 2);
         };
 #pragma unroll
-        for (int s = 0; s < KS; ++s) f[s] = rows(half == 0 ? q : k, r, s);
+        for (int s = 0; s < KS; ++s) f[s] = rows(half == 0 ? q : k, half == 0 ? sQ : sK, r, s);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             f4 dot = {};
             if (c <= w) {
 #pragma unroll
-                for (int s = 0; s < KS; ++s) mma(dot, f[s], rows(k, 16 * c + lr, s));
+                for (int s = 0; s < KS; ++s) mma(dot, f[s], rows(k, sK, 16 * c + lr, s));
             }
             __builtin_amdgcn_sched_barrier(0);  // else the loads of all tiles are in registers at once
 #pragma unroll
@@ -364,9 +393,14 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
                 f4 qc, kc;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const unsigned o = clamped(16 * w + 4 * lg + e) * kstep + (16 * (half * CT + c) + lr) * (unsigned)sizeof(T);
-                    qc[e] = to_f32(*at8(q, o));
-                    kc[e] = to_f32(*at8(k, o));
+                    const int i = 16 * w + 4 * lg + e, ch = 16 * (half * CT + c) + lr;
+                    if constexpr (KQ) {
+                        qc[e] = (float)sQ[lds_at<KP>(i, ch)];
+                        kc[e] = (float)sK[lds_at<KP>(i, ch)];
+                    } else {
+                        qc[e] = to_f32(*at8(q, clamped(i) * kstep + ch * (unsigned)sizeof(T)));
+                        kc[e] = to_f32(*at8(k, clamped(i) * kstep + ch * (unsigned)sizeof(T)));
+                    }
                 }
                 r1[c] *= a.scale * b;
                 r2[c] *= -b;
@@ -405,7 +439,14 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
 #pragma unroll
             for (int c = 0; c < CT; ++c)
                 if (half * CT + c < K / 16) {
-                    const Parts<PK> kt = load_frag<PK>(a.Kt + kq, half * CT + c, s, lane), qt = load_frag<PK>(a.Qt + kq, half * CT + c, s, lane);
+                    Parts<PK> kt, qt;
+                    if constexpr (KQ) {
+                        kt = lds_frag_turned<PK, C, KP>(sK, 32 * s + 8 * lg, 16 * (half * CT + c), lane);
+                        qt = lds_frag_turned<PK, C, KP>(sQ, 32 * s + 8 * lg, 16 * (half * CT + c), lane);
+                    } else {
+                        kt = load_frag<PK>(a.Kt + kq, half * CT + c, s, lane);
+                        qt = load_frag<PK>(a.Qt + kq, half * CT + c, s, lane);
+                    }
                     mma(dq[c], fpr, kt);
                     mma(dk[c], fac, kt);
                     mma(dk[c], fpc, qt);

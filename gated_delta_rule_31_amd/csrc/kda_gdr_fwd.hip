@@ -23,7 +23,7 @@ __device__ __forceinline__ Parts<P> column8(const T *m, int ld, int row, int col
 constexpr int BLOCKS = 10, LB = 20;
 __device__ __forceinline__ int block_at(int p, int r) { return (p * (p + 1) / 2 + r) * 16 * LB; }
 
-// One workgroup of four waves per (chunk slot, value head), and in the backward pass one per
+// One workgroup of four waves per (chunk slot, value head), and for float32 gradients one per
 // (chunk slot, key head) that writes K^T and Q^T.  Wave w owns token rows 16w..16w+15 until A
 // is there, then the column blocks w of M.  33 KB of LDS, so that four workgroups share a
 // compute unit: a workgroup mostly waits (for its rows, for substitution and products that
@@ -31,7 +31,8 @@ __device__ __forceinline__ int block_at(int p, int r) { return (p * (p + 1) / 2 
 template <typename T, int K, int P, int PO, bool BWD>
 __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
     constexpr int PK = gdr_input_parts<T>(), KP = K < 32 ? 32 : K, LK = KP + 8, KS = KP / 32, VEC = 16 / sizeof(T);
-    constexpr int WORK = 2 * BLOCKS * 16 * LB * 4, BYTES = BWD && C * LK * (int)sizeof(T) > WORK ? C * LK * (int)sizeof(T) : WORK;
+    constexpr bool TURNED = BWD && PK > 1;  // bf16 rows are turned in LDS where they are used
+    constexpr int WORK = 2 * BLOCKS * 16 * LB * 4, BYTES = TURNED && C * LK * (int)sizeof(T) > WORK ? C * LK * (int)sizeof(T) : WORK;
     __shared__ __attribute__((aligned(16))) char shared[BYTES];
     __shared__ __attribute__((aligned(16))) float sD[4][16 * LB], sP[BWD ? BLOCKS * 16 * LB : 4];
     __shared__ double sG[4][C];
@@ -39,14 +40,14 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
     const T *q = static_cast<const T *>(a.q), *k = static_cast<const T *>(a.k);
     // blocks go to the eight XCDs in turn: a key head's blocks, which read the same rows, are 8
     // apart and share an L2
-    const int i8 = blockIdx.x / 8, each = a.group + BWD, which_head = i8 % each;
+    const int i8 = blockIdx.x / 8, each = a.group + TURNED, which_head = i8 % each;
     const int64_t key = (int64_t)(i8 / each) * 8 + blockIdx.x % 8, slot = key / a.HK;
     const int hk = (int)(key % a.HK);
     if (key >= a.slots * a.HK) return;
     int64_t row;
     int len;
     if (!gdr_chunk(a, slot, row, len)) return;
-    if (BWD && which_head == a.group) {  // K^T, Q^T through LDS
+    if (TURNED && which_head == a.group) {  // K^T, Q^T through LDS
         T *tile = reinterpret_cast<T *>(shared);
         for (int which = 0; which < 2; ++which) {
             const T *from = which ? q : k;
@@ -430,7 +431,7 @@ hipError_t by_width(int K, F f) {
 template <typename T, int P, int PO, bool BWD>
 hipError_t prep(const GdrArgs &a, int K, hipStream_t stream) {
     return by_width(K, [&](auto k) {
-        hipLaunchKernelGGL((gdr_prep_kernel<T, decltype(k)::value, P, PO, BWD>), dim3((unsigned)((a.slots * a.HK + 7) / 8 * 8 * (a.group + BWD))), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((gdr_prep_kernel<T, decltype(k)::value, P, PO, BWD>), dim3((unsigned)((a.slots * a.HK + 7) / 8 * 8 * (a.group + (BWD && sizeof(T) == 4)))), dim3(256), 0, stream, a);
         return hipGetLastError();
     });
 }

@@ -63,8 +63,10 @@ def test_chunk_bwd_refusals(lib, kw, status):
 
 def test_chunk_bwd_workspace(lib):
     size = lambda **kw: kda.gdr_chunk_bwd_workspace_size(**{**dict(dtype=torch.bfloat16, B=1, T=64, HK=2, HV=4, K=16, V=32), **kw})  # noqa: E731
-    # three bf16 parts of M, M^T and P^T; decays (float) and their sums (double); two states and two sets of rows; K^T, Q^T
-    assert size() == 4 * (3 * 3 * 64 * 64 * 2 + 4 * 64 * 4 + 64 * 8 + 2 * 16 * 32 * 4 + 2 * 64 * 32 * 4) + 2 * 2 * 16 * 64 * 2
+    # three bf16 parts of M, M^T and P^T; decays (float) and their sums (double); two states and two sets of rows; with
+    # float32 inputs three parts of K^T and Q^T for a key head
+    assert size() == 4 * (3 * 3 * 64 * 64 * 2 + 4 * 64 * 4 + 64 * 8 + 2 * 16 * 32 * 4 + 2 * 64 * 32 * 4)
+    assert size(dtype=torch.float32) == size() + 2 * 2 * 3 * 16 * 64 * 2
     assert size(T=130, num_seqs=4, varlen=True) == 6 * size() and size(K=24) == 0 and size(T=0, num_seqs=3, varlen=True) == 0
     assert _bwd(lib, V=32, wsz=size() - 1) == 5
 
