@@ -51,8 +51,9 @@ struct GdrArgs {
     // backward
     __bf16 *Mt, *Qt;             // M^T (P holds P^T), Q^T
     double *G;                   // [slots * HV][64], log2 units
-    float *h, *dh;               // [slots * HV][K * V]: state at the chunk's start, gradient at its end
-    float *delta, *dY;           // [slots * HV][64 * V]
+    // by slices of 32 columns (of 16 with V = 16), so that a slice is one run of memory
+    float *h, *dh;               // [slots * HV][slices][K][32]: state at the chunk's start, gradient at its end
+    float *delta, *dY;           // [slots * HV][slices][64][32]
     const void *d_out;           // [rows, HV, V]
     int dout_bf16;
     const float *d_sf;           // [N, HV, K, V] or null
@@ -247,6 +248,11 @@ __device__ __forceinline__ bool gdr_chunk(const GdrArgs &a, int64_t slot, int64_
     len = (int)(l - at < GDR_C ? l - at : GDR_C);
     return true;
 }
+
+// Where a column tile's element stands in the rows of a matrix kept by slices, and the slice's
+// row length.
+__device__ __forceinline__ int gdr_slice_columns(int V) { return V < 32 ? V : 32; }
+__device__ __forceinline__ int64_t gdr_slice_at(int rows, int col, int V) { return (int64_t)(col / 32) * (rows * 32) + (V < 32 ? col : col % 32); }
 
 // The chains' grids: block b of 8 VB ceil(N HV / 8) takes value block b / 8 % VB of pair
 // (b / 8 / VB) 8 + b % 8.  Blocks go to the eight XCDs in turn, so a pair's value blocks, which

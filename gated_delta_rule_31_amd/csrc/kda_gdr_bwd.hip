@@ -104,14 +104,14 @@ __global__ __launch_bounds__(256) void gdr_bwd_chain_kernel(const GdrArgs a) {
     for (int c = chunks - 1; c >= 0; --c) {
         const int next = c > 0 ? c - 1 : 0;
         const int64_t at = (slot + c) * a.HV + hv, t = (int64_t)c * C;
-        float *dh = a.dh + at * ((int64_t)K * a.V) + W * vb;
+        float *dh = a.dh + at * ((int64_t)K * a.V) + gdr_slice_at(K, W * vb, a.V);
 #pragma unroll
         for (int i = 0; i < NC; ++i)
             if (w + 4 * i < K / 16)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
-                    for (int u = 0; u < NV; ++u) dh[(16 * (w + 4 * i) + 4 * lg + e) * a.V + lr + 16 * u] = S[i][u][e];
+                    for (int u = 0; u < NV; ++u) dh[(16 * (w + 4 * i) + 4 * lg + e) * gdr_slice_columns(a.V) + lr + 16 * u] = S[i][u][e];
 #pragma unroll
         for (int i = 0; i < PD; ++i) *reinterpret_cast<bf16x8 *>(sO + i * C * 32 + lds_at<32>(16 * w + lr, 8 * lg)) = o.v[i];
 #pragma unroll
@@ -180,12 +180,12 @@ __global__ __launch_bounds__(256) void gdr_bwd_chain_kernel(const GdrArgs a) {
 #pragma unroll
                 for (int u = 0; u < NV; ++u) lds_put4<P, W, KP>(sS, 16 * u + lr, 16 * (w + 4 * i) + 4 * lg, S[i][u]);
             }
-        float *dY = a.dY + at * ((int64_t)C * a.V) + W * vb;
+        float *dY = a.dY + at * ((int64_t)C * a.V) + gdr_slice_at(C, W * vb, a.V);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
-                dY[(r0 + e) * a.V + lr + 16 * u] = x[u][e];
+                dY[(r0 + e) * gdr_slice_columns(a.V) + lr + 16 * u] = x[u][e];
                 if (r0 + e < len - t) st_out(a.dv, a.grad_bf16, ((row + t + r0 + e) * a.HV + hv) * a.V + W * vb + lr + 16 * u, E[u][e]);
             }
     }
@@ -199,24 +199,27 @@ __global__ __launch_bounds__(256) void gdr_bwd_chain_kernel(const GdrArgs a) {
                     for (int u = 0; u < NV; ++u) a.ds0[state + (int64_t)(16 * (w + 4 * i) + 4 * lg + e) * a.V + lr + 16 * u] = S[i][u][e];
 }
 
-// Columns 4 g .. + 3 and 16 + 4 g .. + 3 of a row's 32-column slice, zeros where !there: lanes next
-// to each other read addresses next to each other, and the products over the slice take their
-// operands' columns in this order (staged_at).
-__device__ __forceinline__ f4 load4(const void *p, unsigned bytes, bool there, const float *) { return there ? at_offset<f4>(p, bytes) : f4{}; }
-__device__ __forceinline__ f4 load4(const void *p, unsigned bytes, bool there, const __bf16 *) {
-    typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
-    return there ? __builtin_convertvector(at_offset<bf16x4>(p, bytes), f4) : f4{};
-}
+// Columns 4 g .. + 3 and 16 + 4 g .. + 3 of a row's 32-column slice: lanes next to each other read
+// addresses next to each other, and the products over the slice take their operands' columns in
+// this order (staged_at).  The loads are unconditional (a slice of 16 columns reads its first
+// quads twice) and nothing is done with what they bring until it is used: a condition or a
+// conversion here would wait for them.
 template <typename D>
-__device__ __forceinline__ void slice8(float (&x)[8], const void *p, unsigned bytes, int g, int columns) {
-    const f4 u = load4(p, bytes + 4 * g * (unsigned)sizeof(D), 4 * g < columns, (const D *)nullptr);
-    const f4 v = load4(p, bytes + (16 + 4 * g) * (unsigned)sizeof(D), 16 + 4 * g < columns, (const D *)nullptr);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[i] = u[i];
-        x[4 + i] = v[i];
+struct Slice8 {
+    typedef __attribute__((ext_vector_type(4))) D d4;
+    d4 x[2];
+    __device__ __forceinline__ void load(const void *p, unsigned bytes, int g, int columns) {
+        x[0] = at_offset<d4>(p, bytes + 4 * g * (unsigned)sizeof(D));
+        x[1] = at_offset<d4>(p, bytes + (4 * g + (columns > 16 ? 16 : 0)) * (unsigned)sizeof(D));
     }
-}
+    __device__ __forceinline__ void get(float (&y)[8], int columns) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y[i] = (float)x[0][i];
+            y[4 + i] = columns > 16 ? (float)x[1][i] : 0.f;
+        }
+    }
+};
 __device__ __forceinline__ int staged_at(int row, int quad) { return lds_at<32>(row, quad % 4 * 8 + quad / 4 * 4); }
 
 // One workgroup of eight waves per (chunk slot, key head).  Wave (w, h) owns token rows
@@ -254,22 +257,25 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
         }
     // a slice's rows on their way: corrections, dY and d_out of this lane's row, four columns each of
     // rows of the two states
-    float xv[8], xe[8], xo[8];
+    Slice8<float> raw_v, raw_e;
+    Slice8<D> raw_o;
+    float raw_beta;
     f4 hx[QUADS], hy[QUADS];
     auto load = [&](int hv, int sl, int tid) {
         const int64_t at = slot * a.HV + hv;
-        const int lane = tid & 63, r = 16 * w + (lane & 15), lg = lane >> 4, left = V - 32 * sl;
+        const int lane = tid & 63, r = 16 * w + (lane & 15), lg = lane >> 4, left = V - 32 * sl, width = gdr_slice_columns(V);
         const char *dO = static_cast<const char *>(a.d_out) + ((row * a.HV + hv) * V + 32 * sl) * (int64_t)sizeof(D);
-        slice8<float>(xv, a.delta + at * ((int64_t)C * V) + 32 * sl, r * V * 4u, lg, left);
-        slice8<float>(xe, a.dY + at * ((int64_t)C * V) + 32 * sl, r * V * 4u, lg, left);
-        slice8<D>(xo, dO, clamped(r) * dstep, lg, r < len ? left : 0);
-        const float *h = a.h + at * ((int64_t)K * V) + 32 * sl, *dh = a.dh + at * ((int64_t)K * V) + 32 * sl;
+        raw_v.load(a.delta + at * ((int64_t)C * V) + C * 32 * sl, r * width * 4u, lg, left);
+        raw_e.load(a.dY + at * ((int64_t)C * V) + C * 32 * sl, r * width * 4u, lg, left);
+        raw_o.load(dO, clamped(r) * dstep, lg, left);
+        raw_beta = at_offset<float>(a.dec + at * 4 * C, (2 * C + r) * 4u);
+        const float *h = a.h + at * ((int64_t)K * V) + K * 32 * sl, *dh = a.dh + at * ((int64_t)K * V) + K * 32 * sl;
 #pragma unroll
         for (int j = 0; j < QUADS; ++j) {
-            const int i = tid + 512 * j;
-            const bool there = i < K * 8 && i % 8 * 4 < left;
-            hx[j] = load4(h, (i / 8 * V + i % 8 * 4) * 4u, there, (const float *)nullptr);
-            hy[j] = load4(dh, (i / 8 * V + i % 8 * 4) * 4u, there, (const float *)nullptr);
+            const int i = (tid + 512 * j) % (K * 8);
+            const unsigned from = (i / 8 * width + i % 8 * 4 % width) * 4u;
+            hx[j] = at_offset<f4>(h, from);
+            hy[j] = at_offset<f4>(dh, from);
         }
     };
     load(hk * a.group, 0, threadIdx.x);
@@ -284,18 +290,24 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
         const int lane = tid & 63, lr = lane & 15, lg = lane >> 4, r = 16 * w + lr;
         const int64_t at = slot * a.HV + hv;
         const float *dec = a.dec + at * 4 * C;
-        if (tid < C) sG[tid] = a.G[at * C + tid];
+        const double g = a.G[at * C + lane];
         f4 r1[CT], r2[CT], r3[CT], pair[4];
 #pragma unroll
         for (int c = 0; c < CT; ++c) r1[c] = r2[c] = r3[c] = f4{};
 #pragma unroll
         for (int c = 0; c < 4; ++c) pair[c] = f4{};
-        const float beta_r = dec[2 * C + r];
         float keep = 0.f, db = 0.f;
         for (int sl = 0; sl < slices; ++sl) {
+            const int left = V - 32 * sl;
+            const float beta_r = raw_beta;
+            float xv[8], xe[8], xo[8];
+            raw_v.get(xv, left);
+            raw_e.get(xe, left);
+            raw_o.get(xo, left);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 db += xe[i] * xv[i];
+                xo[i] = r < len ? xo[i] : 0.f;
                 xv[i] *= beta_r;
                 xe[i] *= beta_r;
             }
@@ -304,6 +316,7 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
             unsigned cx[QUADS][2][P], cy[QUADS][2][P];
 #pragma unroll
             for (int j = 0; j < QUADS; ++j) {
+                if (tid + 512 * j >= K * 8 || (tid + 512 * j) % 8 * 4 >= left) hx[j] = hy[j] = f4{};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) keep += hx[j][e] * hy[j][e];
                 cut2<P>(hx[j][0], hx[j][1], cx[j][0]);
@@ -311,9 +324,12 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
                 cut2<P>(hy[j][0], hy[j][1], cy[j][0]);
                 cut2<P>(hy[j][2], hy[j][3], cy[j][1]);
             }
-            if (sl + 1 < slices) load(hv, sl + 1, tid);
-            else if (hv + 1 < (hk + 1) * a.group) load(hv + 1, 0, tid);
+            // the next slice, or the next head's first (the last head's again at the end): one call
+            // without a condition, or the registers would be copied, and the copy waits
+            __builtin_amdgcn_sched_barrier(0);
+            load(sl + 1 < slices || hv + 1 == (hk + 1) * a.group ? hv : hv + 1, sl + 1 < slices ? sl + 1 : 0, tid);
             gdr_lds_barrier();  // the last slice has been read
+            if (sl == 0 && w8 == 0) sG[lane] = g;
             if (half == 0)
 #pragma unroll
                 for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x8 *>(sV + p * C * 32 + lds_at<32>(r, 8 * lg)) = fv.v[p];

@@ -321,14 +321,14 @@ __global__ __launch_bounds__(256) void gdr_chain_kernel(const GdrArgs a) {
         v = nv;
         load_rows(next);
         if (TRAIN) {
-            float *h = a.h + ((slot + c) * a.HV + hv) * ((int64_t)K * a.V) + W * vb;
+            float *h = a.h + ((slot + c) * a.HV + hv) * ((int64_t)K * a.V) + gdr_slice_at(K, W * vb, a.V);
 #pragma unroll
             for (int i = 0; i < NC; ++i)
                 if (w + 4 * i < K / 16)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
-                        for (int u = 0; u < NV; ++u) h[(16 * (w + 4 * i) + 4 * lg + e) * a.V + lr + 16 * u] = S[i][u][e];
+                        for (int u = 0; u < NV; ++u) h[(16 * (w + 4 * i) + 4 * lg + e) * gdr_slice_columns(a.V) + lr + 16 * u] = S[i][u][e];
         }
         gdr_lds_barrier();
         // K's rows also go to LDS, where the state's update reads them by columns
@@ -384,11 +384,11 @@ __global__ __launch_bounds__(256) void gdr_chain_kernel(const GdrArgs a) {
             }
         const int64_t t = (int64_t)c * C;
         if (TRAIN) {
-            float *d = a.delta + ((slot + c) * a.HV + hv) * ((int64_t)C * a.V) + W * vb;
+            float *d = a.delta + ((slot + c) * a.HV + hv) * ((int64_t)C * a.V) + gdr_slice_at(C, W * vb, a.V);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
-                for (int u = 0; u < NV; ++u) d[(r0 + e) * a.V + lr + 16 * u] = x[u][e];
+                for (int u = 0; u < NV; ++u) d[(r0 + e) * gdr_slice_columns(a.V) + lr + 16 * u] = x[u][e];
         } else {
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
