@@ -238,6 +238,19 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
     const int64_t slot = unit / a.HK;
     int64_t row;
     int len;
+    if (a.cu && slot == a.slots - 1) {  // rows behind the last sequence have no gradient
+        int64_t l, s;
+        gdr_sequence(a, a.N - 1, row, l, s);
+        row += l;
+        const int64_t each = (int64_t)a.group * a.V + 2 * K + 2 * a.group, left = (a.T - row) * each;
+        for (int64_t i = threadIdx.x; i < left; i += 512) {
+            const int64_t t = row + i / each;
+            const int c = (int)(i % each), gv = a.group * a.V, h = c - gv - 2 * K;
+            if (c < gv) st_out(a.dv, a.grad_bf16, (t * a.HV + hk * a.group) * a.V + c, 0.f);
+            else if (h < 0) st_out(c < gv + K ? a.dq : a.dk, a.grad_bf16, (t * a.HK + hk) * K + (c - gv) % K, 0.f);
+            else (h < a.group ? a.dg : a.dbeta)[t * a.HV + hk * a.group + h % a.group] = 0.f;
+        }
+    }
     if (!gdr_chunk(a, slot, row, len)) return;
     const int w8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = w8 & 3, half = w8 >> 2;
     const int V = a.V, slices = (V + 31) / 32;

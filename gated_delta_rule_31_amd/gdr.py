@@ -13,21 +13,51 @@
 """
 from __future__ import annotations
 
+import functools
 from typing import Optional, Tuple
 
 import torch
 
-from . import _check, _dev, _dtype_code, _load, _needs_grad, _ptr, _stream
+from . import _check, _dtype_code, _load, _needs_grad
 
 
 def _input(x: Optional[torch.Tensor], name: str, like: Optional[torch.Tensor] = None, dtype=None) -> Optional[torch.Tensor]:
     """A dense tensor on the device of ``like``, on a 16-byte border (copied to one if need be)."""
-    x = _dev(x, name, dtype)
     if x is None:
         return None
-    if like is not None and x.device != like.device:
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if like is None:
+        if not x.is_cuda:
+            raise ValueError("%s must be on the GPU (got %s)" % (name, x.device))
+    elif x.device != like.device:
         raise ValueError("%s is on %s, but q is on %s" % (name, x.device, like.device))
+    if dtype is not None and x.dtype != dtype:
+        raise ValueError("%s must be %s (got %s)" % (name, dtype, x.dtype))
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError("%s requires grad: the raw kernels do not record autograd; use gated_delta_rule, or call gdr_chunk_bwd yourself" % name)
+    if not x.is_contiguous():
+        x = x.contiguous()
     return x.clone() if x.data_ptr() % 16 else x
+
+
+def _p(x: Optional[torch.Tensor]):
+    return None if x is None else x.data_ptr()
+
+
+# the current stream's handle without a Stream object around it (2 us of a 14 us call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def _call(fn, device: torch.device, *args) -> None:
+    """A C entry point on the device's current stream; the device is made current where it is not."""
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, _raw_stream(device.index))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _raw_stream(device.index))
+    if st:
+        _check(fn.__name__, st)
 
 
 def _output(x: torch.Tensor, name: str, shape, dtype, device) -> torch.Tensor:
@@ -70,11 +100,17 @@ def _chunk_inputs(q, k, v, g, beta, initial_state, cu_seqlens):
     return q, k, v, g, beta, initial_state, cu_seqlens, (B, T, HK, HV, K, V, N)
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace_size(fn: str, *shape: int) -> int:
+    """A workspace's size by its shape alone."""
+    return int(getattr(_load(), fn)(*shape))
+
+
 def gdr_chunk_fwd_workspace_size(dtype: torch.dtype, B: int, T: int, HK: int, HV: int, K: int, V: int, num_seqs: int = 0,
                                  varlen: bool = False) -> int:
     """Bytes of device workspace ``gdr_chunk_fwd`` needs for this shape (0: unsupported or empty)."""
-    return int(_load().kda_gdr_chunk_fwd_workspace_size(_dtype_code(dtype), int(B), int(T), int(num_seqs), 1 if varlen else 0, int(HK),
-                                                        int(HV), int(K), int(V)))
+    return _workspace_size("kda_gdr_chunk_fwd_workspace_size", _dtype_code(dtype), int(B), int(T), int(num_seqs), 1 if varlen else 0, int(HK),
+                           int(HV), int(K), int(V))
 
 
 def gdr_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
@@ -87,30 +123,28 @@ def gdr_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     [B,T,HV] float32; initial_state [N,HV,K,V] float32 or None (zeros); cu_seqlens int32 [N+1]
     (B == 1) or None.  Returns (out [B,T,HV,V], final_state [N,HV,K,V] or None).  ``final_state``
     may be passed in (it may be ``initial_state``).  Rows of ``out`` behind the last packed
-    sequence are left as they were (zeros in an ``out`` made here)."""
+    sequence are left as they were (unset in an ``out`` made here)."""
     q, k, v, g, beta, initial_state, cu_seqlens, (B, T, HK, HV, K, V, N) = _chunk_inputs(q, k, v, g, beta, initial_state, cu_seqlens)
     od, dev = out_dtype or v.dtype, q.device
     if out is None:
-        out = (torch.empty if cu_seqlens is None else torch.zeros)((B, T, HV, V), dtype=od, device=dev)
-    out = _output(out, "out", (B, T, HV, V), od, dev)
-    if output_final_state and final_state is None:
-        final_state = torch.empty((N, HV, K, V), dtype=torch.float32, device=dev)
-    if final_state is not None:
+        out = torch.empty((B, T, HV, V), dtype=od, device=dev)
+    else:
+        out = _output(out, "out", (B, T, HV, V), od, dev)
+    if final_state is None:
+        final_state = torch.empty((N, HV, K, V), dtype=torch.float32, device=dev) if output_final_state else None
+    else:
         final_state = _output(final_state, "final_state", (N, HV, K, V), torch.float32, dev)
     workspace = _workspace(workspace, gdr_chunk_fwd_workspace_size(q.dtype, B, T, HK, HV, K, V, N, cu_seqlens is not None), dev)
-    with torch.cuda.device(dev):
-        st = _load().kda_gdr_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q.dtype), _ptr(g), _ptr(beta), _ptr(initial_state),
-                                       _ptr(final_state), _ptr(cu_seqlens), N, B, T, HK, HV, K, V, float(scale), _ptr(out),
-                                       _dtype_code(od), _ptr(workspace), workspace.numel(), _stream(q))
-    _check("kda_gdr_chunk_fwd", st)
+    _call(_load().kda_gdr_chunk_fwd, dev, _p(q), _p(k), _p(v), _dtype_code(q.dtype), _p(g), _p(beta), _p(initial_state), _p(final_state),
+          _p(cu_seqlens), N, B, T, HK, HV, K, V, scale, _p(out), _dtype_code(od), _p(workspace), workspace.numel())
     return out, final_state
 
 
 def gdr_chunk_bwd_workspace_size(dtype: torch.dtype, B: int, T: int, HK: int, HV: int, K: int, V: int, num_seqs: int = 0,
                                  varlen: bool = False) -> int:
     """Bytes of device workspace ``gdr_chunk_bwd`` needs for this shape (0: unsupported or empty)."""
-    return int(_load().kda_gdr_chunk_bwd_workspace_size(_dtype_code(dtype), int(B), int(T), int(num_seqs), 1 if varlen else 0, int(HK),
-                                                        int(HV), int(K), int(V)))
+    return _workspace_size("kda_gdr_chunk_bwd_workspace_size", _dtype_code(dtype), int(B), int(T), int(num_seqs), 1 if varlen else 0, int(HK),
+                           int(HV), int(K), int(V))
 
 
 def gdr_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, d_out: torch.Tensor,
@@ -130,17 +164,13 @@ def gdr_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     if d_final_state is not None and d_final_state.shape != (N, HV, K, V):
         raise ValueError("d_final_state must be %s" % [N, HV, K, V])
     gd, dev = grad_dtype or q.dtype, q.device
-    new = torch.empty if cu_seqlens is None else torch.zeros
-    dq, dk, dv = (new(x.shape, dtype=gd, device=dev) for x in (q, k, v))
-    dg, dbeta = (new(g.shape, dtype=torch.float32, device=dev) for _ in range(2))
+    dq, dk, dv = (torch.empty(x.shape, dtype=gd, device=dev) for x in (q, k, v))
+    dg, dbeta = (torch.empty(g.shape, dtype=torch.float32, device=dev) for _ in range(2))
     ds0 = torch.empty((N, HV, K, V), dtype=torch.float32, device=dev) if want_d_initial_state else None
     workspace = _workspace(workspace, gdr_chunk_bwd_workspace_size(q.dtype, B, T, HK, HV, K, V, N, cu_seqlens is not None), dev)
-    with torch.cuda.device(dev):
-        st = _load().kda_gdr_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q.dtype), _ptr(g), _ptr(beta), _ptr(initial_state),
-                                       _ptr(cu_seqlens), N, B, T, HK, HV, K, V, float(scale), _ptr(d_out), _dtype_code(d_out.dtype),
-                                       _ptr(d_final_state), _ptr(dq), _ptr(dk), _ptr(dv), _dtype_code(gd), _ptr(dg), _ptr(dbeta),
-                                       _ptr(ds0), _ptr(workspace), workspace.numel(), _stream(q))
-    _check("kda_gdr_chunk_bwd", st)
+    _call(_load().kda_gdr_chunk_bwd, dev, _p(q), _p(k), _p(v), _dtype_code(q.dtype), _p(g), _p(beta), _p(initial_state), _p(cu_seqlens), N, B,
+          T, HK, HV, K, V, scale, _p(d_out), _dtype_code(d_out.dtype), _p(d_final_state), _p(dq), _p(dk), _p(dv), _dtype_code(gd), _p(dg),
+          _p(dbeta), _p(ds0), _p(workspace), workspace.numel())
     return dq, dk, dv, dg, dbeta, ds0
 
 
@@ -149,7 +179,8 @@ class _GatedDeltaRuleFn(torch.autograd.Function):
     def forward(ctx, q, k, v, g, beta, initial_state, cu_seqlens, scale):
         d = lambda x: None if x is None else x.detach()  # noqa: E731
         with torch.no_grad():
-            out, fin = gdr_chunk_fwd(d(q), d(k), d(v), d(g), d(beta), initial_state=d(initial_state), cu_seqlens=cu_seqlens, scale=scale)
+            out = None if cu_seqlens is None else torch.zeros_like(v, memory_format=torch.contiguous_format)
+            out, fin = gdr_chunk_fwd(d(q), d(k), d(v), d(g), d(beta), initial_state=d(initial_state), cu_seqlens=cu_seqlens, scale=scale, out=out)
         ctx.save_for_backward(q, k, v, g, beta, initial_state, cu_seqlens)
         ctx.scale = scale
         ctx.set_materialize_grads(False)
@@ -170,7 +201,8 @@ class _GatedDeltaRuleFn(torch.autograd.Function):
 def gated_delta_rule(q, k, v, g, beta, initial_state=None, cu_seqlens=None, scale: float = 1.0):
     """``gdr_chunk_fwd`` as a function of its inputs: (out in the inputs' dtype, final_state), recorded
     for autograd when any of q, k, v, g, beta or initial_state requires grad (through
-    ``gdr_chunk_bwd``)."""
+    ``gdr_chunk_bwd``).  Rows of out behind the last packed sequence are zeros where the call is
+    recorded."""
     if _needs_grad(q, k, v, g, beta, initial_state):
         return _GatedDeltaRuleFn.apply(q, k, v, g, beta, initial_state, cu_seqlens, float(scale))
     return gdr_chunk_fwd(q, k, v, g, beta, initial_state=initial_state, cu_seqlens=cu_seqlens, scale=scale)
@@ -196,7 +228,7 @@ def gdr_recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: tor
         raise TypeError("q must be a torch.Tensor")
     k, v = _input(k, "k", q, q.dtype), _input(v, "v", q, q.dtype)
     g, beta = _input(g, "g", q, torch.float32), _input(beta, "beta", q, torch.float32)
-    slots, start, lengths = (_input(x, n, q, torch.int32) for x, n in ((slots, "slots"), (start, "start"), (lengths, "lengths")))
+    slots, start, lengths = _input(slots, "slots", q, torch.int32), _input(start, "start", q, torch.int32), _input(lengths, "lengths", q, torch.int32)
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k must be [B, S, HK, K] and v [B, S, HV, V]")
     B, S, HK, K = q.shape
@@ -215,17 +247,15 @@ def gdr_recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: tor
             raise ValueError("slots must be [B], [B, 1] or [B, S]")
     if slots is None and (start is not None or pool < B):
         raise ValueError("without slots every request has a state of its own, states[b], and starts from it")
-    if any(x is not None and x.shape != (B,) for x in (start, lengths)):
+    if (start is not None and start.shape != (B,)) or (lengths is not None and lengths.shape != (B,)):
         raise ValueError("start and lengths must be [B]")
     od = out_dtype or v.dtype
     if out is None:
         out = (torch.empty if lengths is None else torch.zeros)((B, S, HV, V), dtype=od, device=dev)
-    out = _output(out, "out", (B, S, HV, V), od, dev)
-    with torch.cuda.device(dev):
-        st = _load().kda_gdr_recurrent_step(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q.dtype), _ptr(g), 1 if g.dim() == 4 else 0, _ptr(beta),
-                                            _ptr(states), pool, _ptr(slots), cols, _ptr(start), _ptr(lengths), B, S, HK, HV, K, V,
-                                            float(scale), _ptr(out), _dtype_code(od), _stream(q))
-    _check("kda_gdr_recurrent_step", st)
+    else:
+        out = _output(out, "out", (B, S, HV, V), od, dev)
+    _call(_load().kda_gdr_recurrent_step, dev, _p(q), _p(k), _p(v), _dtype_code(q.dtype), _p(g), 1 if g.dim() == 4 else 0, _p(beta), _p(states),
+          pool, _p(slots), cols, _p(start), _p(lengths), B, S, HK, HV, K, V, scale, _p(out), _dtype_code(od))
     return out
 
 
@@ -255,9 +285,7 @@ def draft_verify(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uniform
     dev = p.device
     tokens = torch.empty((B, D + 1), dtype=torch.int32, device=dev)
     accepted = torch.empty((B,), dtype=torch.int32, device=dev)
-    workspace = _workspace(None, int(_load().kda_draft_verify_workspace_size(B, vocab)), dev)
-    with torch.cuda.device(dev):
-        st = _load().kda_draft_verify(_ptr(p), _ptr(x), _ptr(q), _ptr(u), _ptr(lengths), B, D, vocab, _ptr(tokens), _ptr(accepted),
-                                      _ptr(workspace), workspace.numel(), _stream(p))
-    _check("kda_draft_verify", st)
+    workspace = _workspace(None, _workspace_size("kda_draft_verify_workspace_size", B, vocab), dev)
+    _call(_load().kda_draft_verify, dev, _p(p), _p(x), _p(q), _p(u), _p(lengths), B, D, vocab, _p(tokens), _p(accepted), _p(workspace),
+          workspace.numel())
     return tokens, accepted

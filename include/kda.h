@@ -382,7 +382,7 @@ kda_status kda_gdr_chunk_fwd(const void *q, const void *k, const void *v, kda_dt
  *   d_initial_state [N, HV, K, V] float32, or NULL (not wanted); with initial_state NULL it is
  *          the gradient at the zero state
  * from d_out [B, T, HV, V] in dout_dtype and d_final_state [N, HV, K, V] float32 or NULL (zeros).
- * Rows behind the last packed sequence are left as they were.  The forward is computed again,
+ * Rows behind the last packed sequence get zeros.  The forward is computed again,
  * chunk by chunk; its intermediates live in the workspace (about 0.27 MB per chunk and value
  * head at K = V = 128), scratch as in the forward.  Float32 precision throughout (computed
  * operands enter the matrix cores with 24 mantissa bits).  A token with g = -inf gets dg = 0.

@@ -150,8 +150,10 @@ def test_fwd_empty():
     out, fin = kda.gdr_chunk_fwd(z(2, 0, 2, 16), z(2, 0, 2, 16), z(2, 0, 4, 32), z(2, 0, 4), z(2, 0, 4), initial_state=s0)
     assert out.shape == (2, 0, 4, 32) and torch.equal(fin, s0)
     cu = torch.zeros(3, dtype=torch.int32, device="cuda")
-    out, fin = kda.gdr_chunk_fwd(z(1, 9, 2, 16), z(1, 9, 2, 16), z(1, 9, 4, 32), z(1, 9, 4), z(1, 9, 4), cu_seqlens=cu)
-    assert not fin.any() and not out.any()
+    out, fin = kda.gdr_chunk_fwd(z(1, 9, 2, 16), z(1, 9, 2, 16), z(1, 9, 4, 32), z(1, 9, 4), z(1, 9, 4), cu_seqlens=cu, out=z(1, 9, 4, 32) + 3)
+    assert not fin.any() and bool((out == 3).all())
+    grads = kda.gdr_chunk_bwd(z(1, 9, 2, 16), z(1, 9, 2, 16), z(1, 9, 4, 32), z(1, 9, 4), z(1, 9, 4), z(1, 9, 4, 32) + 1, cu_seqlens=cu, d_final_state=s0)
+    assert not any(x.any() for x in grads[:5]) and torch.equal(grads[5], s0)
 
 
 def test_fwd_graph_and_other_stream():
