@@ -16,6 +16,8 @@ bool width_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 bool type_ok(kda_dtype t) { return t == KDA_F32 || t == KDA_BF16; }
 bool aligned(const void *p) { return (uintptr_t)p % 16 == 0; }
 
+constexpr int64_t MAX_UNITS = 1 << 22;  // (chunk slot, value head) or (sequence, value head, column tile)
+
 int64_t chunk_slots(int B, int64_t T, int num_seqs, bool varlen) {
     const int64_t C = kda::GDR_C;
     return varlen ? T / C + num_seqs : B * ((T + C - 1) / C);
@@ -71,7 +73,7 @@ kda_status chunk_args(kda::GdrArgs &a, const void *q, const void *k, const void 
     if (!heads_ok(HK, HV)) return KDA_ERR_BAD_SHAPE;
     if (!type_ok(in_dtype)) return KDA_ERR_BAD_DTYPE;
     if (!width_ok(K) || !width_ok(V)) return KDA_ERR_UNSUPPORTED;
-    if (cu && (B != 1 || num_seqs < 0)) return KDA_ERR_BAD_ARGUMENT;
+    if (cu && (B != 1 || num_seqs < 0 || (num_seqs == 0 && T > 0))) return KDA_ERR_BAD_ARGUMENT;
     const int64_t N = cu ? num_seqs : B;
     a = kda::GdrArgs{};
     a.q = q;
@@ -94,8 +96,8 @@ kda_status chunk_args(kda::GdrArgs &a, const void *q, const void *k, const void 
     a.chunks = (int)((T + kda::GDR_C - 1) / kda::GDR_C);
     // a chunk's rows are addressed by 32-bit offsets
     if (HK > 65535 || HV > 65535) return KDA_ERR_UNSUPPORTED;
-    // (chunk slot, value head) and (sequence, value head, column block) index grids as int
-    if (a.slots > (int64_t)INT32_MAX / HV / 2 || N > (int64_t)INT32_MAX / HV / (V / 16) - 8) return KDA_ERR_UNSUPPORTED;
+    // a grid has fewer than 2^32 threads
+    if (a.slots > MAX_UNITS / HV || N > MAX_UNITS / HV / (V / 16)) return KDA_ERR_UNSUPPORTED;
     if (!q || !k || !v || !g || !beta) return KDA_ERR_NULL_POINTER;
     return KDA_OK;
 }
@@ -108,7 +110,7 @@ bool size_args(kda::GdrArgs &a, kda_dtype in_dtype, int B, int64_t T, int num_se
     a.HV = HV;
     a.V = V;
     a.slots = T == 0 ? 0 : chunk_slots(B, T, num_seqs, varlen != 0);
-    return a.slots <= (int64_t)INT32_MAX / HV / 2;
+    return a.slots <= MAX_UNITS / HV;
 }
 
 }  // namespace
@@ -215,7 +217,8 @@ kda_status kda_gdr_recurrent_step(const void *q, const void *k, const void *v, k
     if (B == 0 || S == 0) return KDA_OK;
     if (slot_cols != 1 && slot_cols != S) return KDA_ERR_BAD_SHAPE;
     if (!slots && (slot_cols != 1 || start || pool < B)) return KDA_ERR_BAD_ARGUMENT;
-    if (B > INT32_MAX / HV / (V / 16)) return KDA_ERR_UNSUPPORTED;
+    if (start && slot_cols != S) return KDA_ERR_BAD_ARGUMENT;
+    if (B > (1 << 24) / HV / (V / 16)) return KDA_ERR_UNSUPPORTED;  // a grid has fewer than 2^32 threads
     if (!q || !k || !v || !g || !beta || !states || !out) return KDA_ERR_NULL_POINTER;
     const void *ins[] = {q, k, v, g, beta, slots, start, lengths};
     for (const void *p : ins)
@@ -261,7 +264,7 @@ kda_status kda_draft_verify(const float *target_probs, const int32_t *draft_toke
     // the whole of a row's weights has to fit 64 bits; the second kernel's threads sum the tiles
     if (vocab > (1 << 19) || D == INT32_MAX) return KDA_ERR_UNSUPPORTED;
     if (B == 0) return KDA_OK;
-    if (B > INT32_MAX / 512) return KDA_ERR_UNSUPPORTED;
+    if (B > (1 << 24) / ((vocab + kda::DRAFT_TILE - 1) / kda::DRAFT_TILE)) return KDA_ERR_UNSUPPORTED;  // likewise
     if (!target_probs || (D && !draft_tokens) || !uniforms || !tokens || !accepted || !workspace) return KDA_ERR_NULL_POINTER;
     const void *ins[] = {target_probs, draft_tokens, draft_probs, uniforms, lengths}, *outs[] = {tokens, accepted, workspace};
     for (int i = 0; i < 3; ++i) {

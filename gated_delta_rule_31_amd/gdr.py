@@ -187,6 +187,7 @@ class _GatedDeltaRuleFn(torch.autograd.Function):
         return out, fin
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, d_out, d_fin):
         q, k, v, g, beta, s0, cu = ctx.saved_tensors
         if d_out is None:
@@ -218,7 +219,8 @@ def gdr_recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: tor
 
     slots int32 [B, S]: the state after each token goes to a slot of its own (a slot outside the
     pool keeps none), and a request starts from ``slots[b, start[b]]``, ``start`` int32 [B] being
-    the number of drafts that held (None: column 0).  slots [B] or [B, 1]: a request starts from
+    the number of drafts that held in the round before (None: column 0); rounds that follow one
+    another keep one table and one S, and give fewer tokens by ``lengths``.  slots [B] or [B, 1]: a request starts from
     its slot and leaves the state after its last token there; None: slot b.  A slot that one
     request writes must not be named by another.  lengths int32 [B]: tokens of each request
     (None: S); rows of ``out`` behind them are left as they were (zeros in an ``out`` made here).
@@ -247,6 +249,8 @@ def gdr_recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: tor
             raise ValueError("slots must be [B], [B, 1] or [B, S]")
     if slots is None and (start is not None or pool < B):
         raise ValueError("without slots every request has a state of its own, states[b], and starts from it")
+    if start is not None and cols != S:
+        raise ValueError("start names a column of slots [B, S]")
     if (start is not None and start.shape != (B,)) or (lengths is not None and lengths.shape != (B,)):
         raise ValueError("start and lengths must be [B]")
     od = out_dtype or v.dtype

@@ -409,7 +409,9 @@ kda_status kda_gdr_chunk_bwd(const void *q, const void *k, const void *v, kda_dt
  *          is written to slot slots[b, t]; with slot_cols == 1 the state after the last token
  *          to slots[b, 0].  NULL: slot b (slot_cols must be 1, pool >= B).
  *   start  [B] int32 or NULL: request b starts from the state in slots[b, start[b]] (NULL: from
- *          slots[b, 0]) -- after a round of drafting, the number of drafts that held.
+ *          slots[b, 0]) -- after a round of drafting, the number of drafts that held.  Only with
+ *          slot_cols == S.  The columns are this call's, so rounds that follow one another keep
+ *          one table and one S, and give fewer tokens by `lengths`.
  *   lengths [B] int32 or NULL: tokens of request b, 0..S (brought into that range; NULL: S).
  *          Rows of `out` and slots behind a request's last token are left as they were.
  * A slot outside 0..pool-1 holds no state: nothing is written to it, and a request that starts

@@ -25,7 +25,7 @@ def _fwd(lib, q=0x1000, k=0x2000, v=0x3000, dt=1, g=0x4000, beta=0x5000, s0=None
 @pytest.mark.parametrize("kw,status", [
     (dict(K=24), 4), (dict(V=256), 4), (dict(HK=0), 2), (dict(HV=3), 2), (dict(HK=4, HV=2), 2), (dict(T=-1), 2), (dict(B=-1), 2),
     (dict(dt=5), 3), (dict(od=7), 3), (dict(q=None), 1), (dict(g=None), 1), (dict(out=None), 1), (dict(ws=None), 1),
-    (dict(cu=0x900, B=2, N=2), 5), (dict(cu=0x900, N=-1), 5), (dict(out=0x1000), 6), (dict(sf=0x3000), 6), (dict(ws=0x1000), 6),
+    (dict(cu=0x900, B=2, N=2), 5), (dict(cu=0x900, N=-1), 5), (dict(cu=0x900, N=0), 5), (dict(HK=1, HV=65536), 4), (dict(B=1 << 22), 4), (dict(out=0x1000), 6), (dict(sf=0x3000), 6), (dict(ws=0x1000), 6),
     (dict(sf=0x6000), 6), (dict(ws=0x6000), 6), (dict(q=0x1004), 5), (dict(out=0x6008), 5), (dict(ws=0x7004), 5), (dict(s0=0x8004), 5),
     (dict(wsz=64), 5), (dict(T=1 << 40), 4),
     (dict(T=0, q=None, out=None, ws=None), 0), (dict(B=0, q=None, out=None, ws=None), 0),
@@ -78,7 +78,7 @@ def _step(lib, q=0x1000, k=0x2000, v=0x3000, dt=1, g=0x4000, ch=0, beta=0x5000, 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(K=48), 4), (dict(HV=5), 2), (dict(S=-1), 2), (dict(pool=-1), 2), (dict(dt=3), 3), (dict(od=3), 3), (dict(cols=2), 2),
-    (dict(slots=None, cols=3), 5), (dict(slots=None, cols=1, start=0x800), 5), (dict(slots=None, cols=1, pool=1), 5),
+    (dict(slots=None, cols=3), 5), (dict(slots=None, cols=1, start=0x800), 5), (dict(slots=None, cols=1, pool=1), 5), (dict(cols=1, start=0x800), 5),
     (dict(st=None), 1), (dict(beta=None), 1), (dict(out=None), 1), (dict(out=0x3000), 6), (dict(st=0x1000), 6), (dict(out=0x6000), 6),
     (dict(st=0x6004), 5), (dict(g=0x4004, ch=1), 5), (dict(B=1 << 30), 4), (dict(B=0, q=None, st=None), 0), (dict(S=0, q=None, st=None), 0),
 ])
@@ -93,7 +93,7 @@ def _verify(lib, p=0x1000, x=0x2000, q=0x3000, u=0x4000, lens=None, B=2, D=3, vo
 @pytest.mark.parametrize("kw,status", [
     (dict(D=-1), 2), (dict(vocab=0), 2), (dict(vocab=(1 << 19) + 1), 4), (dict(B=1 << 30), 4), (dict(p=None), 1), (dict(x=None), 1),
     (dict(u=None), 1), (dict(t=None), 1), (dict(ws=None), 1), (dict(t=0x2000), 6), (dict(a=0x5000), 6), (dict(ws=0x1000), 6),
-    (dict(ws=0x7004), 5), (dict(wsz=31), 5), (dict(B=0, p=None), 0),
+    (dict(ws=0x7004), 5), (dict(wsz=31), 5), (dict(B=1 << 20, vocab=1 << 19), 4), (dict(B=0, p=None), 0),
 ])
 def test_verify_refusals(lib, kw, status):
     assert _verify(lib, **kw) == status

@@ -70,7 +70,7 @@ def test_fwd_lengths(dtype, T):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("lens", [[70, 0, 1, 64, 130], [0, 0, 3], [1, 1, 1, 1], [65, 63, 0], [200]])
+@pytest.mark.parametrize("lens", [[70, 0, 1, 64, 130], [0, 0, 3], [1, 1, 1, 1], [65, 63, 0], [200], [5, 0, 66] * 23, [3, 7, 1, 64] * 16])
 def test_fwd_packed(dtype, lens):
     i = ref.make(1, sum(lens), 2, 4, 32, 48 - 16, dtype, seed=sum(lens), seqlens=lens)
     out, final = _fwd(i, 0.5, out_dtype=torch.float32)
@@ -154,6 +154,35 @@ def test_fwd_empty():
     assert not fin.any() and bool((out == 3).all())
     grads = kda.gdr_chunk_bwd(z(1, 9, 2, 16), z(1, 9, 2, 16), z(1, 9, 4, 32), z(1, 9, 4), z(1, 9, 4), z(1, 9, 4, 32) + 1, cu_seqlens=cu, d_final_state=s0)
     assert not any(x.any() for x in grads[:5]) and torch.equal(grads[5], s0)
+
+
+@pytest.mark.parametrize("HV", [5, 32, 136])
+def test_fwd_head_counts(HV):
+    """Odd numbers of heads, and enough of them for two column tiles a workgroup (from 2 x 256 on)."""
+    i = ref.make(1, 70, 1 if HV == 5 else HV // 4, HV, 32, 64, torch.bfloat16, seed=HV)
+    out, final = _fwd(i, out_dtype=torch.float32)
+    _check(out, final, i, 1.0, torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype,K", [(torch.bfloat16, 128), (torch.bfloat16, 16), (torch.float32, 128), (torch.float32, 64)])
+def test_bwd_two_column_tiles(dtype, K):
+    _bwd_check(ref.make(1, 70, 33, 132, K, 64, dtype, seed=K), 3, 0.5, dtype)
+
+
+def test_fwd_two_streams_at_once():
+    """Calls that overlap in time, each with the workspace that it takes itself."""
+    cases = [_gpu(ref.make(1, 300 + 50 * n, 2, 4, 64, 64, torch.bfloat16, seed=40 + n)) for n in range(4)]
+    args = [[d[n] for n in ("q", "k", "v", "g", "beta")] for d in cases]
+    want = [kda.gdr_chunk_fwd(*x) for x in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for _ in range(5):
+        for x, st in zip(args, streams):
+            with torch.cuda.stream(st):
+                got.append(kda.gdr_chunk_fwd(*x))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i % 4][0]) and torch.equal(f, want[i % 4][1]) for i, (o, f) in enumerate(got))
 
 
 def test_fwd_graph_and_other_stream():
@@ -389,6 +418,45 @@ def test_step_slots_outside_the_pool_and_named_twice():
     i["slots"] = torch.tensor([[-1, 0, 1], [2, 2, 2], [99, 3, -7], [4, 5, 4]], dtype=torch.int32)
     _step_check(i, torch.tensor([0, 1, 0, 3], dtype=torch.int32), torch.tensor([3, 3, 9, -2], dtype=torch.int32), 1.0, torch.float32)
     _step_check(i, torch.tensor([2, -1, 1, 0], dtype=torch.int32), None, 1.0, torch.float32)
+
+
+def test_step_and_verify_in_a_graph():
+    """One round, captured: drafts in, states and the next start out; replayed with new inputs in place."""
+    i = _step_case(3, 3, 2, 4, 32, 32, torch.bfloat16, 14)
+    d = _gpu(i)
+    gen = torch.Generator().manual_seed(15)
+    p, x, u = _probs(gen, 3, 3, 500).cuda(), torch.zeros(3, 2, dtype=torch.int32, device="cuda"), torch.rand(3, 3, generator=gen).cuda()
+    start = torch.zeros(3, dtype=torch.int32, device="cuda")
+    args = [d[n] for n in ("q", "k", "v", "g", "beta")]
+
+    def turn(states):
+        out = kda.gdr_recurrent_step(*args, states, slots=d["slots"], start=start)
+        tokens, accepted = kda.draft_verify(p, x, u)
+        start.copy_(accepted)
+        return out, tokens
+    turn(d["states"].clone())
+    torch.cuda.synchronize()
+    states, mine = d["states"].clone(), d["states"].clone()
+    start.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = turn(states)
+    start.zero_()
+    theirs = start.clone()
+    for n in range(4):
+        p.copy_(_probs(gen, 3, 3, 500))
+        x.copy_(p[:, :2].argmax(-1))
+        u.copy_(0.3 * torch.rand(3, 3, generator=gen))
+        begin = start.clone()
+        assert torch.equal(begin, theirs)
+        graph.replay()
+        torch.cuda.synchronize()
+        after = start.clone()
+        start.copy_(begin)
+        want = turn(mine)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(states, mine) and torch.equal(after, start)
+        theirs = start.clone()
 
 
 def test_step_one_slot_for_several_tokens():
