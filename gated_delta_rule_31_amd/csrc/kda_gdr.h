@@ -259,9 +259,9 @@ __device__ __forceinline__ int64_t gdr_slice_at(int rows, int col, int V) { retu
 // read the same keys, share one XCD's L2, and a long sequence's heads spread over all of them.
 // Packed sequences (up to 64) are taken longest first, so that none is left to run alone.
 // False for a block without a pair.
-__device__ __forceinline__ bool gdr_pair(const GdrArgs &a, int VB, int &vb, int &hv, int &n) {
-    const int i = blockIdx.x / 8;
-    const int64_t pair = (int64_t)(i / VB) * 8 + blockIdx.x % 8;
+__device__ __forceinline__ bool gdr_pair(const GdrArgs &a, int block, int VB, int &vb, int &hv, int &n) {
+    const int i = block / 8;
+    const int64_t pair = (int64_t)(i / VB) * 8 + block % 8;
     vb = i % VB;
     hv = (int)(pair % a.HV);
     n = (int)(pair / a.HV);
@@ -290,7 +290,7 @@ inline int64_t gdr_pair_blocks(const GdrArgs &a, int VB) { return ((int64_t)a.N 
 
 // the products that do not depend on the state, for every (chunk slot, value head)
 hipError_t launch_gdr_prep(const GdrArgs &a, bool fp32, int K, bool bwd, hipStream_t stream);
-hipError_t launch_gdr_fwd_chain(const GdrArgs &a, bool fp32, int K, bool train, hipStream_t stream);
+hipError_t launch_gdr_fwd_chain(const GdrArgs &a, bool fp32, int K, hipStream_t stream);
 hipError_t launch_gdr_bwd(const GdrArgs &a, bool fp32, int K, hipStream_t stream);
 
 }  // namespace kda

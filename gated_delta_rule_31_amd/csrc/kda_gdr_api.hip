@@ -160,7 +160,7 @@ kda_status kda_gdr_chunk_fwd(const void *q, const void *k, const void *v, kda_dt
     a.out = out;
     a.out_bf16 = out_dtype == KDA_BF16;
     const hipError_t e = kda::launch_gdr_prep(a, in_dtype == KDA_F32, K, false, stream);
-    return done(e != hipSuccess ? e : kda::launch_gdr_fwd_chain(a, in_dtype == KDA_F32, K, false, stream));
+    return done(e != hipSuccess ? e : kda::launch_gdr_fwd_chain(a, in_dtype == KDA_F32, K, stream));
 }
 
 kda_status kda_gdr_chunk_bwd(const void *q, const void *k, const void *v, kda_dtype in_dtype, const float *g,

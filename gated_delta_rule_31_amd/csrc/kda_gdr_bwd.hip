@@ -12,12 +12,12 @@
 // holds g_t, the rows that read S through it, and those that reach S' through it.  Summed so,
 // no term is added that another one takes away.
 //
-// Four kernels: the pre-pass and the forward chain (kda_gdr_fwd.hip), which keeps every
-// chunk's start state and delta; the chain of gradients, serial backwards over the chunks;
-// and one workgroup per (chunk, key head) for the rest, which goes through the value heads of
+// Three kernels: the pre-pass (kda_gdr_fwd.hip); in one launch the forward chain
+// (kda_gdr_chain.h), which keeps every chunk's start state and delta, and the chain of
+// gradients, serial backwards over the chunks; and one workgroup per (chunk, key head) for the rest, which goes through the value heads of
 // its group, so that the shared heads' gradients are summed in a fixed order.  Computed
 // operands enter the matrix cores as three bf16 parts (24 bits).
-#include "kda_gdr.h"
+#include "kda_gdr_chain.h"
 
 namespace kda {
 namespace {
@@ -27,12 +27,11 @@ constexpr int C = GDR_C, P = 3;
 // The chain of gradients: workgroups, waves and operands in flight as in the forward chain.
 // D: the type of d_out, whose parts are exact until the read's scale meets them.
 template <typename T, typename D, int K, int NV>
-__global__ __launch_bounds__(256) void gdr_bwd_chain_kernel(const GdrArgs a) {
+__device__ __forceinline__ void gdr_bwd_chain(const GdrArgs &a, int block, __bf16 *sS, __bf16 *sX, __bf16 *sE, __bf16 *sB, __bf16 *sK, __bf16 *sQ, __bf16 *sO) {
     constexpr int PK = gdr_input_parts<T>(), PD = gdr_input_parts<D>(), KP = K < 32 ? 32 : K, KS = KP / 32, NC = (K / 16 + 3) / 4, W = 16 * NV;
     constexpr int SZ = sizeof(T), DZ = sizeof(D);
-    __shared__ __attribute__((aligned(16))) __bf16 sS[P * W * KP], sX[P * W * C], sB[P * W * C], sE[P * W * C], sK[PK * C * KP], sQ[PK * C * KP], sO[PD * C * 32];
     int vb, hv, n;
-    if (!gdr_pair(a, a.V / W, vb, hv, n)) return;
+    if (!gdr_pair(a, block, a.V / W, vb, hv, n)) return;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15, lg = lane >> 4, hk = hv / a.group;
     int64_t row, len, slot;
     gdr_sequence(a, n, row, len, slot);
@@ -197,6 +196,18 @@ __global__ __launch_bounds__(256) void gdr_bwd_chain_kernel(const GdrArgs a) {
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
                     for (int u = 0; u < NV; ++u) a.ds0[state + (int64_t)(16 * (w + 4 * i) + 4 * lg + e) * a.V + lr + 16 * u] = S[i][u][e];
+}
+
+// Both chains in one launch: neither needs the other's results, each waits most of its time, and
+// a compute unit has room for a workgroup of both.  Groups of eight blocks (one an XCD) take them
+// in turn.
+template <typename T, typename D, int K, int NV>
+__global__ __launch_bounds__(256) void gdr_chains_kernel(const GdrArgs a) {
+    constexpr int PK = gdr_input_parts<T>(), PD = gdr_input_parts<D>(), KP = K < 32 ? 32 : K, W = 16 * NV;
+    __shared__ __attribute__((aligned(16))) __bf16 sS[P * W * KP], sX[P * W * C], sE[P * W * C], sB[P * W * C], sK[PK * C * KP], sQ[PK * C * KP], sO[PD * C * 32];
+    const int block = blockIdx.x / 16 * 8 + blockIdx.x % 8;
+    if (blockIdx.x / 8 % 2 == 0) gdr_bwd_chain<T, D, K, NV>(a, block, sS, sX, sE, sB, sK, sQ, sO);
+    else gdr_chain<T, float, K, P, P, NV, true>(a, block, sS, sX, sE, nullptr, sK);
 }
 
 // Columns 4 g .. + 3 and 16 + 4 g .. + 3 of a row's 32-column slice: lanes next to each other read
@@ -540,8 +551,8 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
 template <typename T, typename D, int K>
 hipError_t launch(const GdrArgs &a, hipStream_t stream) {
     constexpr bool WIDE = sizeof(T) == 2 || K < 128;  // two tiles of float32 rows of 128 channels do not fit the LDS
-    if (WIDE && gdr_column_tiles(a) == 2) hipLaunchKernelGGL((gdr_bwd_chain_kernel<T, D, K, WIDE ? 2 : 1>), dim3((unsigned)gdr_pair_blocks(a, a.V / 32)), dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((gdr_bwd_chain_kernel<T, D, K, 1>), dim3((unsigned)gdr_pair_blocks(a, a.V / 16)), dim3(256), 0, stream, a);
+    if (WIDE && gdr_column_tiles(a) == 2) hipLaunchKernelGGL((gdr_chains_kernel<T, D, K, WIDE ? 2 : 1>), dim3((unsigned)(2 * gdr_pair_blocks(a, a.V / 32))), dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((gdr_chains_kernel<T, D, K, 1>), dim3((unsigned)(2 * gdr_pair_blocks(a, a.V / 16))), dim3(256), 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((gdr_grads_kernel<T, D, K>), dim3((unsigned)(a.slots * a.HK)), dim3(512), 0, stream, a);
@@ -562,8 +573,6 @@ hipError_t by_width(const GdrArgs &a, int K, hipStream_t stream) {
 
 hipError_t launch_gdr_bwd(const GdrArgs &a, bool fp32, int K, hipStream_t stream) {
     hipError_t e = launch_gdr_prep(a, fp32, K, true, stream);
-    if (e != hipSuccess) return e;
-    e = launch_gdr_fwd_chain(a, fp32, K, true, stream);
     if (e != hipSuccess) return e;
     if (a.dout_bf16) return fp32 ? by_width<float, __bf16>(a, K, stream) : by_width<__bf16, __bf16>(a, K, stream);
     return fp32 ? by_width<float, float>(a, K, stream) : by_width<__bf16, float>(a, K, stream);
