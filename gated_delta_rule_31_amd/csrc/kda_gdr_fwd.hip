@@ -75,14 +75,22 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
     double g = (double)a.g[at] * 1.4426950408889634;
     float beta = a.beta[at];
     Parts<PK> fk[KS], fq[KS];
-    auto rows8 = [&](const T *x, int r, int s) {
-        const bool there = r < len && 32 * s + 8 * lg < K;
-        return load8<PK>(x + ((row + (there ? r : 0)) * a.HK + hk) * K + (there ? 32 * s + 8 * lg : 0), there);
+    // rows behind the end read the last row: their beta is 0 and their d_out too, so that what their
+    // rows of A, M and P hold reaches nothing
+    const char *kbase = reinterpret_cast<const char *>(k + (row * a.HK + hk) * K), *qbase = reinterpret_cast<const char *>(q + (row * a.HK + hk) * K);
+    const unsigned kstep = (unsigned)a.HK * K * sizeof(T);
+    auto rows8 = [&](const char *base, int r, int s) {
+        const unsigned at = (unsigned)(r < len ? r : len - 1) * kstep + (K < 32 ? lg % 2 * 8 : 8 * lg) * (unsigned)sizeof(T);
+        Parts<PK> y = load8<PK>(reinterpret_cast<const T *>(base + at + 32 * s * sizeof(T)), true);
+        if (K < 32)
+#pragma unroll
+            for (int p = 0; p < PK; ++p) y.v[p] = lg < 2 ? y.v[p] : bf16x8{};
+        return y;
     };
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-        fk[s] = rows8(k, 16 * w + lr, s);
-        fq[s] = rows8(q, 16 * w + lr, s);
+        fk[s] = rows8(kbase, 16 * w + lr, s);
+        fq[s] = rows8(qbase, 16 * w + lr, s);
     }
     if (lane >= len) g = 0.0, beta = 0.f;
     g = g < -1000.0 ? -1000.0 : g;
@@ -95,8 +103,8 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
     if (w == 0) {
         const double last = __shfl(g, 63);
         float *dec = a.dec + unit * 4 * C;
-        dec[lane] = exp2f((float)g);
-        dec[C + lane] = exp2f((float)(last - g));
+        dec[lane] = __builtin_amdgcn_exp2f((float)g);
+        dec[C + lane] = __builtin_amdgcn_exp2f((float)(last - g));
         dec[2 * C + lane] = beta;
         if (BWD) a.G[unit * C + lane] = g;
     }
@@ -112,7 +120,7 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
             f4 kk = {}, qk = {};
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                const Parts<PK> f = c == w ? fk[s] : rows8(k, 16 * c + lr, s);
+                const Parts<PK> f = c == w ? fk[s] : rows8(kbase, 16 * c + lr, s);
                 mma(kk, fk[s], f);
                 mma(qk, fq[s], f);
             }
