@@ -46,7 +46,7 @@ __device__ __forceinline__ void gdr_bwd_chain(const GdrArgs &a, int block, __bf1
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             S[i][u] = f4{};
-            if (w + 4 * i < K / 16) {
+            if (K % 64 == 0 || w + 4 * i < K / 16) {
                 const int ch = 16 * (w + 4 * i) + 4 * lg;
                 if (a.d_sf)
 #pragma unroll
@@ -67,6 +67,7 @@ __device__ __forceinline__ void gdr_bwd_chain(const GdrArgs &a, int block, __bf1
     Parts<PK> k[KS], q[KS];
     Parts<P> m[2], p[2];
     Parts<PD> o;
+    m[0] = p[0] = Parts<P>{};  // rows 32..63 have nothing in the first 32 columns of M^T and P^T
     f4 b, end, beta;
     float last;
     // rows behind the sequence's end read its last row: P^T and M^T are 0 there, and so is beta
@@ -85,7 +86,7 @@ __device__ __forceinline__ void gdr_bwd_chain(const GdrArgs &a, int block, __bf1
         const __bf16 *from = base + ((slot + c) * a.HV + hv) * (P * C * C);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (s >= w / 2) f[s] = load_frag<P>(from, w, s, lane);
+            if (s == 1 || w < 2) f[s] = load_frag<P>(from, w, s, lane);
     };
     auto load_dec = [&](int c) {
         const float *dec = a.dec + ((slot + c) * a.HV + hv) * (4 * C);
@@ -106,7 +107,7 @@ __device__ __forceinline__ void gdr_bwd_chain(const GdrArgs &a, int block, __bf1
         float *dh = a.dh + at * ((int64_t)K * a.V) + gdr_slice_at(K, W * vb, a.V);
 #pragma unroll
         for (int i = 0; i < NC; ++i)
-            if (w + 4 * i < K / 16)
+            if (K % 64 == 0 || w + 4 * i < K / 16)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -133,9 +134,8 @@ __device__ __forceinline__ void gdr_bwd_chain(const GdrArgs &a, int block, __bf1
             for (int u = 0; u < NV; ++u) mma(x[u], k[s], lds_frag<P, W, KP>(sS, 16 * u + lr, 32 * s + 8 * lg));
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (s >= w / 2)
 #pragma unroll
-                for (int u = 0; u < NV; ++u) mma(y[u], p[s], lds_frag_turned<PD, C, 32>(sO, 32 * s + 8 * lg, 16 * u, lane));
+            for (int u = 0; u < NV; ++u) mma(y[u], p[s], lds_frag_turned<PD, C, 32>(sO, 32 * s + 8 * lg, 16 * u, lane));
         load_kqo(next);
         load_frags(a.P, p, next);
 #pragma unroll
@@ -147,9 +147,8 @@ __device__ __forceinline__ void gdr_bwd_chain(const GdrArgs &a, int block, __bf1
         gdr_lds_barrier();
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (s >= w / 2)
 #pragma unroll
-                for (int u = 0; u < NV; ++u) mma(x[u], m[s], lds_frag<P, W, C>(sX, 16 * u + lr, 32 * s + 8 * lg));
+            for (int u = 0; u < NV; ++u) mma(x[u], m[s], lds_frag<P, W, C>(sX, 16 * u + lr, 32 * s + 8 * lg));
         load_frags(a.Mt, m, next);
         f4 E[NV];
 #pragma unroll
@@ -165,7 +164,7 @@ __device__ __forceinline__ void gdr_bwd_chain(const GdrArgs &a, int block, __bf1
         gdr_lds_barrier();
 #pragma unroll
         for (int i = 0; i < NC; ++i)
-            if (w + 4 * i < K / 16) {
+            if (K % 64 == 0 || w + 4 * i < K / 16) {
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     const Parts<PK> qt = lds_frag_turned<PK, C, KP>(sQ, 32 * s + 8 * lg, 16 * (w + 4 * i), lane);
@@ -191,7 +190,7 @@ __device__ __forceinline__ void gdr_bwd_chain(const GdrArgs &a, int block, __bf1
     if (a.ds0)
 #pragma unroll
         for (int i = 0; i < NC; ++i)
-            if (w + 4 * i < K / 16)
+            if (K % 64 == 0 || w + 4 * i < K / 16)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -200,9 +199,10 @@ __device__ __forceinline__ void gdr_bwd_chain(const GdrArgs &a, int block, __bf1
 
 // Both chains in one launch: neither needs the other's results, each waits most of its time, and
 // a compute unit has room for a workgroup of both.  Groups of eight blocks (one an XCD) take them
-// in turn.
+// in turn.  Two workgroups a compute unit where the LDS allows it: without that bound the compiler
+// takes 264 registers instead of 256 and one fits (1360 against 1262 us for the layer's call).
 template <typename T, typename D, int K, int NV>
-__global__ __launch_bounds__(256) void gdr_chains_kernel(const GdrArgs a) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 && NV == 1 ? 2 : 1) void gdr_chains_kernel(const GdrArgs a) {
     constexpr int PK = gdr_input_parts<T>(), PD = gdr_input_parts<D>(), KP = K < 32 ? 32 : K, W = 16 * NV;
     __shared__ __attribute__((aligned(16))) __bf16 sS[P * W * KP], sX[P * W * C], sE[P * W * C], sB[P * W * C], sK[PK * C * KP], sQ[PK * C * KP], sO[PD * C * 32];
     const int block = blockIdx.x / 16 * 8 + blockIdx.x % 8;

@@ -41,7 +41,7 @@ __device__ __forceinline__ void gdr_chain(const GdrArgs &a, int block, __bf16 *s
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             S[c][u] = f4{};
-            if (w + 4 * c < K / 16) {
+            if (K % 64 == 0 || w + 4 * c < K / 16) {
                 const int ch = 16 * (w + 4 * c) + 4 * lg;
                 if (a.s0)
 #pragma unroll
@@ -61,6 +61,10 @@ __device__ __forceinline__ void gdr_chain(const GdrArgs &a, int block, __bf16 *s
     Parts<PK> k[KS], q[KS];
     Parts<P> m[2];
     Parts<PO> p[2];
+    // rows 0..31 have nothing in M's and P's second 32 columns: waves 0 and 1 multiply zeros that they
+    // hold, while the others work, so that a phase has no branches and its parts are interleaved
+    m[1] = Parts<P>{};
+    p[1] = Parts<PO>{};
     f4 b, end, beta, nb, nend, nbeta;
     Parts<PK> v, nv;
     bf16x8 one[NV];
@@ -84,13 +88,13 @@ __device__ __forceinline__ void gdr_chain(const GdrArgs &a, int block, __bf16 *s
         const __bf16 *from = a.M + ((slot + c) * a.HV + hv) * (P * C * C);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (s <= w / 2) m[s] = load_frag<P>(from, w, s, lane);
+            if (s == 0 || w >= 2) m[s] = load_frag<P>(from, w, s, lane);
     };
     auto load_p = [&](int c) {
         const __bf16 *from = a.P + ((slot + c) * a.HV + hv) * (PO * C * C);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (!TRAIN && s <= w / 2) p[s] = load_frag<PO>(from, w, s, lane);
+            if (!TRAIN && (s == 0 || w >= 2)) p[s] = load_frag<PO>(from, w, s, lane);
     };
     auto load_rows = [&](int c) {  // into the second set
         const float *dec = a.dec + ((slot + c) * a.HV + hv) * (4 * C);
@@ -118,7 +122,7 @@ __device__ __forceinline__ void gdr_chain(const GdrArgs &a, int block, __bf16 *s
             float *h = a.h + ((slot + c) * a.HV + hv) * ((int64_t)K * a.V) + gdr_slice_at(K, W * vb, a.V);
 #pragma unroll
             for (int i = 0; i < NC; ++i)
-                if (w + 4 * i < K / 16)
+                if (K % 64 == 0 || w + 4 * i < K / 16)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -151,9 +155,8 @@ __device__ __forceinline__ void gdr_chain(const GdrArgs &a, int block, __bf16 *s
         gdr_lds_barrier();
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (s <= w / 2)
 #pragma unroll
-                for (int u = 0; u < NV; ++u) mma(x[u], m[s], lds_frag<P, W, C>(sX, 16 * u + lr, 32 * s + 8 * lg));
+            for (int u = 0; u < NV; ++u) mma(x[u], m[s], lds_frag<P, W, C>(sX, 16 * u + lr, 32 * s + 8 * lg));
         load_m(next);
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
@@ -164,7 +167,7 @@ __device__ __forceinline__ void gdr_chain(const GdrArgs &a, int block, __bf16 *s
         gdr_lds_barrier();
 #pragma unroll
         for (int i = 0; i < NC; ++i)
-            if (w + 4 * i < K / 16) {
+            if (K % 64 == 0 || w + 4 * i < K / 16) {
                 Parts<PK> kt[2];
 #pragma unroll
                 for (int s = 0; s < 2; ++s) kt[s] = lds_frag_turned<PK, C, KP>(sK, 32 * s + 8 * lg, 16 * (w + 4 * i), lane);
@@ -189,7 +192,7 @@ __device__ __forceinline__ void gdr_chain(const GdrArgs &a, int block, __bf16 *s
                 y[u] *= blr;
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
-                    if (s <= w / 2) mma_to<PO>(y[u], lds_frag<PO, W, C>(sV, 16 * u + lr, 32 * s + 8 * lg), p[s]);
+                    mma_to<PO>(y[u], lds_frag<PO, W, C>(sV, 16 * u + lr, 32 * s + 8 * lg), p[s]);
                 y[u] *= a.scale;
             }
             load_p(next);
@@ -204,7 +207,7 @@ __device__ __forceinline__ void gdr_chain(const GdrArgs &a, int block, __bf16 *s
     if (!TRAIN && a.sf)
 #pragma unroll
         for (int i = 0; i < NC; ++i)
-            if (w + 4 * i < K / 16)
+            if (K % 64 == 0 || w + 4 * i < K / 16)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
