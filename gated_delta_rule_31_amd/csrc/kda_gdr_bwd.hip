@@ -337,6 +337,10 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
             }
             const Parts<P> fv = cut8<P>(xv), fe = cut8<P>(xe);
             const Parts<PD> fd = cut8<PD>(xo);
+            Parts<P> fpair = fe;  // the whole square of pairs, with no branch: what is above the diagonal is dropped
+            if (half == 0)
+#pragma unroll
+                for (int p = 0; p < P; ++p) fpair.v[p] = p < PD ? fd.v[p < PD ? p : 0] : bf16x8{};
             unsigned cx[QUADS][2][P], cy[QUADS][2][P];
 #pragma unroll
             for (int j = 0; j < QUADS; ++j) {
@@ -370,21 +374,15 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
             gdr_lds_barrier();
 #pragma unroll
             for (int c = 0; c < CT; ++c)
-                if (half * CT + c < K / 16) {
+                if (K % 32 == 0 || half * CT + c < K / 16) {
                     const int ch = 16 * (half * CT + c) + lr;
                     const Parts<P> s = lds_frag<P, K, 32>(sS, ch, 8 * lg), d = lds_frag<P, K, 32>(sH, ch, 8 * lg);
                     mma(r1[c], fd, s);
                     mma(r2[c], fe, s);
                     mma(r3[c], fv, d);
-                    __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (c <= w) {
-                    const Parts<P> f = lds_frag<P, C, 32>(sV, 16 * c + lr, 8 * lg);
-                    if (half == 0) mma(pair[c], fd, f);
-                    else mma(pair[c], fe, f);
-                }
+            for (int c = 0; c < 4; ++c) mma(pair[c], fpair, lds_frag<P, C, 32>(sV, 16 * c + lr, 8 * lg));
         }
         // dbeta: a row's eight-column pieces lie in lanes 16 apart
         db += __shfl_xor(db, 16);
@@ -429,7 +427,7 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
         f4 reads = {}, ends = {};
 #pragma unroll
         for (int c = 0; c < CT; ++c)
-            if (half * CT + c < K / 16) {
+            if (K % 32 == 0 || half * CT + c < K / 16) {
                 f4 qc, kc;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -478,7 +476,7 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
             const Parts<P> fpr = cut8<P>(pr), fpc = cut8<P>(pc), fac = cut8<P>(ac);
 #pragma unroll
             for (int c = 0; c < CT; ++c)
-                if (half * CT + c < K / 16) {
+                if (K % 32 == 0 || half * CT + c < K / 16) {
                     Parts<PK> kt, qt;
                     if constexpr (KQ) {
                         kt = lds_frag_turned<PK, C, KP>(sK, 32 * s + 8 * lg, 16 * (half * CT + c), lane);
@@ -536,7 +534,7 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
     const int lr = threadIdx.x & 15, lg = threadIdx.x >> 4 & 3;
 #pragma unroll
     for (int c = 0; c < CT; ++c)
-        if (half * CT + c < K / 16)
+        if (K % 32 == 0 || half * CT + c < K / 16)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = 16 * w + 4 * lg + e;
