@@ -230,6 +230,19 @@ struct Slice8 {
             y[4 + i] = columns > 16 ? (float)x[1][i] : 0.f;
         }
     }
+    // as operand parts, zeros where !there
+    __device__ __forceinline__ Parts<gdr_input_parts<D>()> parts(int columns, bool there) const {
+        if constexpr (sizeof(D) == 2) {
+            const u32x2 u = there ? __builtin_bit_cast(u32x2, x[0]) : u32x2{}, v = there && columns > 16 ? __builtin_bit_cast(u32x2, x[1]) : u32x2{};
+            return {{__builtin_bit_cast(bf16x8, u32x4{u[0], u[1], v[0], v[1]})}};
+        } else {
+            float y[8];
+            get(y, columns);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = there ? y[i] : 0.f;
+            return cut8<gdr_input_parts<D>()>(y);
+        }
+    }
 };
 __device__ __forceinline__ int staged_at(int row, int quad) { return lds_at<32>(row, quad % 4 * 8 + quad / 4 * 4); }
 
@@ -241,8 +254,8 @@ template <typename T, typename D, int K>
 __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
     constexpr int PK = gdr_input_parts<T>(), PD = gdr_input_parts<D>(), KS = K < 32 ? 1 : K / 32, CT = (K / 16 + 1) / 2, LA = C + 4, KP = K < 32 ? 32 : K, QUADS = K * 8 / 512 ? K * 8 / 512 : 1;
     constexpr bool KQ = PK == 1;  // k and q rows stay in LDS over the heads of a group where they fit
-    __shared__ __attribute__((aligned(16))) __bf16 sS[P * K * 32], sH[P * K * 32], sV[P * C * 32];
-    __shared__ __attribute__((aligned(16))) float sP[C * LA], sA[C * LA], sT[C * LA], sSum[4][C], sReads[2][C], sEnds[2][C], sKeep[8];
+    __shared__ __attribute__((aligned(16))) __bf16 sS[P * K * 32], sH[P * K * 32], sV[P * C * 32], sE[P * C * 32];
+    __shared__ __attribute__((aligned(16))) float sP[C * LA], sA[C * LA], sT[C * LA], sSum[2][4][C], sReads[2][2][C], sEnds[2][2][C], sKeep[2][8];
     __shared__ __attribute__((aligned(16))) __bf16 sK[KQ ? C * KP : 8], sQ[KQ ? C * KP : 8];
     __shared__ double sG[C];
     const int unit = blockIdx.x, hk = unit % a.HK;
@@ -315,6 +328,7 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
         const int64_t at = slot * a.HV + hv;
         const float *dec = a.dec + at * 4 * C;
         const double g = a.G[at * C + lane];
+        const int turn = hv & 1;  // sums of one head are read while the next is on its way
         f4 r1[CT], r2[CT], r3[CT], pair[4];
 #pragma unroll
         for (int c = 0; c < CT; ++c) r1[c] = r2[c] = r3[c] = f4{};
@@ -324,23 +338,21 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
         for (int sl = 0; sl < slices; ++sl) {
             const int left = V - 32 * sl;
             const float beta_r = raw_beta;
-            float xv[8], xe[8], xo[8];
-            raw_v.get(xv, left);
+            // half 0 cuts the corrections and half 1 the rows of E; both take both from LDS
+            float xe[8], x[8];
             raw_e.get(xe, left);
-            raw_o.get(xo, left);
+            if (half == 0) {
+                raw_v.get(x, left);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                db += xe[i] * xv[i];
-                xo[i] = r < len ? xo[i] : 0.f;
-                xv[i] *= beta_r;
-                xe[i] *= beta_r;
+                for (int i = 0; i < 8; ++i) db += xe[i] * x[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = xe[i];
             }
-            const Parts<P> fv = cut8<P>(xv), fe = cut8<P>(xe);
-            const Parts<PD> fd = cut8<PD>(xo);
-            Parts<P> fpair = fe;  // the whole square of pairs, with no branch: what is above the diagonal is dropped
-            if (half == 0)
 #pragma unroll
-                for (int p = 0; p < P; ++p) fpair.v[p] = p < PD ? fd.v[p < PD ? p : 0] : bf16x8{};
+            for (int i = 0; i < 8; ++i) x[i] *= beta_r;
+            const Parts<P> mine = cut8<P>(x);
+            const Parts<PD> fd = raw_o.parts(left, r < len);
             unsigned cx[QUADS][2][P], cy[QUADS][2][P];
 #pragma unroll
             for (int j = 0; j < QUADS; ++j) {
@@ -358,9 +370,8 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
             load(sl + 1 < slices || hv + 1 == (hk + 1) * a.group ? hv : hv + 1, sl + 1 < slices ? sl + 1 : 0, tid);
             gdr_lds_barrier();  // the last slice has been read
             if (sl == 0 && w8 == 0) sG[lane] = g;
-            if (half == 0)
 #pragma unroll
-                for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x8 *>(sV + p * C * 32 + lds_at<32>(r, 8 * lg)) = fv.v[p];
+            for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x8 *>((half == 0 ? sV : sE) + p * C * 32 + lds_at<32>(r, 8 * lg)) = mine.v[p];
 #pragma unroll
             for (int j = 0; j < QUADS; ++j) {
                 const int i = tid + 512 * j;
@@ -372,6 +383,11 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
                     }
             }
             gdr_lds_barrier();
+            const Parts<P> fv = lds_frag<P, C, 32>(sV, r, 8 * lg), fe = lds_frag<P, C, 32>(sE, r, 8 * lg);
+            Parts<P> fpair = fe;  // the whole square of pairs, with no branch: what is above the diagonal is dropped
+            if (half == 0)
+#pragma unroll
+                for (int p = 0; p < P; ++p) fpair.v[p] = p < PD ? fd.v[p < PD ? p : 0] : bf16x8{};
 #pragma unroll
             for (int c = 0; c < CT; ++c)
                 if (K % 32 == 0 || half * CT + c < K / 16) {
@@ -390,7 +406,7 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
         if (half == 0 && lg == 0 && r < len) a.dbeta[(row + r) * a.HV + hv] = db;
 #pragma unroll
         for (int d = 32; d; d /= 2) keep += __shfl_xor(keep, d);
-        if (lane == 0) sKeep[w8] = keep;
+        if (lane == 0) sKeep[turn][w8] = keep;
 
         // the pairs inside the chunk: dP and its share of H, then dA and its
         f4 share[4];
@@ -411,7 +427,7 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
 #pragma unroll
                 for (int s = 0; s < KS; ++s) mma(dot, f[s], rows(k, sK, 16 * c + lr, s));
             }
-            __builtin_amdgcn_sched_barrier(0);  // else the loads of all tiles are in registers at once
+            if (!KQ) __builtin_amdgcn_sched_barrier(0);  // else the loads of all tiles are in registers at once
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = 16 * w + 4 * lg + e, j = 16 * c + lr;
@@ -447,14 +463,13 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
                 ends += kc * r3[c];
                 dq[c] += r1[c];
                 dk[c] += r2[c] + r3[c];
-                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float x = row16_sum(reads[e]), y = row16_sum(ends[e]);
             if (lr == 0) {
-                sReads[half][16 * w + 4 * lg + e] = x;
-                sEnds[half][16 * w + 4 * lg + e] = y;
+                sReads[turn][half][16 * w + 4 * lg + e] = x;
+                sEnds[turn][half][16 * w + 4 * lg + e] = y;
             }
         }
         __syncthreads();
@@ -510,12 +525,12 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
             for (int e = 0; e < 4; ++e) sum += 16 * w + 4 * lg + e >= t ? R[e] : 0.f;
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
-            if (lg == 0) sSum[w][t] = sum;
+            if (lg == 0) sSum[turn][w][t] = sum;
             __builtin_amdgcn_sched_barrier(0);
         }
         __syncthreads();
         if (tid < C) {
-            float from = sReads[0][tid] + sReads[1][tid], upto = sEnds[0][tid] + sEnds[1][tid];
+            float from = sReads[turn][0][tid] + sReads[turn][1][tid], upto = sEnds[turn][0][tid] + sEnds[turn][1][tid];
             const float own = upto;
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) {
@@ -525,11 +540,10 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
             }
             float kept = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) kept += sKeep[i];
-            const float sum = (sSum[0][tid] + sSum[1][tid]) + (sSum[2][tid] + sSum[3][tid]);
+            for (int i = 0; i < 8; ++i) kept += sKeep[turn][i];
+            const float sum = (sSum[turn][0][tid] + sSum[turn][1][tid]) + (sSum[turn][2][tid] + sSum[turn][3][tid]);
             if (tid < len) a.dg[(row + tid) * a.HV + hv] = sum + from + (upto - own) + dec[C - 1] * kept;
         }
-        __syncthreads();
     }
     const int lr = threadIdx.x & 15, lg = threadIdx.x >> 4 & 3;
 #pragma unroll
