@@ -282,7 +282,8 @@ __device__ __forceinline__ bool gdr_pair(const GdrArgs &a, int block, int VB, in
 // Tiles of 16 value columns that one workgroup of a chain takes: one while that gives a compute
 // unit no more than one workgroup (8192 tokens x 32 heads of 128 columns: 291 us, two tiles 361),
 // two from two workgroups a unit on, as a chunk's operands are then loaded half as often (64
-// heads: 412 us, one tile 498; 96 heads 634, 767).
+// heads: 412 us, one tile 498; 96 heads 634, 767; both without branches since: 256 us for 32
+// heads, 360 for 64 and 617 for 96).
 inline int gdr_column_tiles(const GdrArgs &a) {
     return a.V >= 32 && (int64_t)a.N * a.HV * (a.V / 16) >= 2 * device_cu_count() ? 2 : 1;
 }
