@@ -114,6 +114,9 @@ __device__ __forceinline__ void gdr_bwd_chain(const GdrArgs &a, int block, __bf1
                     for (int u = 0; u < NV; ++u) dh[(16 * (w + 4 * i) + 4 * lg + e) * gdr_slice_columns(a.V) + lr + 16 * u] = S[i][u][e];
 #pragma unroll
         for (int i = 0; i < PD; ++i) *reinterpret_cast<bf16x8 *>(sO + i * C * 32 + lds_at<32>(16 * w + lr, 8 * lg)) = o.v[i];
+        gdr_lds_barrier();
+        // behind the barrier: until then other waves may still read the rows of the chunk before (the
+        // rows of d_out are read by none of them behind that chunk's second barrier)
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -121,7 +124,6 @@ __device__ __forceinline__ void gdr_bwd_chain(const GdrArgs &a, int block, __bf1
                 *reinterpret_cast<bf16x8 *>(sK + i * C * KP + lds_at<KP>(16 * w + lr, 32 * s + 8 * lg)) = k[s].v[i];
                 *reinterpret_cast<bf16x8 *>(sQ + i * C * KP + lds_at<KP>(16 * w + lr, 32 * s + 8 * lg)) = q[s].v[i];
             }
-        gdr_lds_barrier();
         f4 x[NV], y[NV], d[NV];
 #pragma unroll
         for (int u = 0; u < NV; ++u) {

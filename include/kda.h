@@ -361,10 +361,11 @@ size_t kda_noalloc_scratch_bytes(void);
  * outside [0, T] or out of order are brought into range on the device (no access outside the
  * tensors; the results are then unspecified).  The workspace is scratch as in kda_chunk_fwd
  * (required; at least kda_gdr_chunk_fwd_workspace_size bytes, which is 0 for a shape that is
- * not supported).  bf16 inputs are exact on the matrix cores; states and corrected values
- * enter them with 16 mantissa bits (24 with float32 inputs) and float32 sums, so the
- * relative error of out and of final_state is about 1e-5 at most, before `out` is rounded to
- * its type.
+ * not supported).  bf16 inputs are exact on the matrix cores; what is computed from them enters
+ * the products with 24 mantissa bits on its way to the state and, with bf16 inputs, with 16 on
+ * its way to `out` alone, and is summed in float32: final_state is off by about 1e-6 of its norm
+ * at most, out by about 1e-5 before it is rounded to its type.  Values that are not finite may
+ * reach other tokens of their chunk and other columns of their head.
  */
 size_t kda_gdr_chunk_fwd_workspace_size(kda_dtype in_dtype, int B, int64_t T, int num_seqs, int varlen, int HK,
                                         int HV, int K, int V);

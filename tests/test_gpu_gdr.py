@@ -6,10 +6,10 @@ Tolerances, set from the roundings that the kernels make:
 * float32 inputs: operands are sums of three bf16 parts, off by at most 2^-24 of the value,
   and float32 sums of at most 128 + 64 terms: sqrt(192) 2^-24 is 8e-7 of a sum's terms; a
   dozen such sums follow one another in a chunk: 1e-5.
-* bfloat16 inputs: state, M, beta X, Vn enter as two parts, each off by at most 2^-16 of the
-  value; five such roundings in a chunk, which fade or are corrected like the state itself,
-  give at most 5 2^-16 = 7.6e-5 of the terms, and terms reach about 6 times the rms: 5e-4 of
-  the rms for the largest element, and (as they are independent, with an rms of 2^-18 each)
+* bfloat16 inputs: the state's path as with float32 inputs; state, P and Vn enter the output as
+  two parts, each off by at most 2^-16 of the value.  The bounds were set for five such roundings
+  in a chunk: at most 5 2^-16 = 7.6e-5 of the terms, and terms reach about 6 times the rms: 5e-4
+  of the rms for the largest element, and (as they are independent, with an rms of 2^-18 each)
   2^-16 in the 2-norm.
 * an output in bfloat16 is rounded once more, by at most half a step, 2^-8 of the value.
 * the decode step is float32 throughout, sums of at most 128 terms: 128 2^-24 = 8e-6 of them.
