@@ -136,7 +136,7 @@ def gdr_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
         final_state = _output(final_state, "final_state", (N, HV, K, V), torch.float32, dev)
     workspace = _workspace(workspace, gdr_chunk_fwd_workspace_size(q.dtype, B, T, HK, HV, K, V, N, cu_seqlens is not None), dev)
     _call(_load().kda_gdr_chunk_fwd, dev, _p(q), _p(k), _p(v), _dtype_code(q.dtype), _p(g), _p(beta), _p(initial_state), _p(final_state),
-          _p(cu_seqlens), N, B, T, HK, HV, K, V, scale, _p(out), _dtype_code(od), _p(workspace), workspace.numel())
+          _p(cu_seqlens), N, B, T, HK, HV, K, V, float(scale), _p(out), _dtype_code(od), _p(workspace), workspace.numel())
     return out, final_state
 
 
@@ -169,7 +169,7 @@ def gdr_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     ds0 = torch.empty((N, HV, K, V), dtype=torch.float32, device=dev) if want_d_initial_state else None
     workspace = _workspace(workspace, gdr_chunk_bwd_workspace_size(q.dtype, B, T, HK, HV, K, V, N, cu_seqlens is not None), dev)
     _call(_load().kda_gdr_chunk_bwd, dev, _p(q), _p(k), _p(v), _dtype_code(q.dtype), _p(g), _p(beta), _p(initial_state), _p(cu_seqlens), N, B,
-          T, HK, HV, K, V, scale, _p(d_out), _dtype_code(d_out.dtype), _p(d_final_state), _p(dq), _p(dk), _p(dv), _dtype_code(gd), _p(dg),
+          T, HK, HV, K, V, float(scale), _p(d_out), _dtype_code(d_out.dtype), _p(d_final_state), _p(dq), _p(dk), _p(dv), _dtype_code(gd), _p(dg),
           _p(dbeta), _p(ds0), _p(workspace), workspace.numel())
     return dq, dk, dv, dg, dbeta, ds0
 
@@ -259,7 +259,7 @@ def gdr_recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: tor
     else:
         out = _output(out, "out", (B, S, HV, V), od, dev)
     _call(_load().kda_gdr_recurrent_step, dev, _p(q), _p(k), _p(v), _dtype_code(q.dtype), _p(g), 1 if g.dim() == 4 else 0, _p(beta), _p(states),
-          pool, _p(slots), cols, _p(start), _p(lengths), B, S, HK, HV, K, V, scale, _p(out), _dtype_code(od))
+          pool, _p(slots), cols, _p(start), _p(lengths), B, S, HK, HV, K, V, float(scale), _p(out), _dtype_code(od))
     return out
 
 

@@ -321,6 +321,23 @@ def test_bwd_deterministic_and_workspace_contents_do_not_matter():
     assert all(torch.equal(x, y) for x, y in zip(*fw))
 
 
+@pytest.mark.parametrize("dtype,HK,HV", [(torch.bfloat16, 16, 32), (torch.bfloat16, 24, 72), (torch.float32, 8, 16)])
+def test_long_calls_repeat_bit_for_bit(dtype, HK, HV):
+    """Many chunks and enough workgroups to fill the GPU: forward and gradients, three times each."""
+    gen = torch.Generator(device="cuda").manual_seed(HV)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    unit = lambda x: (x / x.norm(dim=-1, keepdim=True)).to(dtype)  # noqa: E731
+    T = 1500
+    args = [unit(rand(1, T, HK, 128)), unit(rand(1, T, HK, 128)), rand(1, T, HV, 128).to(dtype), -torch.nn.functional.softplus(rand(1, T, HV)),
+            torch.sigmoid(rand(1, T, HV))]
+    d_out, d_fin = rand(1, T, HV, 128).to(dtype), rand(1, HV, 128, 128)
+    first = None
+    for _ in range(3):
+        now = kda.gdr_chunk_fwd(*args) + kda.gdr_chunk_bwd(*args, d_out, d_final_state=d_fin)
+        first = first or now
+        assert all(bool(torch.isfinite(x).all()) and torch.equal(x, y) for x, y in zip(now, first))
+
+
 def test_autograd_matches_bwd():
     i = ref.make(2, 100, 2, 4, 32, 32, torch.bfloat16, seed=25)
     d = _gpu(i)
