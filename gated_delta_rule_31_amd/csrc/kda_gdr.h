@@ -46,7 +46,7 @@ struct GdrArgs {
     int64_t slots;               // chunk slots
     int chunks;                  // chunk slots of a batch row (no cu)
     __bf16 *M, *P;               // [slots * HV][parts * 4096]
-    __bf16 *Kt;                  // [slots * HK][parts of k * K * 64]
+    __bf16 *Kt;                  // [slots * HK][parts of k * K * 64], float32 gradients only
     float *dec;                  // [slots * HV][4 * 64]: e^G, e^{G_C - G}, beta, unused
     // backward
     __bf16 *Mt, *Qt;             // M^T (P holds P^T), Q^T

@@ -25,8 +25,8 @@ namespace {
 constexpr int C = GDR_C, P = 3;
 
 // The chain of gradients: workgroups, waves and operands in flight as in the forward chain, and
-// bound alike.  Both chains together, 8192 tokens x 32 heads, K = V = 128, bf16: 763 us (one after
-// the other 851), 0.9 GB read and 0.9 GB written.
+// bound alike.  Both chains together, 8192 tokens x 32 heads, K = V = 128, bf16: 751 us, 0.6 GB
+// read and 0.9 GB written.
 // D: the type of d_out, whose parts are exact until the read's scale meets them.
 template <typename T, typename D, int K, int NV>
 __device__ __forceinline__ void gdr_bwd_chain(const GdrArgs &a, int block, __bf16 *sS, __bf16 *sX, __bf16 *sE, __bf16 *sB, __bf16 *sK, __bf16 *sQ, __bf16 *sO) {
@@ -254,8 +254,8 @@ __device__ __forceinline__ int staged_at(int row, int quad) { return lds_at<32>(
 // 16w..16w+15 and the h-th half of the channels; of the C x C products, h = 0 has dP and h = 1
 // dA.  The products over V go through LDS in slices of 32 columns, the next slice's rows on
 // their way meanwhile.  Bound by issue: cutting float32 states and rows into parts takes the vector
-// units about 40% of the time, the products the matrix cores 20% (8192 tokens x 32 heads, K = V =
-// 128, bf16: 461 us, 1.1 GB read; four waves, each with all channels, spilled and took 843 us).
+// units about 40% of the time, the products the matrix cores 23% (8192 tokens x 32 heads, K = V =
+// 128, bf16: 471 us, 1.05 GB read; its first form, four waves that spilled, took 843 us).
 template <typename T, typename D, int K>
 __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
     constexpr int PK = gdr_input_parts<T>(), PD = gdr_input_parts<D>(), KS = K < 32 ? 1 : K / 32, CT = (K / 16 + 1) / 2, LA = C + 4, KP = K < 32 ? 32 : K, QUADS = K * 8 / 512 ? K * 8 / 512 : 1;
