@@ -7,8 +7,9 @@
 //
 // Bound by reading two rows of probabilities for a request.  Two kernels: one wave for every
 // 1024 tokens of the row that is drawn from writes the sums of its weights, then one
-// workgroup a request walks the sums and looks inside one tile.  192 requests over 131,072 tokens:
-// 40 us and 6 us for 0.2 GB; one request over 32,768 tokens: 16 us, the host's time for two launches.
+// workgroup a request walks the sums and looks inside one tile.  192 requests over
+// 131,072 tokens: 40 us and 6 us for 0.2 GB; one request over 32,768 tokens: 16 to 20 us a call,
+// the host's time for two launches.
 #include "kda_gdr_step.h"
 
 namespace kda {

@@ -1,6 +1,6 @@
 // kda_gdr_fwd.hip -- chunkwise prefill of the gated delta rule with one decay per value head
 // (formulas and precision: kda_gdr.h).  Two kernels: a pre-pass over all (chunk, value head)
-// pairs at once, which forms what does not depend on the state (M, P, the decays, K^T), and
+// pairs at once, which forms what does not depend on the state (M, P, the decays), and
 // the chain, serial over a sequence's chunks and parallel over sequences, value heads and
 // blocks of 16 value columns.
 #include "kda_gdr_chain.h"
@@ -27,8 +27,8 @@ __device__ __forceinline__ int block_at(int p, int r) { return (p * (p + 1) / 2 
 // (chunk slot, key head) that writes K^T and Q^T.  Wave w owns token rows 16w..16w+15 until A
 // is there, then the column blocks w of M.  33 KB of LDS, so that four workgroups share a
 // compute unit: a workgroup mostly waits (for its rows, for substitution and products that
-// follow one another), and what it writes, 30 KB, is more than it reads.  8192 tokens x 96 heads, K
-// = 128, bf16: 190 to 204 us, 0.19 GB read and 0.39 GB written.
+// follow one another), and what it writes, 30 KB, is more than it reads.  8192 tokens x 96
+// heads, K = 128, bf16: 190 to 204 us, 0.19 GB read and 0.39 GB written.
 template <typename T, int K, int P, int PO, bool BWD>
 __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
     constexpr int PK = gdr_input_parts<T>(), KP = K < 32 ? 32 : K, LK = KP + 8, KS = KP / 32, VEC = 16 / sizeof(T);

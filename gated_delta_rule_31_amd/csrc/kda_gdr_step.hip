@@ -6,9 +6,10 @@
 // Bound by the state's bytes: one read for each request and head, one write for each kept
 // token.  A wave owns CW = 32 value columns of one (request, head): lane (r, c) holds K / RG
 // key rows of four columns in registers, so a row's piece is one whole cache line, the sums
-// over key rows stay inside the wave, and no wave waits for another.  64 requests x 96 heads, K = V
-// = 128, bf16, one token: 146 to 156 us for 0.81 GB over states that do not fit the last-level cache (5.3
-// TB/s; a large device copy reaches 5.0); 24 requests of 1 to 5 tokens x 32 heads: 37 us for 0.2 GB.
+// over key rows stay inside the wave, and no wave waits for another.  64 requests x 96 heads, K =
+// V = 128, bf16, one token: 146 to 156 us for 0.81 GB over states that do not fit the last-level
+// cache (5.2 to 5.5 TB/s; a large device copy reaches 5.0); 24 requests of 1 to 5 tokens x 32
+// heads: 37 to 39 us for 0.2 GB.
 #include "kda_gdr_step.h"
 
 namespace kda {
