@@ -16,10 +16,10 @@
 // Precision.  States, sums and decays are float32 (G itself is summed in float64: e^{G_i-G_j}
 // of nearby tokens must not lose the bits that far tokens take).  A product's operands go to
 // the matrix cores as sums of bf16 parts: bf16 inputs are one part and exact, float32 numbers
-// are cut into 2 parts (16 bits; one part is off by at most 2^-8 of the value, its remainder's
-// part by 2^-8 of that) or 3 (24 bits), and the part products that matter are added in
-// float32: 2 parts cost 2 (against an exact operand) or 3 instructions, 3 parts 3 or 6, where
-// the float32 matrix instruction costs 16 times a bf16 one.
+// are cut into 3 parts (24 bits: one part is off by at most 2^-8 of the value, its remainder's
+// part by 2^-8 of that, and so on), and the part products that matter are added in float32: 3
+// instructions against an exact operand, 6 against another of 3 parts, where the float32 matrix
+// instruction costs 16 times a bf16 one.
 #pragma once
 
 #include "kda_device.h"
@@ -28,10 +28,23 @@
 namespace kda {
 
 constexpr int GDR_C = 64;  // tokens per chunk
-constexpr int GDR_STATE_PARTS = 3;
+// Parts of a computed operand, on its way to the state and to the output alike.  Two parts (16
+// bits) of those that reach the output alone left it 4e-6 off in the 2-norm, which a float32
+// output shows, for 6% less of a call's time (8192 tokens x 96 heads, K = V = 128, bf16: 728 us
+// against 775).
+constexpr int GDR_PARTS = 3;
 
 // Workspace of one call; the matrices are stored in the order in which a wave loads its
-// matrix-core fragments: [.., 16-row tile][32-column step][part][lane][8].
+// matrix-core fragments: [.., fragment][part][lane][8], a fragment being a 16-row tile of 32
+// columns.
+//
+// The prefill's M and P are lower triangles: six fragments of the eight, M's and then P's, 36 KB
+// of the GDR_UNIT that every (chunk slot, value head) has.
+constexpr int GDR_UNIT = 5 * GDR_C * GDR_C;
+__device__ __forceinline__ constexpr int gdr_full(int r, int s) { return r * 2 + s; }               // tile r, step s
+__device__ __forceinline__ constexpr int gdr_lower(int r, int s) { return r < 2 ? r : 2 * r - 2 + s; }  // s <= r / 2
+constexpr int GDR_P_AT = 6 * GDR_PARTS * 512;  // where a unit's P starts
+static_assert(2 * GDR_P_AT <= GDR_UNIT, "M and P of a unit");
 struct GdrArgs {
     const void *q, *k, *v;       // [rows, HK, K], [rows, HK, K], [rows, HV, V]
     const float *g, *beta;       // [rows, HV]
@@ -45,7 +58,7 @@ struct GdrArgs {
     float scale;
     int64_t slots;               // chunk slots
     int chunks;                  // chunk slots of a batch row (no cu)
-    __bf16 *M, *P;               // [slots * HV][parts * 4096]
+    __bf16 *M, *P;               // M: [slots * HV][GDR_UNIT], with P behind it; backward: [slots * HV][parts * 4096] each
     __bf16 *Kt;                  // [slots * HK][parts of k * K * 64], float32 gradients only
     float *dec;                  // [slots * HV][4 * 64]: e^G, e^{G_C - G}, beta, unused
     // backward
@@ -105,20 +118,17 @@ __device__ __forceinline__ Parts<P> cut8(const float *x) {
     return f;
 }
 
-// acc += A B for operands given in parts: the part products i + j < L, smallest first (by
-// default all that matter beside the finer operand's last part).
-template <int L, int NA, int NB>
-__device__ __forceinline__ void mma_to(f4 &acc, const Parts<NA> &a, const Parts<NB> &b) {
+// acc += A B for operands given in parts: the part products that matter beside the finer
+// operand's last part, smallest first.
+template <int NA, int NB>
+__device__ __forceinline__ void mma(f4 &acc, const Parts<NA> &a, const Parts<NB> &b) {
+    constexpr int L = NA > NB ? NA : NB;
 #pragma unroll
     for (int s = L - 1; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i < NA; ++i)
             if (s - i >= 0 && s - i < NB)
                 acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[s - i], acc, 0, 0, 0);
-}
-template <int NA, int NB>
-__device__ __forceinline__ void mma(f4 &acc, const Parts<NA> &a, const Parts<NB> &b) {
-    mma_to<(NA > NB ? NA : NB)>(acc, a, b);
 }
 
 // Eight consecutive elements of an input as parts; zeros where !there.
@@ -138,19 +148,19 @@ __device__ __forceinline__ Parts<PK> load8(const float *p, bool there) {
     return cut8<PK>(x);
 }
 
-// A wave's fragment of a workspace matrix: tile r, step s of a matrix with two 32-column steps.
+// A wave's fragment i of a workspace matrix.
 template <int P>
-__device__ __forceinline__ Parts<P> load_frag(const __bf16 *m, int r, int s, int lane) {
+__device__ __forceinline__ Parts<P> load_frag(const __bf16 *m, int i, int lane) {
     Parts<P> f;
-    const char *from = reinterpret_cast<const char *>(m) + (r * 2 + s) * P * 1024;
+    const char *from = reinterpret_cast<const char *>(m) + i * P * 1024;
 #pragma unroll
     for (int p = 0; p < P; ++p) f.v[p] = *reinterpret_cast<const bf16x8 *>(from + (unsigned)(lane * 16) + p * 1024);
     return f;
 }
 template <int P>
-__device__ __forceinline__ void store_frag(__bf16 *m, int r, int s, int lane, const Parts<P> &f) {
+__device__ __forceinline__ void store_frag(__bf16 *m, int i, int lane, const Parts<P> &f) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x8 *>(m + ((((r * 2 + s) * P + p) * 64) + lane) * 8) = f.v[p];
+    for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x8 *>(m + (((i * P + p) * 64) + lane) * 8) = f.v[p];
 }
 
 // Operands in LDS: parts of an R x N matrix (N a multiple of 32), rows of N elements without

@@ -36,17 +36,18 @@ struct Carver {
 };
 
 size_t carve_fwd(kda::GdrArgs &a, void *base, bool fp32) {
-    const int C = kda::GDR_C, parts = fp32 ? 3 : kda::GDR_STATE_PARTS, out_parts = fp32 ? 3 : 2;
+    // the sizes that callers were told before M and P were kept without their upper fragments: the
+    // last 4 KB of a unit, and with float32 inputs the last sixth, are not used
+    const int C = kda::GDR_C;
     const int64_t units = a.slots * a.HV;
     Carver w{static_cast<char *>(base)};
-    w.take(a.M, units * parts * C * C);
-    w.take(a.P, units * out_parts * C * C);
+    w.take(a.M, units * (fp32 ? 6 * C * C : kda::GDR_UNIT));
     w.take(a.dec, units * 4 * C);
     return w.used;
 }
 
 size_t carve_bwd(kda::GdrArgs &a, void *base, bool fp32, int K) {
-    const int C = kda::GDR_C, parts = 3, turned_parts = fp32 ? 3 : 0;
+    const int C = kda::GDR_C, parts = kda::GDR_PARTS, turned_parts = fp32 ? 3 : 0;
     const int64_t units = a.slots * a.HV;
     Carver w{static_cast<char *>(base)};
     w.take(a.M, units * parts * C * C);

@@ -22,7 +22,7 @@
 namespace kda {
 namespace {
 
-constexpr int C = GDR_C, P = 3;
+constexpr int C = GDR_C, P = GDR_PARTS;
 
 // The chain of gradients: workgroups, waves and operands in flight as in the forward chain, and
 // bound alike.  Both chains together, 8192 tokens x 32 heads, K = V = 128, bf16: 751 us, 0.6 GB
@@ -88,7 +88,7 @@ __device__ __forceinline__ void gdr_bwd_chain(const GdrArgs &a, int block, __bf1
         const __bf16 *from = base + ((slot + c) * a.HV + hv) * (P * C * C);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (s == 1 || w < 2) f[s] = load_frag<P>(from, w, s, lane);
+            if (s == 1 || w < 2) f[s] = load_frag<P>(from, gdr_full(w, s), lane);
     };
     auto load_dec = [&](int c) {
         const float *dec = a.dec + ((slot + c) * a.HV + hv) * (4 * C);
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && NV == 1 ? 2 : 1) void gdr_ch
     __shared__ __attribute__((aligned(16))) __bf16 sS[P * W * KP], sX[P * W * C], sE[P * W * C], sB[P * W * C], sK[PK * C * KP], sQ[PK * C * KP], sO[PD * C * 32];
     const int block = blockIdx.x / 16 * 8 + blockIdx.x % 8;
     if (blockIdx.x / 8 % 2 == 0) gdr_bwd_chain<T, D, K, NV>(a, block, sS, sX, sE, sB, sK, sQ, sO);
-    else gdr_chain<T, float, K, P, P, NV, true>(a, block, sS, sX, sE, nullptr, sK);
+    else gdr_chain<T, float, K, NV, true>(a, block, sS, sX, sE, nullptr, sK);
 }
 
 // Columns 4 g .. + 3 and 16 + 4 g .. + 3 of a row's 32-column slice: lanes next to each other read
@@ -503,8 +503,8 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
                         kt = lds_frag_turned<PK, C, KP>(sK, 32 * s + 8 * lg, 16 * (half * CT + c), lane);
                         qt = lds_frag_turned<PK, C, KP>(sQ, 32 * s + 8 * lg, 16 * (half * CT + c), lane);
                     } else {
-                        kt = load_frag<PK>(a.Kt + kq, half * CT + c, s, lane);
-                        qt = load_frag<PK>(a.Qt + kq, half * CT + c, s, lane);
+                        kt = load_frag<PK>(a.Kt + kq, gdr_full(half * CT + c, s), lane);
+                        qt = load_frag<PK>(a.Qt + kq, gdr_full(half * CT + c, s), lane);
                     }
                     mma(dq[c], fpr, kt);
                     mma(dk[c], fac, kt);

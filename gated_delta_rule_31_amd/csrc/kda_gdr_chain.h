@@ -18,16 +18,15 @@ namespace kda {
 //
 // Bound by the dependence of a chunk's three phases while a compute unit has one workgroup (2.0
 // us a chunk, 8192 tokens x 32 heads, K = V = 128, bf16: 256 to 260 us), by the loads of the
-// operands (62 KB a chunk and workgroup, mostly from L2) and instruction issue beyond (96 heads:
+// operands (68 KB a chunk and workgroup, mostly from L2) and instruction issue beyond (96 heads:
 // 612 to 641 us, 1.2 GB from and to HBM).
 //
-// P: parts of what reaches the state, PO: parts of what reaches the output alone.  TRAIN: for the
-// gradients; every chunk's start state and corrections are kept and there is no output.  The LDS
-// arrays are the kernel's: sS [P][16 NV][K], sX and sE [P][16 NV][64], sV [PO][16 NV][64] (null for
-// TRAIN), sK [parts of k][64][K], rows of 32 at K = 16.
-template <typename T, typename OT, int K, int P, int PO, int NV, bool TRAIN>
+// TRAIN: for the gradients; every chunk's start state and corrections are kept and there is no
+// output.  The LDS arrays are the kernel's, with P = 3 parts: sS [P][16 NV][K], sX, sE and sV [P][16
+// NV][64] (sV null for TRAIN), sK [parts of k][64][K], rows of 32 at K = 16.
+template <typename T, typename OT, int K, int NV, bool TRAIN>
 __device__ __forceinline__ void gdr_chain(const GdrArgs &a, int block, __bf16 *sS, __bf16 *sX, __bf16 *sE, __bf16 *sV, __bf16 *sK) {
-    constexpr int C = GDR_C;
+    constexpr int C = GDR_C, P = GDR_PARTS, UNIT = TRAIN ? P * C * C : GDR_UNIT;
     constexpr int PK = gdr_input_parts<T>(), KP = K < 32 ? 32 : K, KS = KP / 32, NC = (K / 16 + 3) / 4, W = 16 * NV, SZ = sizeof(T);
     int vb, hv, n;
     if (!gdr_pair(a, block, a.V / W, vb, hv, n)) return;
@@ -64,12 +63,10 @@ __device__ __forceinline__ void gdr_chain(const GdrArgs &a, int block, __bf16 *s
     const unsigned kcol = (K < 32 ? lg % 2 * 8 : 8 * lg) * SZ;  // beside a width of 16 the state's parts are zero
     const unsigned krow = (16 * w + lr) * kstep + kcol, r0 = 16 * w + 4 * lg;
     Parts<PK> k[KS], q[KS];
-    Parts<P> m[2];
-    Parts<PO> p[2];
+    Parts<P> m[2], p[2];
     // rows 0..31 have nothing in M's and P's second 32 columns: waves 0 and 1 multiply zeros that they
     // hold, while the others work, so that a phase has no branches and its parts are interleaved
-    m[1] = Parts<P>{};
-    p[1] = Parts<PO>{};
+    m[1] = p[1] = Parts<P>{};
     f4 b, end, beta, nb, nend, nbeta;
     Parts<PK> v, nv;
     bf16x8 one[NV];
@@ -90,16 +87,16 @@ __device__ __forceinline__ void gdr_chain(const GdrArgs &a, int block, __bf16 *s
         }
     };
     auto load_m = [&](int c) {
-        const __bf16 *from = a.M + ((slot + c) * a.HV + hv) * (P * C * C);
+        const __bf16 *from = a.M + ((slot + c) * a.HV + hv) * UNIT;
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (s == 0 || w >= 2) m[s] = load_frag<P>(from, w, s, lane);
+            if (s == 0 || w >= 2) m[s] = load_frag<P>(from, gdr_lower(w, s), lane);
     };
     auto load_p = [&](int c) {
-        const __bf16 *from = a.P + ((slot + c) * a.HV + hv) * (PO * C * C);
+        const __bf16 *from = a.M + ((slot + c) * a.HV + hv) * UNIT + GDR_P_AT;
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (!TRAIN && (s == 0 || w >= 2)) p[s] = load_frag<PO>(from, w, s, lane);
+            if (!TRAIN && (s == 0 || w >= 2)) p[s] = load_frag<P>(from, gdr_lower(w, s), lane);
     };
     auto load_rows = [&](int c) {  // into the second set
         const float *dec = a.dec + ((slot + c) * a.HV + hv) * (4 * C);
@@ -148,7 +145,7 @@ __device__ __forceinline__ void gdr_chain(const GdrArgs &a, int block, __bf16 *s
             for (int u = 0; u < NV; ++u) {
                 const Parts<P> f = lds_frag<P, W, KP>(sS, 16 * u + lr, 32 * s + 8 * lg);
                 mma(x[u], k[s], f);
-                if (!TRAIN) mma_to<PO>(y[u], f, q[s]);  // columns by tokens: a lane gets four columns of a token
+                if (!TRAIN) mma(y[u], f, q[s]);  // columns by tokens: a lane gets four columns of a token
             }
         load_kq(next);
 #pragma unroll
@@ -167,7 +164,7 @@ __device__ __forceinline__ void gdr_chain(const GdrArgs &a, int block, __bf16 *s
         for (int u = 0; u < NV; ++u) {
             const f4 vn = beta * x[u];
             lds_put4<P, W, C>(sE, 16 * u + lr, r0, end * vn);
-            if (!TRAIN) lds_put4<PO, W, C>(sV, 16 * u + lr, r0, vn);
+            if (!TRAIN) lds_put4<P, W, C>(sV, 16 * u + lr, r0, vn);
         }
         gdr_lds_barrier();
 #pragma unroll
@@ -197,7 +194,7 @@ __device__ __forceinline__ void gdr_chain(const GdrArgs &a, int block, __bf16 *s
                 y[u] *= blr;
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
-                    mma_to<PO>(y[u], lds_frag<PO, W, C>(sV, 16 * u + lr, 32 * s + 8 * lg), p[s]);
+                    mma(y[u], lds_frag<P, W, C>(sV, 16 * u + lr, 32 * s + 8 * lg), p[s]);
                 y[u] *= a.scale;
             }
             load_p(next);

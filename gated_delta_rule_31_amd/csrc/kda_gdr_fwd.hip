@@ -8,7 +8,7 @@
 namespace kda {
 namespace {
 
-constexpr int C = GDR_C;
+constexpr int C = GDR_C, P = GDR_PARTS;
 
 // Eight elements down a column of an LDS tile, as parts.
 template <int P, typename T>
@@ -27,9 +27,9 @@ __device__ __forceinline__ int block_at(int p, int r) { return (p * (p + 1) / 2 
 // (chunk slot, key head) that writes K^T and Q^T.  Wave w owns token rows 16w..16w+15 until A
 // is there, then the column blocks w of M.  33 KB of LDS, so that four workgroups share a
 // compute unit: a workgroup mostly waits (for its rows, for substitution and products that
-// follow one another), and what it writes, 30 KB, is more than it reads.  8192 tokens x 96
+// follow one another), and what it writes, 37 KB, is more than it reads.  8192 tokens x 96
 // heads, K = 128, bf16: 190 to 204 us, 0.19 GB read and 0.39 GB written.
-template <typename T, int K, int P, int PO, bool BWD>
+template <typename T, int K, bool BWD>
 __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
     constexpr int PK = gdr_input_parts<T>(), KP = K < 32 ? 32 : K, LK = KP + 8, KS = KP / 32, VEC = 16 / sizeof(T);
     constexpr bool TURNED = BWD && PK > 1;  // bf16 rows are turned in LDS where they are used
@@ -62,7 +62,7 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
             __syncthreads();
             __bf16 *to = (which ? a.Qt : a.Kt) + key * (PK * K * C);
             for (int i = w; i < K / 16 * 2; i += 4)
-                store_frag<PK>(to, i / 2, i % 2, lane, column8<PK>(tile, LK, 32 * (i % 2) + 8 * lg, 16 * (i / 2) + lr));
+                store_frag<PK>(to, gdr_full(i / 2, i % 2), lane, column8<PK>(tile, LK, 32 * (i % 2) + 8 * lg, 16 * (i / 2) + lr));
         }
         return;
     }
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
         for (int s = 0; s < 2; ++s)
             if (s <= w / 2) {
                 row8f(sM, s, x8);
-                store_frag<PO>(a.P + unit * (PO * C * C), w, s, lane, cut8<PO>(x8));
+                store_frag<P>(a.M + unit * GDR_UNIT + GDR_P_AT, gdr_lower(w, s), lane, cut8<P>(x8));
             }
     // the inverse of block w of 1 + A beta on the diagonal by substitution, a column a lane: as
     // soon as row m of the inverse is there its part is taken off all rows below
@@ -215,22 +215,22 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
     for (int s = 0; s < 2; ++s) {
         if (s <= w / 2) {
             row8f(sM, s, x8);
-            store_frag<P>(a.M + unit * (P * C * C), w, s, lane, cut8<P>(x8));
+            store_frag<P>(a.M + unit * (BWD ? P * C * C : GDR_UNIT), gdr_lower(w, s), lane, cut8<P>(x8));
         }
         if (BWD && s >= w / 2) {
             column8f(sM, s, x8);
-            store_frag<P>(a.Mt + unit * (P * C * C), w, s, lane, cut8<P>(x8));
+            store_frag<P>(a.Mt + unit * (P * C * C), gdr_full(w, s), lane, cut8<P>(x8));
             column8f(sP, s, x8);
-            store_frag<P>(a.P + unit * (P * C * C), w, s, lane, cut8<P>(x8));
+            store_frag<P>(a.P + unit * (P * C * C), gdr_full(w, s), lane, cut8<P>(x8));
         }
     }
 }
 
-template <typename T, typename OT, int K, int P, int PO, int NV>
+template <typename T, typename OT, int K, int NV>
 __global__ __launch_bounds__(256) void gdr_chain_kernel(const GdrArgs a) {
     constexpr int PK = gdr_input_parts<T>(), KP = K < 32 ? 32 : K, W = 16 * NV;
-    __shared__ __attribute__((aligned(16))) __bf16 sS[P * W * KP], sX[P * W * C], sE[P * W * C], sV[PO * W * C], sK[PK * C * KP];
-    gdr_chain<T, OT, K, P, PO, NV, false>(a, blockIdx.x, sS, sX, sE, sV, sK);
+    __shared__ __attribute__((aligned(16))) __bf16 sS[P * W * KP], sX[P * W * C], sE[P * W * C], sV[P * W * C], sK[PK * C * KP];
+    gdr_chain<T, OT, K, NV, false>(a, blockIdx.x, sS, sX, sE, sV, sK);
 }
 
 template <typename F>
@@ -244,19 +244,19 @@ hipError_t by_width(int K, F f) {
     return hipErrorNotSupported;
 }
 
-template <typename T, int P, int PO, bool BWD>
+template <typename T, bool BWD>
 hipError_t prep(const GdrArgs &a, int K, hipStream_t stream) {
     return by_width(K, [&](auto k) {
-        hipLaunchKernelGGL((gdr_prep_kernel<T, decltype(k)::value, P, PO, BWD>), dim3((unsigned)((a.slots * a.HK + 7) / 8 * 8 * (a.group + (BWD && sizeof(T) == 4)))), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((gdr_prep_kernel<T, decltype(k)::value, BWD>), dim3((unsigned)((a.slots * a.HK + 7) / 8 * 8 * (a.group + (BWD && sizeof(T) == 4)))), dim3(256), 0, stream, a);
         return hipGetLastError();
     });
 }
-template <typename T, typename OT, int P, int PO>
+template <typename T, typename OT>
 hipError_t chain(const GdrArgs &a, int K, hipStream_t stream) {
     return by_width(K, [&](auto k) {
         constexpr int KK = decltype(k)::value;
-        if (gdr_column_tiles(a) == 2) hipLaunchKernelGGL((gdr_chain_kernel<T, OT, KK, P, PO, 2>), dim3((unsigned)gdr_pair_blocks(a, a.V / 32)), dim3(256), 0, stream, a);
-        else hipLaunchKernelGGL((gdr_chain_kernel<T, OT, KK, P, PO, 1>), dim3((unsigned)gdr_pair_blocks(a, a.V / 16)), dim3(256), 0, stream, a);
+        if (gdr_column_tiles(a) == 2) hipLaunchKernelGGL((gdr_chain_kernel<T, OT, KK, 2>), dim3((unsigned)gdr_pair_blocks(a, a.V / 32)), dim3(256), 0, stream, a);
+        else hipLaunchKernelGGL((gdr_chain_kernel<T, OT, KK, 1>), dim3((unsigned)gdr_pair_blocks(a, a.V / 16)), dim3(256), 0, stream, a);
         return hipGetLastError();
     });
 }
@@ -264,13 +264,13 @@ hipError_t chain(const GdrArgs &a, int K, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_gdr_prep(const GdrArgs &a, bool fp32, int K, bool bwd, hipStream_t stream) {
-    if (bwd) return fp32 ? prep<float, 3, 3, true>(a, K, stream) : prep<__bf16, 3, 3, true>(a, K, stream);
-    return fp32 ? prep<float, 3, 3, false>(a, K, stream) : prep<__bf16, GDR_STATE_PARTS, 2, false>(a, K, stream);
+    if (bwd) return fp32 ? prep<float, true>(a, K, stream) : prep<__bf16, true>(a, K, stream);
+    return fp32 ? prep<float, false>(a, K, stream) : prep<__bf16, false>(a, K, stream);
 }
 
 hipError_t launch_gdr_fwd_chain(const GdrArgs &a, bool fp32, int K, hipStream_t stream) {
-    if (a.out_bf16) return fp32 ? chain<float, __bf16, 3, 3>(a, K, stream) : chain<__bf16, __bf16, GDR_STATE_PARTS, 2>(a, K, stream);
-    return fp32 ? chain<float, float, 3, 3>(a, K, stream) : chain<__bf16, float, GDR_STATE_PARTS, 2>(a, K, stream);
+    if (a.out_bf16) return fp32 ? chain<float, __bf16>(a, K, stream) : chain<__bf16, __bf16>(a, K, stream);
+    return fp32 ? chain<float, float>(a, K, stream) : chain<__bf16, float>(a, K, stream);
 }
 
 }  // namespace kda

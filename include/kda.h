@@ -362,10 +362,9 @@ size_t kda_noalloc_scratch_bytes(void);
  * tensors; the results are then unspecified).  The workspace is scratch as in kda_chunk_fwd
  * (required; at least kda_gdr_chunk_fwd_workspace_size bytes, which is 0 for a shape that is
  * not supported).  bf16 inputs are exact on the matrix cores; what is computed from them enters
- * the products with 24 mantissa bits on its way to the state and, with bf16 inputs, with 16 on
- * its way to `out` alone, and is summed in float32: final_state is off by about 1e-6 of its norm
- * at most, out by about 1e-5 before it is rounded to its type.  Values that are not finite may
- * reach other tokens of their chunk and other columns of their head.
+ * the products with 24 mantissa bits and is summed in float32: final_state, and out before it is
+ * rounded to its type, are off by about 1e-6 of their norm at most.  Values that are not finite
+ * may reach other tokens of their chunk and other columns of their head.
  */
 size_t kda_gdr_chunk_fwd_workspace_size(kda_dtype in_dtype, int B, int64_t T, int num_seqs, int varlen, int HK,
                                         int HV, int K, int V);

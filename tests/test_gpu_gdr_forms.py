@@ -1,0 +1,43 @@
+"""GPU parity of the gated delta rule in the forms and at the sizes that it is trained and served
+with: the bits that a float32 output keeps, two column tiles a workgroup at full width, mixed
+types, packed batches that are padded behind their last sequence.
+
+Tolerances, from the roundings that the kernels make.  Operands of the matrix cores are exact
+(bf16 inputs) or off by at most 2^-24 of the value (three bf16 parts), accumulators and the rest
+are float32, whose roundings are at most 2^-24 and, as they are independent, 2^-24 / sqrt(3) = 3.4e-8
+in the mean square.  On the way to a chunk's end state stand about 40 of them (12 matrix instructions
+and a scaling for X, 12 for M (beta X), 6 for K^T E, the cuts and the decays), as many in M itself,
+and 30 more on the way to an output (12 for Q S, 12 for P Vn, the cuts, three factors): sqrt(110)
+3.4e-8 = 3.6e-7 of the partial sums, which are somewhat larger than what they end as.  NORM, 1e-6 of
+an output's or a state's 2-norm, leaves a factor of three for that.  An operand of two parts (16 bits) is
+off by 2^-16 at most and 2^-18 = 3.8e-6 in the mean square, and does not pass it.  The largest element
+is held to 1e-5, as with float32 inputs elsewhere.
+"""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_31_amd as kda
+from tests import gdr_reference as ref
+from tests.helpers import err_fp32, f64
+from tests.test_gpu_gdr import NAMES, _cotangents, _fwd, _gpu, _norm
+
+pytestmark = pytest.mark.gpu
+
+NORM = 1e-6
+
+
+def _full_bits(out, final, want, what=""):
+    for name, x, y in (("out", out, want[0]), ("state", final, want[1])):
+        assert x.dtype == torch.float32 and np.all(np.isfinite(f64(x))), (what, name)
+        n, e = _norm(x, y), err_fp32(x, y)
+        assert n <= NORM and e <= 1e-5, "%s %s: %.2e in norm, %.2e" % (what, name, n, e)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("HK,HV,K,V,lens", [(2, 4, 128, 128, None), (1, 3, 16, 16, None), (1, 2, 32, 64, None), (2, 2, 64, 32, [70, 0, 129, 1])])
+def test_fwd_float32_output_keeps_24_bits(dtype, HK, HV, K, V, lens):
+    """The state's part of an output, the chunk's own and both, with inputs in either type."""
+    i = ref.make(1, 200, HK, HV, K, V, dtype, seed=50 + K, seqlens=lens)
+    out, final = _fwd(i, K ** -0.5, out_dtype=torch.float32)
+    _full_bits(out, final, ref.scan(i, K ** -0.5))
