@@ -268,21 +268,29 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
     const int64_t slot = unit / a.HK;
     int64_t row;
     int len;
-    if (a.cu && slot == a.slots - 1) {  // rows behind the last sequence have no gradient
+    const int w8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = w8 & 3, half = w8 >> 2;
+    if (a.cu) {
+        // rows behind the last sequence have no gradient: each slot clears 64 of them, the last slot
+        // the first ones.  There are T / 64 + N slots, enough for all T rows, and those counted from
+        // the last one hold no chunk, but for one at most.  1000 of 8192 rows used, 16 key and 32 value
+        // heads, K = V = 128, bf16: 241 us a call, where one workgroup a key head that clears all of
+        // them takes 2127 (and a full bucket 1290).
         int64_t l, s;
         gdr_sequence(a, a.N - 1, row, l, s);
-        row += l;
-        const int64_t each = (int64_t)a.group * a.V + 2 * K + 2 * a.group, left = (a.T - row) * each;
-        for (int64_t i = threadIdx.x; i < left; i += 512) {
-            const int64_t t = row + i / each;
-            const int c = (int)(i % each), gv = a.group * a.V, h = c - gv - 2 * K;
-            if (c < gv) st_out(a.dv, a.grad_bf16, (t * a.HV + hk * a.group) * a.V + c, 0.f);
-            else if (h < 0) st_out(c < gv + K ? a.dq : a.dk, a.grad_bf16, (t * a.HK + hk) * K + (c - gv) % K, 0.f);
-            else (h < a.group ? a.dg : a.dbeta)[t * a.HV + hk * a.group + h % a.group] = 0.f;
+        const int64_t first = row + l + (a.slots - 1 - slot) * C;
+        const unsigned es = a.grad_bf16 ? 2 : 4;
+        auto clear = [&](void *x, int64_t at, unsigned n) {  // n elements of a row, on 16-byte borders
+            char *to = static_cast<char *>(x) + at * es;
+            for (unsigned b = (threadIdx.x & 63) * 16; b < n * es; b += 1024) *reinterpret_cast<f4 *>(to + b) = f4{};
+        };
+        for (int64_t t = first + w8; t < first + C && t < a.T; t += 8) {
+            clear(a.dq, (t * a.HK + hk) * K, K);
+            clear(a.dk, (t * a.HK + hk) * K, K);
+            clear(a.dv, (t * a.HV + hk * a.group) * a.V, a.group * a.V);
+            for (int h = threadIdx.x & 63; h < a.group; h += 64) a.dg[t * a.HV + hk * a.group + h] = a.dbeta[t * a.HV + hk * a.group + h] = 0.f;
         }
     }
     if (!gdr_chunk(a, slot, row, len)) return;
-    const int w8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = w8 & 3, half = w8 >> 2;
     const int V = a.V, slices = (V + 31) / 32;
     // addresses are one of the wave's and a lane's 32-bit offset; rows behind the end read the last
     // row, where dO is taken as 0 and beta is 0

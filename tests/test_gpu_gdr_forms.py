@@ -41,3 +41,54 @@ def test_fwd_float32_output_keeps_24_bits(dtype, HK, HV, K, V, lens):
     i = ref.make(1, 200, HK, HV, K, V, dtype, seed=50 + K, seqlens=lens)
     out, final = _fwd(i, K ** -0.5, out_dtype=torch.float32)
     _full_bits(out, final, ref.scan(i, K ** -0.5))
+
+
+# ------------------------------------------------------------------- packed and padded to a bucket
+
+def _padded(T, used, HK, HV, K, V, dtype, seed, cuts=(0.3, 0.55)):
+    """A packed batch of three sequences in the first `used` rows of T: what lies behind them is what was there before."""
+    lens = np.diff([0] + [int(used * c) for c in cuts] + [used])
+    i = ref.make(1, used, HK, HV, K, V, dtype, seed=seed, seqlens=list(lens))
+    d = _gpu(i)
+    more = lambda x: torch.cat([x, x.new_full((1, T - used, *x.shape[2:]), float("nan"))], 1)  # noqa: E731
+    d_out, d_fin = _cotangents(i, seed + 1, dtype)
+    return d, {n: more(d[n]) for n in ("q", "k", "v", "g", "beta")}, d_out.cuda(), more(d_out.cuda()), d_fin.cuda()
+
+
+@pytest.mark.parametrize("T,used", [(129, 0), (64, 1), (65, 1), (200, 199), (192, 130), (192, 128), (640, 65), (1000, 63)])
+@pytest.mark.parametrize("dtype,grad,HK,HV,K,V", [(torch.bfloat16, torch.bfloat16, 2, 4, 128, 128), (torch.float32, torch.float32, 1, 3, 16, 16),
+                                                  (torch.bfloat16, torch.float32, 1, 70, 32, 64)])
+def test_bwd_padded_bucket(T, used, dtype, grad, HK, HV, K, V):
+    """Gradients behind the last sequence are zeros, and those of its rows the ones of the batch without them, at
+    tails that end inside a chunk, begin inside one, and are all there is."""
+    d, wide, d_out, wide_out, d_fin = _padded(T, used, HK, HV, K, V, dtype, T + used)
+    kw = dict(initial_state=d["s0"], d_final_state=d_fin, cu_seqlens=d["cu"], grad_dtype=grad)
+    got = kda.gdr_chunk_bwd(*wide.values(), wide_out, **kw)
+    want = kda.gdr_chunk_bwd(*[d[n] for n in wide], d_out, **kw)
+    for name, x, y in zip(NAMES[:5], got, want):
+        assert torch.equal(x[:, :used], y), name
+        assert not x[:, used:].any(), name  # NaN counts as something
+    assert torch.equal(got[5], want[5] if used else d_fin)
+
+
+def test_bwd_padding_is_not_the_call():
+    """A bucket of which an eighth is used costs less than a full one (the slots without a chunk clear the rest)."""
+    def call(used):
+        _, wide, _, d_out, d_fin = (x for x in _padded(8192, used, 16, 32, 128, 128, torch.bfloat16, 60))
+        cu = torch.tensor([0, used // 3, used], dtype=torch.int32, device="cuda")
+        wide = {n: x.nan_to_num() for n, x in wide.items()}
+        return lambda: kda.gdr_chunk_bwd(*wide.values(), d_out.nan_to_num(), cu_seqlens=cu)
+
+    def time(f):
+        out = []
+        for _ in range(7):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            f()
+            b.record()
+            b.synchronize()
+            out.append(a.elapsed_time(b))
+        return sorted(out)[3]
+    few, full = time(call(1000)), time(call(8191))
+    print("1000 of 8192 rows %.0f us, 8191 %.0f us" % (1e3 * few, 1e3 * full))
+    assert few < full
