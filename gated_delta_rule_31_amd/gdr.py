@@ -174,13 +174,18 @@ def gdr_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     return dq, dk, dv, dg, dbeta, ds0
 
 
+def _zeros_behind(q, k, v, g, beta, initial_state, cu_seqlens, scale):
+    """``gdr_chunk_fwd`` with zeros behind the last packed sequence."""
+    out = None if cu_seqlens is None else torch.zeros_like(v, memory_format=torch.contiguous_format)
+    return gdr_chunk_fwd(q, k, v, g, beta, initial_state=initial_state, cu_seqlens=cu_seqlens, scale=scale, out=out)
+
+
 class _GatedDeltaRuleFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, g, beta, initial_state, cu_seqlens, scale):
         d = lambda x: None if x is None else x.detach()  # noqa: E731
         with torch.no_grad():
-            out = None if cu_seqlens is None else torch.zeros_like(v, memory_format=torch.contiguous_format)
-            out, fin = gdr_chunk_fwd(d(q), d(k), d(v), d(g), d(beta), initial_state=d(initial_state), cu_seqlens=cu_seqlens, scale=scale, out=out)
+            out, fin = _zeros_behind(d(q), d(k), d(v), d(g), d(beta), d(initial_state), cu_seqlens, scale)
         ctx.save_for_backward(q, k, v, g, beta, initial_state, cu_seqlens)
         ctx.scale = scale
         ctx.set_materialize_grads(False)
@@ -202,11 +207,11 @@ class _GatedDeltaRuleFn(torch.autograd.Function):
 def gated_delta_rule(q, k, v, g, beta, initial_state=None, cu_seqlens=None, scale: float = 1.0):
     """``gdr_chunk_fwd`` as a function of its inputs: (out in the inputs' dtype, final_state), recorded
     for autograd when any of q, k, v, g, beta or initial_state requires grad (through
-    ``gdr_chunk_bwd``).  Rows of out behind the last packed sequence are zeros where the call is
-    recorded."""
+    ``gdr_chunk_bwd``).  Rows of out behind the last packed sequence are zeros, whether the call is
+    recorded or not."""
     if _needs_grad(q, k, v, g, beta, initial_state):
         return _GatedDeltaRuleFn.apply(q, k, v, g, beta, initial_state, cu_seqlens, float(scale))
-    return gdr_chunk_fwd(q, k, v, g, beta, initial_state=initial_state, cu_seqlens=cu_seqlens, scale=scale)
+    return _zeros_behind(q, k, v, g, beta, initial_state, cu_seqlens, scale)
 
 
 def gdr_recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, states: torch.Tensor,

@@ -92,3 +92,24 @@ def test_bwd_padding_is_not_the_call():
     few, full = time(call(1000)), time(call(8191))
     print("1000 of 8192 rows %.0f us, 8191 %.0f us" % (1e3 * few, 1e3 * full))
     assert few < full
+
+
+def test_gated_delta_rule_is_one_function_recorded_or_not():
+    """A padded packed batch gives the same rows, those behind the last sequence among them, in training, without
+    gradients and under no_grad, whatever the memory held that the output is made in."""
+    d, wide, _, _, _ = _padded(300, 130, 2, 4, 32, 64, torch.bfloat16, 70)
+    leaves = [x.clone().requires_grad_() for x in wide.values()]
+
+    def fresh(f):
+        gone = [torch.full_like(wide["v"], float("nan")) for _ in range(4)]  # what the next outputs are made in
+        del gone
+        return f()
+    call = lambda xs: kda.gated_delta_rule(*xs, initial_state=d["s0"], cu_seqlens=d["cu"], scale=0.5)  # noqa: E731
+    recorded = fresh(lambda: call(leaves))
+    assert recorded[0].requires_grad
+    with torch.no_grad():
+        under = fresh(lambda: call(leaves))
+    plain = fresh(lambda: call(list(wide.values())))
+    for out, fin in (under, plain):
+        assert not out.requires_grad and torch.equal(out, recorded[0]) and torch.equal(fin, recorded[1])
+    assert not plain[0][:, 130:].any() and plain[0][:, :130].any()
