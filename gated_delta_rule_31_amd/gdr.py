@@ -21,8 +21,9 @@ import torch
 from . import _check, _dtype_code, _load, _needs_grad
 
 
-def _input(x: Optional[torch.Tensor], name: str, like: Optional[torch.Tensor] = None, dtype=None) -> Optional[torch.Tensor]:
-    """A dense tensor on the device of ``like``, on a 16-byte border (copied to one if need be)."""
+def _input(x: Optional[torch.Tensor], name: str, like: Optional[torch.Tensor] = None, dtype=None, border: int = 16) -> Optional[torch.Tensor]:
+    """A dense tensor on the device of ``like``, on a border of ``border`` bytes (copied to one if need be):
+    16 for what the kernels read in wide loads, 4 for what they read number by number."""
     if x is None:
         return None
     if not isinstance(x, torch.Tensor):
@@ -38,7 +39,7 @@ def _input(x: Optional[torch.Tensor], name: str, like: Optional[torch.Tensor] = 
         raise ValueError("%s requires grad: the raw kernels do not record autograd; use gated_delta_rule, or call gdr_chunk_bwd yourself" % name)
     if not x.is_contiguous():
         x = x.contiguous()
-    return x.clone() if x.data_ptr() % 16 else x
+    return x.clone() if x.data_ptr() % border else x
 
 
 def _p(x: Optional[torch.Tensor]):
@@ -83,9 +84,9 @@ def _chunk_inputs(q, k, v, g, beta, initial_state, cu_seqlens):
     if q is None:
         raise TypeError("q must be a torch.Tensor")
     k, v = _input(k, "k", q, q.dtype), _input(v, "v", q, q.dtype)
-    g, beta = _input(g, "g", q, torch.float32), _input(beta, "beta", q, torch.float32)
+    g, beta = _input(g, "g", q, torch.float32, 4), _input(beta, "beta", q, torch.float32, 4)
     initial_state = _input(initial_state, "initial_state", q, torch.float32)
-    cu_seqlens = _input(cu_seqlens, "cu_seqlens", q, torch.int32)
+    cu_seqlens = _input(cu_seqlens, "cu_seqlens", q, torch.int32, 4)
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k must be [B, T, HK, K] and v [B, T, HV, V]")
     B, T, HK, K = q.shape
@@ -234,8 +235,10 @@ def gdr_recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: tor
     if q is None:
         raise TypeError("q must be a torch.Tensor")
     k, v = _input(k, "k", q, q.dtype), _input(v, "v", q, q.dtype)
-    g, beta = _input(g, "g", q, torch.float32), _input(beta, "beta", q, torch.float32)
-    slots, start, lengths = _input(slots, "slots", q, torch.int32), _input(start, "start", q, torch.int32), _input(lengths, "lengths", q, torch.int32)
+    g, beta = _input(g, "g", q, torch.float32, 4), _input(beta, "beta", q, torch.float32, 4)
+    if g.dim() == 4:  # decays per channel are read in wide loads
+        g = _input(g, "g", q, torch.float32)
+    slots, start, lengths = (_input(x, n, q, torch.int32, 4) for x, n in ((slots, "slots"), (start, "start"), (lengths, "lengths")))
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k must be [B, S, HK, K] and v [B, S, HV, V]")
     B, S, HK, K = q.shape
@@ -280,11 +283,11 @@ def draft_verify(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uniform
     from max(p - q, 0) where a draft was refused (from p if that is nothing), from p where none
     was; in whole weights of 2^-44, so that no order of summation changes it.  Returns (tokens
     int32 [B,D+1]: the drafts that hold, the token drawn, then -1; accepted int32 [B])."""
-    p = _input(target_probs, "target_probs", None, torch.float32)
+    p = _input(target_probs, "target_probs", None, torch.float32, 4)
     if p is None:
         raise TypeError("target_probs must be a torch.Tensor")
-    x, u = _input(draft_tokens, "draft_tokens", p, torch.int32), _input(uniforms, "uniforms", p, torch.float32)
-    q, lengths = _input(draft_probs, "draft_probs", p, torch.float32), _input(lengths, "lengths", p, torch.int32)
+    x, u = _input(draft_tokens, "draft_tokens", p, torch.int32, 4), _input(uniforms, "uniforms", p, torch.float32, 4)
+    q, lengths = _input(draft_probs, "draft_probs", p, torch.float32, 4), _input(lengths, "lengths", p, torch.int32, 4)
     if p.dim() != 3 or p.shape[1] < 1:
         raise ValueError("target_probs must be [B, D + 1, vocab]")
     B, D, vocab = p.shape[0], p.shape[1] - 1, p.shape[2]

@@ -113,3 +113,57 @@ def test_gated_delta_rule_is_one_function_recorded_or_not():
     for out, fin in (under, plain):
         assert not out.requires_grad and torch.equal(out, recorded[0]) and torch.equal(fin, recorded[1])
     assert not plain[0][:, 130:].any() and plain[0][:, :130].any()
+
+
+# ------------------------------------------------------------------- views off a 16-byte border
+
+def _off(x, n=1):
+    """x's values n elements behind a 16-byte border."""
+    flat = torch.empty(x.numel() + n, dtype=x.dtype, device="cuda")
+    flat[n:] = x.reshape(-1)
+    return flat[n:].reshape(x.shape)
+
+
+@pytest.mark.parametrize("drawn", [True, False])
+def test_verify_takes_views_as_they_are(drawn):
+    """Requests behind the first of an odd vocabulary start off a 16-byte border: nothing of them is copied."""
+    gen = torch.Generator(device="cuda").manual_seed(80)
+    B, D, vocab = 6, 2, 50001
+    p = torch.softmax(2 * torch.randn(B + 1, D + 1, vocab, generator=gen, device="cuda"), -1)[1:]
+    q = torch.softmax(2 * torch.randn(B + 1, D, vocab, generator=gen, device="cuda"), -1)[1:]
+    x = torch.randint(0, vocab, (B + 1, D), generator=gen, device="cuda").to(torch.int32)[1:]
+    u = torch.rand(B + 1, D + 1, generator=gen, device="cuda")[1:]
+    n = torch.tensor([9, 2, 2, 1, 0, 3, 2], dtype=torch.int32, device="cuda")[1:]
+    assert p.data_ptr() % 16 and n.data_ptr() % 16
+    kw = dict(draft_probs=q if drawn else None, lengths=n)
+    kda.draft_verify(p, x, u, **kw)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    tokens, accepted = kda.draft_verify(p, x, u, **kw)
+    assert torch.cuda.max_memory_allocated() - before < 1 << 20
+    wt, wa = ref.verify(p.cpu(), x.cpu(), u.cpu(), q.cpu() if drawn else None, n.cpu())
+    assert np.array_equal(tokens.cpu().numpy(), wt) and np.array_equal(accepted.cpu().numpy(), wa)
+
+
+def test_calls_take_numbers_off_the_border():
+    """What is read number by number (decays and strengths per head, offsets, slots, lengths) may start on any
+    element; decays per channel, which are read in wide loads, are moved to a border."""
+    d = _gpu(ref.make(1, 130, 2, 4, 32, 32, torch.bfloat16, seed=81, seqlens=[70, 60]))
+    d_out, d_fin = _cotangents(d, 82)
+    args = [d[n] for n in ("q", "k", "v", "g", "beta")]
+    off = args[:3] + [_off(d["g"]), _off(d["beta"], 3)]
+    for f, more in ((kda.gdr_chunk_fwd, ()), (kda.gdr_chunk_bwd, (d_out.cuda(),))):
+        want = f(*args, *more, initial_state=d["s0"], cu_seqlens=d["cu"])
+        got = f(*off, *more, initial_state=d["s0"], cu_seqlens=_off(d["cu"]))
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+    for channels in (False, True):
+        q, k, v, beta = (d[n][0, :9].reshape(3, 3, *d[n].shape[2:]).contiguous() for n in ("q", "k", "v", "beta"))
+        g = -torch.rand(3, 3, 4, *((32,) if channels else ()), device="cuda")
+        slots = torch.arange(9, dtype=torch.int32, device="cuda").reshape(3, 3)
+        start, lengths = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 2, 1], [3, 1, 2]))
+        states = torch.randn(9, 4, 32, 32, device="cuda")
+        a, b = states.clone(), states.clone()
+        want = kda.gdr_recurrent_step(q, k, v, g, beta, a, slots=slots, start=start, lengths=lengths)
+        got = kda.gdr_recurrent_step(q, k, v, _off(g), _off(beta), b, slots=_off(slots), start=_off(start, 3), lengths=_off(lengths, 2))
+        assert torch.equal(want, got) and torch.equal(a, b)
