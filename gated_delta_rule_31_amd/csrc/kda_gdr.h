@@ -219,6 +219,15 @@ __device__ __forceinline__ V at_offset(const void *base, unsigned bytes) {
 // global loads and stores stay in flight across it.
 __device__ __forceinline__ void gdr_lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// Between LDS writes and reads by which lanes of one wave hand values to each other.  A wave's LDS
+// instructions are carried out in order, so nothing has to be waited for: it keeps the compiler
+// from moving one past the other where it could tell a lane's own addresses apart.
+__device__ __forceinline__ void gdr_wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Sequence n: its first token's row, its length and its first chunk slot.  Packed offsets
 // are brought into [0, T] and into order, so that no offset a caller passes reads or writes
 // outside the tensors; slots of different sequences are disjoint and below T / C + N.

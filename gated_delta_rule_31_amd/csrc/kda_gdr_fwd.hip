@@ -25,7 +25,7 @@ __device__ __forceinline__ int block_at(int p, int r) { return (p * (p + 1) / 2 
 
 // One workgroup of four waves per (chunk slot, value head), and for float32 gradients one per
 // (chunk slot, key head) that writes K^T and Q^T.  Wave w owns token rows 16w..16w+15 until A
-// is there, then the column blocks w of M.  33 KB of LDS, so that four workgroups share a
+// is there, then the column blocks w of M.  38 KB of LDS, so that four workgroups share a
 // compute unit: a workgroup mostly waits (for its rows, for substitution and products that
 // follow one another), and what it writes, 37 KB, is more than it reads.  8192 tokens x 96
 // heads, K = 128, bf16: 190 to 204 us, 0.19 GB read and 0.39 GB written.
@@ -35,7 +35,7 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
     constexpr bool TURNED = BWD && PK > 1;  // bf16 rows are turned in LDS where they are used
     constexpr int WORK = 2 * BLOCKS * 16 * LB * 4, BYTES = TURNED && C * LK * (int)sizeof(T) > WORK ? C * LK * (int)sizeof(T) : WORK;
     __shared__ __attribute__((aligned(16))) char shared[BYTES];
-    __shared__ __attribute__((aligned(16))) float sD[4][16 * LB], sP[BWD ? BLOCKS * 16 * LB : 4];
+    __shared__ __attribute__((aligned(16))) float sD[4][16 * LB], sI[4][16 * LB], sP[BWD ? BLOCKS * 16 * LB : 4];
     __shared__ double sG[4][C];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), lr = lane & 15, lg = lane >> 4;
     const T *q = static_cast<const T *>(a.q), *k = static_cast<const T *>(a.k);
@@ -101,6 +101,7 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
         if (lane >= d) g += up;
     }
     sG[w][lane] = g;  // every wave has its own copy: no barrier
+    gdr_wave_fence();
     if (w == 0) {
         const double last = __shfl(g, 63);
         float *dec = a.dec + unit * 4 * C;
@@ -138,6 +139,7 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
             }
             if (c == w) *reinterpret_cast<f4 *>(sD[w] + lr * LB + 4 * lg) = bj * kk;  // A beta, columns first
         }
+    gdr_wave_fence();  // the wave's rows of P and its diagonal block are read by other lanes
     // eight elements of a row, or of a column, of a matrix held by blocks; zeros above the diagonal
     auto row8f = [&](const float *m, int s, float (&x)[8]) {
         const int c = 2 * s + lg / 2;
@@ -179,7 +181,7 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
         }
         if (lg == 0) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sD[w][i * LB + lr] = x[i / 4][i % 4];
+            for (int i = 0; i < 16; ++i) sI[w][i * LB + lr] = x[i / 4][i % 4];
         }
     }
     gdr_lds_barrier();
@@ -200,7 +202,7 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], m[r][e], acc, 0, 0, 0);
                 }
-            const f4 d = *reinterpret_cast<const f4 *>(sD[p] + lr * LB + 4 * lg);
+            const f4 d = *reinterpret_cast<const f4 *>(sI[p] + lr * LB + 4 * lg);
             f4 y = {};
 #pragma unroll
             for (int e = 0; e < 4; ++e) y = __builtin_amdgcn_mfma_f32_16x16x4f32(d[e], -acc[e], y, 0, 0, 0);
