@@ -131,7 +131,8 @@ __global__ __launch_bounds__(256) void draft_pick_kernel(const DraftVerifyArgs a
         rest = all;
         whole = whole_all;
     }
-    // a uniform number of 1 or more, or NaN, draws the last token that has weight
+    // a uniform number of 1 or more draws the last token that has weight; NaN or one below 0 is taken as
+    // 0 and draws the first
     const double t0 = a.u[(int64_t)b * (a.D + 1) + a.D] * (double)whole;
     u64 t = t0 > 0.0 ? t0 < 9.2e18 ? (u64)t0 : ~0ull : 0;
     if (whole && t >= whole) t = whole - 1;

@@ -281,7 +281,8 @@ def draft_verify(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uniform
 
     Draft i holds while u_i q_i(x_i) < p_i(x_i).  Behind the last that holds one token is drawn,
     from max(p - q, 0) where a draft was refused (from p if that is nothing), from p where none
-    was; in whole weights of 2^-44, so that no order of summation changes it.  Returns (tokens
+    was; in whole weights of 2^-44, so that no order of summation changes it.  A uniform of 1 or
+    more draws the last token that has weight, NaN or one below 0 the first.  Returns (tokens
     int32 [B,D+1]: the drafts that hold, the token drawn, then -1; accepted int32 [B])."""
     p = _input(target_probs, "target_probs", None, torch.float32, 4)
     if p is None:

@@ -440,9 +440,10 @@ kda_status kda_gdr_recurrent_step(const void *q, const void *k, const void *v, k
  * does not hold).  Behind the last that holds one token is drawn: from max(p - q, 0) of the
  * first draft that does not hold (from p if that is nothing), or from p behind all of them.
  * The token drawn is the first whose running sum of weights passes floor(u * sum), the weights
- * being whole numbers of 2^-44 (clamped to [0, 1], cut, NaN as 0): the result does not depend
- * on any order of summation.  A row without any weight gives token 0; a uniform of 1 or more
- * the last token that has weight.
+ * being whole numbers of 2^-44 (clamped to [0, 1], cut, NaN as 0) and the product one of
+ * float64: the result does not depend on any order of summation.  A row without any weight gives
+ * token 0.  A uniform of 1 or more draws the last token that has weight; NaN or one below 0 counts
+ * as 0 where it draws (the first token that has weight), and no draft holds against NaN.
  * D >= 0, 1 <= vocab <= 2^19.  `workspace`: 8-byte aligned scratch of at least
  * kda_draft_verify_workspace_size bytes.  B == 0 enqueues nothing.
  */

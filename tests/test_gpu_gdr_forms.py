@@ -167,3 +167,15 @@ def test_calls_take_numbers_off_the_border():
         want = kda.gdr_recurrent_step(q, k, v, g, beta, a, slots=slots, start=start, lengths=lengths)
         got = kda.gdr_recurrent_step(q, k, v, _off(g), _off(beta), b, slots=_off(slots), start=_off(start, 3), lengths=_off(lengths, 2))
         assert torch.equal(want, got) and torch.equal(a, b)
+
+
+def test_verify_uniforms_outside_their_range():
+    """1 or more draws the last token that has weight; NaN or less than 0 the first, and no draft holds against NaN."""
+    nan, inf = float("nan"), float("inf")
+    p = torch.tensor([0, 0.25, 0.5, 0.25, 0]).expand(8, 2, 5).contiguous().cuda()
+    x = torch.full((8, 1), 2, dtype=torch.int32, device="cuda")
+    #                   draft 2 holds while u < p(2) = 0.5; refused, the residual is p without token 2
+    u = torch.tensor([[0.0, nan], [0.0, -1.0], [0.0, 1.0], [0.0, inf], [0.0, -inf], [nan, 0.0], [nan, nan], [nan, 7.0]], device="cuda")
+    tokens, accepted = kda.draft_verify(p, x, u)
+    assert accepted.tolist() == [1, 1, 1, 1, 1, 0, 0, 0]
+    assert tokens.tolist() == [[2, 1], [2, 1], [2, 3], [2, 3], [2, 1], [1, -1], [1, -1], [3, -1]]
