@@ -228,10 +228,12 @@ __device__ __forceinline__ void gdr_wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Sequence n: its first token's row, its length and its first chunk slot.  Packed offsets
-// are brought into [0, T] and into order, so that no offset a caller passes reads or writes
-// outside the tensors; slots of different sequences are disjoint and below T / C + N.
-__device__ __forceinline__ void gdr_sequence(const GdrArgs &a, int n, int64_t &row, int64_t &len, int64_t &slot) {
+// Sequence n: its first token's row, its length and its first chunk slot.  Packed offsets are
+// brought into [0, T], and a sequence that ends before it starts is empty, so that no offset a
+// caller passes reads or writes outside the tensors: rows end at T at most, slots at T / C + N.
+// Offsets in order (each at least the one before) give every sequence rows and slots of its own;
+// others may share them, and then what is computed is unspecified.
+__host__ __device__ __forceinline__ void gdr_sequence(const GdrArgs &a, int n, int64_t &row, int64_t &len, int64_t &slot) {
     if (a.cu) {
         int64_t b = a.cu[n], e = a.cu[n + 1];
         b = b < 0 ? 0 : b > a.T ? a.T : b;
@@ -247,7 +249,7 @@ __device__ __forceinline__ void gdr_sequence(const GdrArgs &a, int n, int64_t &r
 }
 
 // The chunk at a slot: its first token's row and its length; false if the slot holds none.
-__device__ __forceinline__ bool gdr_chunk(const GdrArgs &a, int64_t slot, int64_t &row, int &len) {
+__host__ __device__ __forceinline__ bool gdr_chunk(const GdrArgs &a, int64_t slot, int64_t &row, int &len) {
     int64_t r, l, s0;
     if (a.cu) {
         int lo = 0, hi = a.N - 1;  // the last sequence whose first slot is <= slot

@@ -72,7 +72,8 @@ __device__ __forceinline__ void gdr_bwd_chain(const GdrArgs &a, int block, __bf1
     m[0] = p[0] = Parts<P>{};  // rows 32..63 have nothing in the first 32 columns of M^T and P^T
     f4 b, end, beta;
     float last;
-    // rows behind the sequence's end read its last row: P^T and M^T are 0 there, and so is beta
+    // rows behind the sequence's end read its last row, and what P^T, M^T and the keys hold there meets
+    // zeros: d_out is taken as 0, and beta is 0
     auto load_kqo = [&](int c) {
         const int64_t t = (int64_t)c * C;
         const bool there = 16 * w + lr < len - t;

@@ -1,7 +1,12 @@
-"""CPU checks of the binding of the gated delta rule that need no call."""
+"""CPU checks around the gated delta rule's calls that need no GPU: what the binding copies, and how the
+kernels map packed offsets to rows."""
+import os
+import subprocess
+
 import pytest
 import torch
 
+from gated_delta_rule_31_amd.build import HIPCC
 from gated_delta_rule_31_amd.gdr import _input
 
 
@@ -14,3 +19,14 @@ def test_only_wide_loads_need_a_border_of_16(first):
     assert _input(x, "x", base, torch.float32, 4).data_ptr() == x.data_ptr()
     wide = _input(x, "x", base, torch.float32)
     assert wide.data_ptr() % 16 == 0 and torch.equal(wide, x) and (wide.data_ptr() == x.data_ptr()) == (first % 4 == 0)
+
+
+def test_packed_offsets_stay_in_range(tmp_path):
+    """The device's own mapping of offsets to rows and chunk slots, compiled for the host: in range for any offsets,
+    one slot a chunk and one chunk a token for offsets in order."""
+    exe = str(tmp_path / "rows")
+    here = os.path.dirname(os.path.abspath(__file__))
+    subprocess.run([HIPCC, "--offload-host-only", "-O1", "-std=c++17", os.path.join(here, "gdr_rows_check.hip"), "-o", exe], check=True,
+                   capture_output=True, timeout=300)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
