@@ -20,7 +20,7 @@ import torch
 import gated_delta_rule_31_amd as kda
 from tests import gdr_reference as ref
 from tests.helpers import err_fp32, f64
-from tests.test_gpu_gdr import NAMES, _cotangents, _fwd, _gpu, _norm
+from tests.test_gpu_gdr import NAMES, _bwd_check, _cotangents, _fwd, _gpu, _norm
 
 pytestmark = pytest.mark.gpu
 
@@ -179,3 +179,74 @@ def test_verify_uniforms_outside_their_range():
     tokens, accepted = kda.draft_verify(p, x, u)
     assert accepted.tolist() == [1, 1, 1, 1, 1, 0, 0, 0]
     assert tokens.tolist() == [[2, 1], [2, 1], [2, 3], [2, 3], [2, 1], [1, -1], [1, -1], [3, -1]]
+
+
+# ------------------------------------------------------------------- full widths, mixed types, long calls
+
+def _rounded_once(got, want, rest, what=""):
+    """An output in bfloat16: half a step of the value, 2^-8, beside what the float32 one is held to."""
+    rms = np.sqrt(np.mean(want ** 2))
+    assert got.dtype == torch.bfloat16 and np.all(np.isfinite(f64(got))), what
+    over = np.abs(f64(got) - want) - 2.0 ** -8 * np.abs(want) - rest * np.maximum(np.abs(want), rms)
+    assert over.max() <= 0, "%s: %.2e over" % (what, over.max())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("HK,HV,K,V,lens", [(24, 72, 128, 128, None), (16, 32, 128, 128, [70, 60]), (9, 36, 64, 128, [64, 1, 0, 65]), (33, 132, 16, 64, None)])
+def test_fwd_two_column_tiles(dtype, HK, HV, K, V, lens):
+    """Sequences x heads x 16-column tiles of at least twice the compute units (256): two tiles a workgroup."""
+    i = ref.make(1, 130, HK, HV, K, V, dtype, seed=90 + K, seqlens=lens)
+    assert i["N"] * HV * (V // 16) >= 512
+    out, final = _fwd(i, K ** -0.5, out_dtype=torch.float32)
+    want = ref.scan(i, K ** -0.5)
+    _full_bits(out, final, want)
+    out, _ = _fwd(i, K ** -0.5, out_dtype=torch.bfloat16)
+    _rounded_once(out, want[0], 1e-5, "bf16 out")
+
+
+@pytest.mark.parametrize("K,V", [(16, 128), (32, 16), (64, 64), (128, 128)])
+def test_fwd_float32_inputs_bfloat16_output(K, V):
+    i = ref.make(2, 100, 2, 4, K, V, torch.float32, seed=100 + K)
+    out, final = _fwd(i, 0.5, out_dtype=torch.bfloat16)
+    want = ref.scan(i, 0.5)
+    _rounded_once(out, want[0], 1e-5)
+    assert err_fp32(final, want[1]) <= 1e-5
+
+
+@pytest.mark.parametrize("dtype,HK,HV", [(torch.bfloat16, 24, 72), (torch.float32, 8, 24), (torch.float32, 1, 2)])
+def test_fwd_long(dtype, HK, HV):
+    """Twenty-four chunks, the last one cut: the first and the last key head's value heads against the definition."""
+    i = ref.make(1, 1500, HK, HV, 128, 128, dtype, seed=110 + HV, decay=(0.002, 1.0))
+    out, final = _fwd(i, 128 ** -0.5, out_dtype=torch.float32)
+    for h in {0, HK - 1}:
+        some = slice(h * HV // HK, (h + 1) * HV // HK)
+        part = {**i, "q": i["q"][:, :, h : h + 1], "k": i["k"][:, :, h : h + 1], "s0": i["s0"][:, some], **{n: i[n][:, :, some] for n in ("v", "g", "beta")}}
+        _full_bits(out[:, :, some], final[:, some], ref.scan(part, 128 ** -0.5), "key head %d" % h)
+
+
+@pytest.mark.parametrize("HK,HV,K,V", [(2, 4, 16, 32), (1, 3, 32, 16), (2, 2, 64, 64), (2, 4, 128, 128), (33, 132, 64, 64), (33, 132, 128, 64)])
+def test_bwd_float32_inputs_bfloat16_cotangents(HK, HV, K, V):
+    _bwd_check(ref.make(1, 70, HK, HV, K, V, torch.float32, seed=120 + K), 121, 0.5, torch.bfloat16)
+
+
+@pytest.mark.parametrize("K,V,HK,HV", [(128, 128, 2, 4), (64, 128, 1, 3), (16, 16, 2, 2), (128, 128, 16, 32)])
+def test_bwd_packed_bfloat16(K, V, HK, HV):
+    lens = [70, 0, 1, 64, 130] if HV < 32 else [66, 64]
+    _bwd_check(ref.make(1, sum(lens), HK, HV, K, V, torch.bfloat16, seed=130 + K + HV, seqlens=lens), 131, K ** -0.5, torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K,V,lens", [(128, 128, None), (32, 64, [70, 0, 61]), (16, 16, None)])
+def test_bwd_bfloat16_gradients(dtype, K, V, lens):
+    """Gradients written in bfloat16 (dq, dk, dv; dg, dbeta and the state's stay float32) against the definition's."""
+    i = ref.make(1, 131, 2, 4, K, V, dtype, seed=140 + K, seqlens=lens)
+    d_out, d_fin = _cotangents(i, 141, dtype)
+    d = _gpu(i)
+    got = kda.gdr_chunk_bwd(d["q"], d["k"], d["v"], d["g"], d["beta"], d_out.cuda(), initial_state=d["s0"], d_final_state=d_fin.cuda(),
+                            cu_seqlens=d["cu"], scale=0.5, grad_dtype=torch.bfloat16)
+    want = ref.scan_bwd(i, d_out, d_fin, 0.5)
+    for name, x, y in zip(NAMES, got, want):
+        if name in ("dq", "dk", "dv"):
+            _rounded_once(x, y, 5e-5, name)
+        else:
+            assert x.dtype == torch.float32 and err_fp32(x, y) <= 5e-5, name
