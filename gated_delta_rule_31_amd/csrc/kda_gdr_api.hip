@@ -17,6 +17,7 @@ bool type_ok(kda_dtype t) { return t == KDA_F32 || t == KDA_BF16; }
 bool aligned(const void *p) { return (uintptr_t)p % 16 == 0; }
 
 constexpr int64_t MAX_UNITS = 1 << 22;  // (chunk slot, value head) or (sequence, value head, column tile)
+constexpr int64_t MAX_TOKENS = MAX_UNITS * kda::GDR_C;  // more of them in a row are more slots than that: their count stays in 64 bits
 
 int64_t chunk_slots(int B, int64_t T, int num_seqs, bool varlen) {
     const int64_t C = kda::GDR_C;
@@ -93,6 +94,7 @@ kda_status chunk_args(kda::GdrArgs &a, const void *q, const void *k, const void 
     a.scale = scale;
     *empty = B == 0 || T == 0 || N == 0;
     if (*empty) return KDA_OK;
+    if (T > MAX_TOKENS) return KDA_ERR_UNSUPPORTED;
     a.slots = chunk_slots(B, T, num_seqs, cu != nullptr);
     a.chunks = (int)((T + kda::GDR_C - 1) / kda::GDR_C);
     // a chunk's rows are addressed by 32-bit offsets
@@ -106,7 +108,7 @@ kda_status chunk_args(kda::GdrArgs &a, const void *q, const void *k, const void 
 // What a workspace's size depends on; false if the shape is not supported.
 bool size_args(kda::GdrArgs &a, kda_dtype in_dtype, int B, int64_t T, int num_seqs, int varlen, int HK, int HV, int K, int V) {
     a = kda::GdrArgs{};
-    if (B < 0 || T < 0 || num_seqs < 0 || !heads_ok(HK, HV) || !type_ok(in_dtype) || !width_ok(K) || !width_ok(V)) return false;
+    if (B < 0 || T < 0 || T > MAX_TOKENS || num_seqs < 0 || !heads_ok(HK, HV) || !type_ok(in_dtype) || !width_ok(K) || !width_ok(V)) return false;
     a.HK = HK;
     a.HV = HV;
     a.V = V;

@@ -6,8 +6,10 @@ import subprocess
 import pytest
 import torch
 
+import gated_delta_rule_31_amd as kda
 from gated_delta_rule_31_amd.build import HIPCC
 from gated_delta_rule_31_amd.gdr import _input
+from tests.test_gdr import _bwd, _fwd
 
 
 @pytest.mark.parametrize("first", range(1, 8))
@@ -30,3 +32,12 @@ def test_packed_offsets_stay_in_range(tmp_path):
                    capture_output=True, timeout=300)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
+
+
+@pytest.mark.parametrize("B,T", [(1 << 10, 1 << 60), (1 << 10, (1 << 60) + 64), (1 << 12, (1 << 57) + 1), (2, (1 << 63) - 1), (1, (1 << 28) + 1)])
+def test_counts_of_chunks_do_not_wrap(B, T):
+    """Rows whose chunks would pass 64 bits are refused, and have no workspace size, as any that are too long."""
+    lib = kda._load()
+    assert _fwd(lib, B=B, T=T, HK=1, HV=1) == 4 and _bwd(lib, B=B, T=T, HK=1, HV=1) == 4
+    assert kda.gdr_chunk_fwd_workspace_size(torch.bfloat16, B, T, 1, 1, 16, 16) == 0
+    assert kda.gdr_chunk_bwd_workspace_size(torch.bfloat16, B, T, 1, 1, 16, 16) == 0
