@@ -5,11 +5,12 @@
 // do not depend on the order in which they are added: probabilities of float32 are exact down
 // to 2^-44, and the whole of 2^19 of them fits 64 bits.
 //
-// Bound by reading two rows of probabilities for a request.  Two kernels: one wave for every
-// 1024 tokens of the row that is drawn from writes the sums of its weights, then one
-// workgroup a request walks the sums and looks inside one tile.  192 requests over
-// 131,072 tokens: 40 us and 6 us for 0.2 GB; one request over 32,768 tokens: 16 to 20 us a call,
-// the host's time for two launches.
+// Bound by reading the target's row, and the draft's where a draft was refused.  Two kernels: one
+// wave for every 1024 tokens of the row that is drawn from writes the sums of its weights, then one
+// workgroup a request walks the sums and looks inside one tile.  192 requests over 131,072 tokens:
+// 44 us and 6 us for 0.15 GB (half of the requests have a draft refused; a copy would take 30), 32
+// us and 5 us for 0.10 GB where the drafts were certain; one request over 32,768 tokens: 16 to 20
+// us a call, the host's time for two launches.
 #include "kda_gdr_step.h"
 
 namespace kda {

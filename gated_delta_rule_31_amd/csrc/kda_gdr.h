@@ -301,10 +301,10 @@ __device__ __forceinline__ bool gdr_pair(const GdrArgs &a, int block, int VB, in
     return true;
 }
 // Tiles of 16 value columns that one workgroup of a chain takes: one while that gives a compute
-// unit no more than one workgroup (8192 tokens x 32 heads of 128 columns: 291 us, two tiles 361),
-// two from two workgroups a unit on, as a chunk's operands are then loaded half as often (64
-// heads: 412 us, one tile 498; 96 heads 634, 767; both without branches since: 256 us for 32
-// heads, 360 for 64 and 617 for 96).
+// unit no more than one workgroup (forward chain, 8192 tokens x 32 heads of 128 columns, bf16: 277
+// us, two tiles 339), two from two workgroups a unit on, as a chunk's operands are then loaded half
+// as often (64 heads: 395 us, one tile 499; 80 heads 621, 731; 96 heads 610, 725).  The time per
+// head is not even: the workgroups of 80 or 96 heads are more than the units, and less than two each.
 inline int gdr_column_tiles(const GdrArgs &a) {
     return a.V >= 32 && (int64_t)a.N * a.HV * (a.V / 16) >= 2 * device_cu_count() ? 2 : 1;
 }

@@ -25,7 +25,7 @@ namespace {
 constexpr int C = GDR_C, P = GDR_PARTS;
 
 // The chain of gradients: workgroups, waves and operands in flight as in the forward chain, and
-// bound alike.  Both chains together, 8192 tokens x 32 heads, K = V = 128, bf16: 751 us, 0.6 GB
+// bound alike.  Both chains together, 8192 tokens x 32 heads, K = V = 128, bf16: 718 us, 0.6 GB
 // read and 0.9 GB written.
 // D: the type of d_out, whose parts are exact until the read's scale meets them.
 template <typename T, typename D, int K, int NV>
@@ -256,7 +256,7 @@ __device__ __forceinline__ int staged_at(int row, int quad) { return lds_at<32>(
 // dA.  The products over V go through LDS in slices of 32 columns, the next slice's rows on
 // their way meanwhile.  Bound by issue: cutting float32 states and rows into parts takes the vector
 // units about 40% of the time, the products the matrix cores 23% (8192 tokens x 32 heads, K = V =
-// 128, bf16: 471 us, 1.05 GB read; its first form, four waves that spilled, took 843 us).
+// 128, bf16: 424 us, 1.05 GB read; its first form, four waves that spilled, took 843 us).
 template <typename T, typename D, int K>
 __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
     constexpr int PK = gdr_input_parts<T>(), PD = gdr_input_parts<D>(), KS = K < 32 ? 1 : K / 32, CT = (K / 16 + 1) / 2, LA = C + 4, KP = K < 32 ? 32 : K, QUADS = K * 8 / 512 ? K * 8 / 512 : 1;
@@ -274,8 +274,8 @@ __global__ __launch_bounds__(512) void gdr_grads_kernel(const GdrArgs a) {
         // rows behind the last sequence have no gradient: each slot clears 64 of them, the last slot
         // the first ones.  There are T / 64 + N slots, enough for all T rows, and those counted from
         // the last one hold no chunk, but for one at most.  1000 of 8192 rows used, 16 key and 32 value
-        // heads, K = V = 128, bf16: 241 us a call, where one workgroup a key head that clears all of
-        // them takes 2127 (and a full bucket 1290).
+        // heads, K = V = 128, bf16: 196 us a call, 185 for the 1000 rows alone; with one workgroup a
+        // key head that clears all of them, above 2000.
         int64_t l, s;
         gdr_sequence(a, a.N - 1, row, l, s);
         const int64_t first = row + l + (a.slots - 1 - slot) * C;

@@ -16,10 +16,10 @@ namespace kda {
 // over most of a chunk.  Rows behind the sequence's end read its last row: their beta is 0, so
 // nothing of them reaches the state.
 //
-// Bound by the dependence of a chunk's three phases while a compute unit has one workgroup (2.0
-// us a chunk, 8192 tokens x 32 heads, K = V = 128, bf16: 256 to 260 us), by the loads of the
+// Bound by the dependence of a chunk's three phases while a compute unit has one workgroup (2.2
+// us a chunk, 8192 tokens x 32 heads, K = V = 128, bf16: 277 to 284 us), by the loads of the
 // operands (68 KB a chunk and workgroup, mostly from L2) and instruction issue beyond (96 heads:
-// 612 to 641 us, 1.2 GB from and to HBM).
+// 605 us, 1.3 GB from and to HBM).
 //
 // TRAIN: for the gradients; every chunk's start state and corrections are kept and there is no
 // output.  The LDS arrays are the kernel's, with P = 3 parts: sS [P][16 NV][K], sX, sE and sV [P][16

@@ -28,7 +28,7 @@ __device__ __forceinline__ int block_at(int p, int r) { return (p * (p + 1) / 2 
 // is there, then the column blocks w of M.  38 KB of LDS, so that four workgroups share a
 // compute unit: a workgroup mostly waits (for its rows, for substitution and products that
 // follow one another), and what it writes, 37 KB, is more than it reads.  8192 tokens x 96
-// heads, K = 128, bf16: 190 to 204 us, 0.19 GB read and 0.39 GB written.
+// heads, K = 128, bf16: 191 us (183 to 213), 0.18 GB read and 0.46 GB written.
 template <typename T, int K, bool BWD>
 __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrArgs a) {
     constexpr int PK = gdr_input_parts<T>(), KP = K < 32 ? 32 : K, LK = KP + 8, KS = KP / 32, VEC = 16 / sizeof(T);

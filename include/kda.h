@@ -351,7 +351,9 @@ size_t kda_noalloc_scratch_bytes(void);
  *   g      [B, T, HV] float32 log decays, g <= 0; -inf forgets the state.  No lower bound.
  *   beta   [B, T, HV] float32 write strengths, any finite value
  *   states [N, HV, K, V] float32
- * K and V in {16, 32, 64, 128} (KDA_ERR_UNSUPPORTED otherwise).  q, k, v, states, gradients,
+ * K and V in {16, 32, 64, 128} (KDA_ERR_UNSUPPORTED otherwise, and for the chunk calls above
+ * 65535 heads, above 2^22 pairs of a 64-token chunk and a value head, or of 16 value columns of a
+ * sequence and head; for the decode step above 2^24 of the latter).  q, k, v, states, gradients,
  * workspaces must be 16-byte aligned, out too (KDA_ERR_BAD_ARGUMENT otherwise).  The other
  * conventions of this file hold.
  *
