@@ -250,3 +250,111 @@ def test_bwd_bfloat16_gradients(dtype, K, V, lens):
             _rounded_once(x, y, 5e-5, name)
         else:
             assert x.dtype == torch.float32 and err_fp32(x, y) <= 5e-5, name
+
+
+# ------------------------------------------------------------------- offsets past 32 bits
+
+def test_long_rows_pass_32_bits():
+    """More than 2^31 elements of v, and a workspace beyond 2^32 bytes: the last tokens' outputs and gradients are bit
+    for bit those of a call that starts from the state before them (on a chunk's border), and the first tokens'
+    gradients those of a call that ends there."""
+    HK, HV, K, V, tail = 2, 64, 16, 128, 129
+    head = (1 << 31) // (HV * V) // 64 * 64 + 64
+    T = head + tail
+    assert head * HV * V > 1 << 31
+    gen = torch.Generator(device="cuda").manual_seed(150)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    unit = lambda x: (x / x.norm(dim=-1, keepdim=True)).to(torch.bfloat16)  # noqa: E731
+    v, d_out = (torch.empty(1, T, HV, V, dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(2))
+    args = [unit(rand(1, T, HK, K)), unit(rand(1, T, HK, K)), v, -0.05 * rand(1, T, HV).abs(), torch.sigmoid(rand(1, T, HV))]
+    first, last = [x[:, :head] for x in args], [x[:, head:] for x in args]
+    d_fin = rand(1, HV, K, V)
+    out, fin = kda.gdr_chunk_fwd(*args)
+    _, mid = kda.gdr_chunk_fwd(*first)
+    o, f = kda.gdr_chunk_fwd(*last, initial_state=mid)
+    assert torch.equal(out[:, head:], o) and torch.equal(fin, f)
+    del out, o
+    tail_grads = kda.gdr_chunk_bwd(*last, d_out[:, head:], initial_state=mid, d_final_state=d_fin)
+    grads = kda.gdr_chunk_bwd(*args, d_out, d_final_state=d_fin)
+    assert all(torch.equal(x[:, head:], y) for x, y in zip(grads[:5], tail_grads))
+    head_grads = kda.gdr_chunk_bwd(*first, d_out[:, :head], d_final_state=tail_grads[5])
+    assert all(torch.equal(x[:, :head], y) for x, y in zip(grads[:5], head_grads)) and torch.equal(grads[5], head_grads[5])
+    # and the first tokens are the definition's
+    i = dict(zip(("q", "k", "v", "g", "beta"), (x[:, :130].cpu() for x in args)), s0=None, cu=None, N=1)
+    now, _ = kda.gdr_chunk_fwd(*args, output_final_state=False)
+    _rounded_once(now[:, :130], ref.scan(i)[0], 1e-5)
+
+
+def test_step_in_a_large_pool():
+    """Slots whose states lie beyond 2^31 elements, and 2^33 bytes, into the pool."""
+    HV, K, V = 64, 128, 128
+    pool = (1 << 31) // (HV * K * V) + 9
+    i = ref.make(3, 2, 32, HV, K, V, torch.bfloat16, seed=151, state=False)
+    d = _gpu(i)
+    states = torch.empty(pool, HV, K, V, device="cuda")
+    slots = torch.tensor([[pool - 1, pool - 2], [0, pool - 3], [pool - 4, 1]], dtype=torch.int32)
+    where = slots.reshape(-1).long()
+    few = 0.3 * torch.randn(6, HV, K, V, generator=torch.Generator().manual_seed(152))
+    states[where.cuda()] = few.cuda()
+    out = kda.gdr_recurrent_step(d["q"], d["k"], d["v"], d["g"], d["beta"], states, slots=slots.cuda(), out_dtype=torch.float32)
+    wo, ws = ref.step(i["q"], i["k"], i["v"], i["g"], i["beta"], few, torch.arange(6).reshape(3, 2), None, None)
+    assert err_fp32(out, wo) <= 1e-5 and err_fp32(states[where.cuda()], ws) <= 1e-5
+
+
+# ------------------------------------------------------------------- several calls at once, captured training
+
+def test_bwd_and_step_on_streams_at_once():
+    """Gradients and decode steps that overlap in time on four streams, each with its own workspace or pool."""
+    cases = []
+    for n in range(4):
+        i = ref.make(1, 200 + 70 * n, 2, 4, 64, 64, torch.bfloat16, seed=160 + n, seqlens=[90, 110 + 70 * n])
+        d_out, d_fin = _cotangents(i, 161 + n, torch.bfloat16)
+        cases.append((_gpu(i), d_out.cuda(), d_fin.cuda()))
+
+    def call(c, states):
+        d, d_out, d_fin = c
+        args = [d[n] for n in ("q", "k", "v", "g", "beta")]
+        grads = kda.gdr_chunk_bwd(*args, d_out, initial_state=d["s0"], d_final_state=d_fin, cu_seqlens=d["cu"])
+        return grads + (kda.gdr_recurrent_step(*[x[:, :3] for x in args], states), states)
+    want = [call(c, c[0]["s0"][:1].clone()) for c in cases]
+    pools = [[c[0]["s0"][:1].clone() for c in cases] for _ in range(5)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in cases], []
+    for states in pools:
+        for c, s, st in zip(cases, states, streams):
+            with torch.cuda.stream(st):
+                got.append(call(c, s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for n, g in enumerate(got) for x, y in zip(g, want[n % 4]))
+
+
+def test_recorded_call_in_a_graph():
+    """A forward and backward pass through autograd, captured, replayed with new inputs in place between eager
+    passes: every replay gives the eager gradients."""
+    i = _gpu(ref.make(1, 160, 2, 4, 64, 64, torch.bfloat16, seed=170, seqlens=[60, 70, 0, 30]))
+    names = ("q", "k", "v", "g", "beta", "s0")
+    data = [torch.cat([i[n], i[n][:, :30]], 1) if n != "s0" else i[n] for n in names]  # thirty rows behind the last sequence
+
+    def turn(xs):
+        xs = [x.detach().requires_grad_() for x in xs]
+        out, fin = kda.gated_delta_rule(*xs[:5], initial_state=xs[5], cu_seqlens=i["cu"], scale=0.5)
+        return (out, fin) + torch.autograd.grad([(out.float() ** 2).mean() + fin.square().mean()], xs)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        turn(data)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = turn(data)
+    for seed in (171, 172, 173):
+        new = _gpu(ref.make(1, 160, 2, 4, 64, 64, torch.bfloat16, seed=seed, seqlens=[60, 70, 0, 30]))
+        for x, n in zip(data, names):
+            (x if n == "s0" else x[:, :160]).copy_(new[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        want = turn(data)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        assert not got[0][:, 160:].any() and all(bool(torch.isfinite(x).all()) for x in got)
