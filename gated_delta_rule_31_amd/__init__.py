@@ -137,6 +137,32 @@ def _load():
     lib.kda_draft_verify_workspace_size.restype = sz
     lib.kda_draft_verify.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, sz, vp]
     lib.kda_draft_verify.restype = i32
+    lib.kda_short_conv_fwd.argtypes = [vp, i64, i32, vp, vp, vp, vp, vp, i32, i32, i64, i32, i32, u32, vp, vp]
+    lib.kda_short_conv_fwd.restype = i32
+    lib.kda_short_conv_bwd_workspace_size.argtypes = [i32, i32, i64, i32, i32]
+    lib.kda_short_conv_bwd_workspace_size.restype = sz
+    lib.kda_short_conv_bwd.argtypes = [vp, i64, i32, vp, vp, vp, vp, i32, i32, i64, i32, i32, u32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.kda_short_conv_bwd.restype = i32
+    lib.kda_short_conv_step.argtypes = [vp, i32, vp, vp, vp, i64, vp, i32, vp, vp, i32, i32, i32, i32, u32, vp, vp]
+    lib.kda_short_conv_step.restype = i32
+    for name in ("kda_glr_kept_size", "kda_glr_fwd_workspace_size"):
+        getattr(lib, name).argtypes = [i32, i64, i32, i32]
+        getattr(lib, name).restype = sz
+    lib.kda_glr_bwd_workspace_size.argtypes = [i32, i64, i32, i32, i32, i32]
+    lib.kda_glr_bwd_workspace_size.restype = sz
+    lib.kda_glr_fwd.argtypes = [vp, i64, i32, vp, i64, vp, vp, f32, vp, i64, u32, vp, vp, vp, i32, i32, i64, i32, i32, vp, vp, vp, sz, vp]
+    lib.kda_glr_fwd.restype = i32
+    lib.kda_glr_bwd.argtypes = [vp, i64, i32, vp, i64, vp, vp, f32, vp, i64, u32, vp, vp, i32, i32, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp,
+                                vp, vp, sz, vp]
+    lib.kda_glr_bwd.restype = i32
+    lib.kda_glr_step.argtypes = [vp, i32, vp, vp, vp, f32, vp, u32, vp, i64, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp]
+    lib.kda_glr_step.restype = i32
+    lib.kda_block_norm_fwd.argtypes = [vp, vp, i64, i32, vp, i32, vp, vp, i64, i32, i32, f32, f32, u32, vp, vp, vp]
+    lib.kda_block_norm_fwd.restype = i32
+    lib.kda_block_norm_bwd_workspace_size.argtypes = [i64, i32, i32]
+    lib.kda_block_norm_bwd_workspace_size.restype = sz
+    lib.kda_block_norm_bwd.argtypes = [vp, vp, i64, i32, vp, i32, vp, vp, i64, i32, i32, f32, f32, u32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.kda_block_norm_bwd.restype = i32
     lib.kda_status_string.argtypes = [i32]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_abi_version.argtypes = []
@@ -697,3 +723,11 @@ from .gdr import (draft_verify, gated_delta_rule, gdr_chunk_bwd, gdr_chunk_bwd_w
 
 __all__ += ["gated_delta_rule", "gdr_chunk_fwd", "gdr_chunk_fwd_workspace_size", "gdr_chunk_bwd",
             "gdr_chunk_bwd_workspace_size", "gdr_recurrent_step", "draft_verify"]
+
+from .layer import (block_norm, block_norm_bwd, block_norm_bwd_workspace_size, block_norm_fwd, gated_linear_recurrence,  # noqa: E402
+                    gated_norm, glr_bwd, glr_bwd_workspace_size, glr_fwd, glr_fwd_workspace_size, glr_kept_size, glr_step, short_conv,
+                    short_conv_bwd, short_conv_bwd_workspace_size, short_conv_fwd, short_conv_step)
+
+__all__ += ["short_conv", "short_conv_fwd", "short_conv_bwd", "short_conv_bwd_workspace_size", "short_conv_step",
+            "gated_linear_recurrence", "glr_fwd", "glr_fwd_workspace_size", "glr_kept_size", "glr_bwd", "glr_bwd_workspace_size", "glr_step",
+            "block_norm", "block_norm_fwd", "block_norm_bwd", "block_norm_bwd_workspace_size", "gated_norm"]

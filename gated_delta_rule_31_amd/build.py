@@ -11,7 +11,8 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libkda.so")
 SOURCES = ["kda_api.hip", "kda_chunk.hip", "kda_chunk_logits.hip", "kda_chunk_logits_norm.hip", "kda_chunk_chain.hip", "kda_recurrent.hip", "kda_step.hip", "kda_gate.hip", "kda_util.hip", "kda_bwd.hip", "kda_noalloc.hip",
-           "kda_gdr_api.hip", "kda_gdr_fwd.hip", "kda_gdr_bwd.hip", "kda_gdr_step.hip", "kda_draft_verify.hip"]
+           "kda_gdr_api.hip", "kda_gdr_fwd.hip", "kda_gdr_bwd.hip", "kda_gdr_step.hip", "kda_draft_verify.hip",
+           "kda_rows_api.hip", "kda_conv.hip", "kda_glr_fwd.hip", "kda_glr_bwd.hip", "kda_norm.hip", "kda_sums.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
          # no packed-fp32 instructions in device code

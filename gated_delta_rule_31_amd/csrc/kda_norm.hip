@@ -1,0 +1,296 @@
+// kda_norm.hip -- what stands between two blocks, and behind a recurrence's heads (gfx950):
+//   p = y r w_after, r = 1 / sqrt(mean y^2 + eps)      (or p = y)
+//   h = residual + scale act(gate) p                   (act: sigmoid or silu; without a gate 1)
+//   n = h r' w_before, r' = 1 / sqrt(mean h^2 + eps)
+// and its gradients, every row by itself: one pass over memory, the row in registers between its
+// sums.  Bound by memory.
+//
+// LANES lanes share a row (16, 32 or 64 of a wave, or a whole workgroup), each with NV vectors of
+// VEC neighbouring channels, LANES vectors apart.  Workgroups go from row to row and keep the
+// weights in registers, and in the backward pass the weights' sums, which they write once.
+#include "kda_rows.h"
+
+namespace kda {
+namespace {
+
+template <int LANES>
+constexpr int THREADS = LANES > 256 ? LANES : 256;
+
+// Sums over the lanes of a row, N at a time; the order is fixed.  Rows of whole workgroups go through
+// LDS, by turns in two places, so that one barrier a call is enough.
+template <int LANES, int N>
+struct RowSum {
+    static constexpr int PARTS = LANES > 64 ? LANES / 64 : 1;
+    float part[2][N][PARTS];
+};
+template <int LANES, int N, int M>
+__device__ __forceinline__ void row_sum(float (&x)[N], RowSum<LANES, M> &lds, int &turn) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        x[j] = row16_sum(x[j]);
+        if constexpr (LANES >= 32) x[j] += __shfl_xor(x[j], 16);
+        if constexpr (LANES >= 64) x[j] += __shfl_xor(x[j], 32);
+    }
+    if constexpr (LANES > 64) {
+        const int wave = threadIdx.x / 64;
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int j = 0; j < N; ++j) lds.part[turn][j][wave] = x[j];
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < LANES / 64; ++w) s += lds.part[turn][j][w];
+            x[j] = s;
+        }
+        turn ^= 1;
+    }
+}
+
+template <int VEC, int LANES, int NV>
+__device__ __forceinline__ void load_weight(float (&w)[NV][VEC], const float *p, bool on, int lane, int vecs) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) w[k][i] = on && p && lane + k * LANES < vecs ? p[(lane + k * LANES) * VEC + i] : 1.f;
+}
+
+template <typename T, int VEC, int LANES, int NV>
+__device__ __forceinline__ void load_rows(Raw<T, VEC> (&r)[NV], const void *p, int64_t at, int lane, int vecs) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        r[k].zero();
+        if (lane + k * LANES < vecs) r[k].load(static_cast<const T *>(p) + at + (lane + k * LANES) * VEC);
+    }
+}
+
+// T: y, the gate and n; R: the residual stream
+template <typename T, typename R, int VEC, int LANES, int NV>
+__global__ __launch_bounds__(THREADS<LANES>) void norm_fwd_kernel(const NormArgs a) {
+    constexpr int EACH = THREADS<LANES> / LANES;
+    __shared__ RowSum<LANES, 1> lds;
+    int turn = 0;
+    const int lane = threadIdx.x % LANES, vecs = a.D / VEC;
+    const float inv = 1.f / a.D;
+    float wa[NV][VEC], wb[NV][VEC];
+    load_weight<VEC, LANES, NV>(wa, a.wa, a.after, lane, vecs);
+    load_weight<VEC, LANES, NV>(wb, a.wb, a.before, lane, vecs);
+    for (int64_t row = (int64_t)blockIdx.x * EACH + threadIdx.x / LANES; row < a.rows; row += (int64_t)gridDim.x * EACH) {
+        Raw<T, VEC> y[NV], z[NV];
+        Raw<R, VEC> x[NV];
+        load_rows<T, VEC, LANES, NV>(y, a.y, row * a.D, lane, vecs);
+        if (a.gate) load_rows<T, VEC, LANES, NV>(z, a.gate, row / a.heads * a.gate_stride + row % a.heads * a.D, lane, vecs);
+        if (a.residual) load_rows<R, VEC, LANES, NV>(x, a.residual, row * a.D, lane, vecs);
+        float r = a.scale;
+        if (a.after) {
+            float s[1] = {0.f};
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) s[0] = fmaf(y[k].get(i), y[k].get(i), s[0]);
+            row_sum<LANES>(s, lds, turn);
+            r *= __builtin_amdgcn_rsqf(fmaf(s[0], inv, a.eps));
+        }
+        float h[NV][VEC], q[1] = {0.f};
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            Raw<R, VEC> o;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                float p = y[k].get(i) * r * wa[k][i];
+                if (a.gate) {
+                    const float g = z[k].get(i), s = sigmoid_f32(g);
+                    p *= a.silu ? g * s : s;
+                }
+                if (a.residual) p += x[k].get(i);
+                h[k][i] = p;
+                q[0] = fmaf(p, p, q[0]);
+                o.set(i, p);
+            }
+            if (lane + k * LANES < vecs) o.store(static_cast<R *>(a.h) + row * a.D + (lane + k * LANES) * VEC);
+        }
+        if (!a.before) continue;
+        row_sum<LANES>(q, lds, turn);
+        const float rh = __builtin_amdgcn_rsqf(fmaf(q[0], inv, a.eps));
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            Raw<T, VEC> o;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o.set(i, h[k][i] * rh * wb[k][i]);
+            if (lane + k * LANES < vecs) o.store(static_cast<T *>(a.n) + row * a.D + (lane + k * LANES) * VEC);
+        }
+    }
+}
+
+// Gradients.  With u = h r', v = y r and <.> the mean over the row:
+//   dh = d_h + r' (d_n w_before - u <d_n w_before u>),        d w_before += d_n u,   d residual = dh
+//   dp = scale act(gate) dh,   d gate = scale act'(gate) p dh
+//   dy = r (dp w_after - v <dp w_after v>),                    d w_after += dp v
+template <typename T, typename R, int VEC, int LANES, int NV>
+__global__ __launch_bounds__(THREADS<LANES>) void norm_bwd_kernel(const NormArgs a) {
+    constexpr int EACH = THREADS<LANES> / LANES;
+    __shared__ RowSum<LANES, 3> lds;
+    int turn = 0;
+    const int lane = threadIdx.x % LANES, vecs = a.D / VEC;
+    const float inv = 1.f / a.D;
+    float wa[NV][VEC], wb[NV][VEC], da[NV][VEC] = {}, db[NV][VEC] = {};
+    load_weight<VEC, LANES, NV>(wa, a.wa, a.after, lane, vecs);
+    load_weight<VEC, LANES, NV>(wb, a.wb, a.before, lane, vecs);
+    for (int64_t row = (int64_t)blockIdx.x * EACH + threadIdx.x / LANES; row < a.rows; row += (int64_t)gridDim.x * EACH) {
+        const int64_t at = row * a.D;
+        Raw<T, VEC> y[NV], z[NV], dn[NV];
+        Raw<R, VEC> h[NV], dh[NV];
+        load_rows<T, VEC, LANES, NV>(y, a.y, at, lane, vecs);
+        if (a.gate) load_rows<T, VEC, LANES, NV>(z, a.gate, row / a.heads * a.gate_stride + row % a.heads * a.D, lane, vecs);
+        if (a.d_h) load_rows<R, VEC, LANES, NV>(dh, a.d_h, at, lane, vecs);
+        if (a.before) {
+            load_rows<R, VEC, LANES, NV>(h, a.h_in, at, lane, vecs);
+            load_rows<T, VEC, LANES, NV>(dn, a.d_n, at, lane, vecs);
+        }
+        float s[3] = {0.f, 0.f, 0.f};  // y^2, h^2, d_n w_before h
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                s[0] = fmaf(y[k].get(i), y[k].get(i), s[0]);
+                if (a.before) {
+                    const float x = h[k].get(i);
+                    s[1] = fmaf(x, x, s[1]);
+                    s[2] = fmaf(dn[k].get(i) * wb[k][i], x, s[2]);
+                }
+            }
+        if (a.before || a.after) row_sum<LANES>(s, lds, turn);
+        const float r = a.after ? __builtin_amdgcn_rsqf(fmaf(s[0], inv, a.eps)) : 1.f;
+        const float rh = a.before ? __builtin_amdgcn_rsqf(fmaf(s[1], inv, a.eps)) : 0.f, mean = s[2] * inv * rh * rh;
+        float dp[NV][VEC], q[1] = {0.f};
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const bool on = lane + k * LANES < vecs;
+            Raw<R, VEC> ox;
+            Raw<T, VEC> oz;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                float g = a.d_h ? dh[k].get(i) : 0.f;
+                if (a.before) {
+                    const float x = h[k].get(i), d = dn[k].get(i);
+                    g = fmaf(rh, fmaf(d, wb[k][i], -x * mean), g);
+                    db[k][i] = fmaf(d * rh, x, db[k][i]);
+                    ox.set(i, g);
+                }
+                g *= a.scale;
+                const float v = y[k].get(i) * r;
+                if (a.gate) {
+                    const float t = z[k].get(i);
+                    float f;  // 1 - e
+                    const float e = sigmoid_f32(t, f);
+                    oz.set(i, g * v * wa[k][i] * (a.silu ? e * fmaf(t, f, 1.f) : e * f));
+                    g *= a.silu ? t * e : e;
+                }
+                da[k][i] = fmaf(g, v, da[k][i]);
+                dp[k][i] = g * wa[k][i];
+                q[0] = fmaf(dp[k][i], v, q[0]);
+            }
+            if (on) {
+                if (a.before && a.d_res) ox.store(static_cast<R *>(a.d_res) + at + (lane + k * LANES) * VEC);
+                if (a.gate) oz.store(static_cast<T *>(a.d_gate) + at + (lane + k * LANES) * VEC);
+            }
+        }
+        if (a.after) row_sum<LANES>(q, lds, turn);
+        const float back = a.after ? q[0] * inv * r : 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            Raw<T, VEC> o;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o.set(i, r * fmaf(-back, y[k].get(i), dp[k][i]));
+            if (lane + k * LANES < vecs) o.store(static_cast<T *>(a.dy) + at + (lane + k * LANES) * VEC);
+        }
+    }
+    if (!a.part) return;
+    if constexpr (EACH > 1) {  // the rows of a workgroup, in their order
+        __shared__ float all[EACH][LANES * NV * VEC];
+        const int group = threadIdx.x / LANES;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            if (w) __syncthreads();
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) all[group][(lane + k * LANES) * VEC + i] = w ? db[k][i] : da[k][i];
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.D; c += THREADS<LANES>) {
+                float x = 0.f;
+#pragma unroll
+                for (int g = 0; g < EACH; ++g) x += all[g][c];
+                a.part[((int64_t)blockIdx.x * 2 + w) * a.D + c] = x;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (lane + k * LANES < vecs)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const int64_t at = (int64_t)blockIdx.x * 2 * a.D + (lane + k * LANES) * VEC + i;
+                    a.part[at] = da[k][i];
+                    a.part[at + a.D] = db[k][i];
+                }
+    }
+}
+
+// Workgroups: enough to fill the chip, each with rows enough to pay for its weights (and, in the
+// backward pass, for the sums that it writes).
+template <bool BWD, typename T, typename R, int VEC, int LANES, int NV>
+hipError_t launch(NormArgs &a, hipStream_t stream) {
+    constexpr int EACH = THREADS<LANES> / LANES;
+    const int64_t need = (a.rows + EACH - 1) / EACH, most = BWD ? a.groups : 2048;
+    a.groups = (int)(need < most ? need : most);
+    const dim3 grid((unsigned)a.groups), block(THREADS<LANES>);
+    if constexpr (BWD) hipLaunchKernelGGL((norm_bwd_kernel<T, R, VEC, LANES, NV>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((norm_fwd_kernel<T, R, VEC, LANES, NV>), grid, block, 0, stream, a);
+    return hipGetLastError();
+}
+
+template <bool BWD, typename T, typename R, int VEC>
+hipError_t by_width(NormArgs &a, hipStream_t stream) {
+    const int vecs = a.D / VEC;
+    if constexpr (VEC > 1) {
+        if (vecs <= 16) return launch<BWD, T, R, VEC, 16, 1>(a, stream);
+        if (vecs <= 32) return launch<BWD, T, R, VEC, 32, 1>(a, stream);
+        if (vecs <= 64) return launch<BWD, T, R, VEC, 64, 1>(a, stream);
+        if (vecs <= 256) return launch<BWD, T, R, VEC, 256, 1>(a, stream);
+        if (vecs <= 512) return launch<BWD, T, R, VEC, 512, 1>(a, stream);
+        if (vecs <= 1024) return launch<BWD, T, R, VEC, 512, 2>(a, stream);
+        if (vecs <= 2048) return launch<BWD, T, R, VEC, 1024, 2>(a, stream);
+        if (vecs <= 4096) return launch<BWD, T, R, VEC, 1024, 4>(a, stream);
+    } else {
+        if (vecs <= 64) return launch<BWD, T, R, VEC, 16, 4>(a, stream);
+        if (vecs <= 512) return launch<BWD, T, R, VEC, 64, 8>(a, stream);
+        if (vecs <= 2048) return launch<BWD, T, R, VEC, 256, 8>(a, stream);
+        if (vecs <= 16384) return launch<BWD, T, R, VEC, 1024, 16>(a, stream);
+    }
+    return hipErrorNotSupported;
+}
+
+template <bool BWD>
+hipError_t by_type(NormArgs &a, bool fp32, bool h_fp32, bool wide, hipStream_t stream) {
+    if (fp32) return wide ? by_width<BWD, float, float, 4>(a, stream) : by_width<BWD, float, float, 1>(a, stream);
+    if (h_fp32) return wide ? by_width<BWD, __bf16, float, 8>(a, stream) : by_width<BWD, __bf16, float, 1>(a, stream);
+    return wide ? by_width<BWD, __bf16, __bf16, 8>(a, stream) : by_width<BWD, __bf16, __bf16, 1>(a, stream);
+}
+
+}  // namespace
+
+int norm_groups(int64_t rows, int D) { return (int)(rows < 512 ? rows : 512); }
+
+hipError_t launch_norm_fwd(NormArgs a, bool fp32, bool h_fp32, bool wide, hipStream_t stream) {
+    return by_type<false>(a, fp32, h_fp32, wide, stream);
+}
+
+hipError_t launch_norm_bwd(NormArgs a, bool fp32, bool h_fp32, bool wide, float *d_wa, float *d_wb, hipStream_t stream) {
+    const hipError_t e = by_type<true>(a, fp32, h_fp32, wide, stream);
+    if (e != hipSuccess || !a.part) return e;
+    return launch_column_sums(ColumnSums{a.part, a.groups, 2 * a.D, a.D, 1, d_wa, d_wb}, stream);
+}
+
+}  // namespace kda

@@ -454,6 +454,147 @@ kda_status kda_draft_verify(const float *target_probs, const int32_t *draft_toke
                             const float *uniforms, const int32_t *lengths, int B, int D, int vocab, int32_t *tokens,
                             int32_t *accepted, void *workspace, size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * What stands around the recurrence in a layer: the short causal convolution of its inputs (the
+ * KDA layer's ShortConvolution), the gated linear recurrence (the recurrence without keys: a
+ * state of one number a channel, with this library's bounded decay), and the norms behind a
+ * recurrence's heads and between two blocks (the layer's gated output norm).  Conventions of
+ * these calls:
+ *   - Rows are tokens; `*_stride` is the distance between two rows in elements (at least the
+ *     row's width), so that x, a gate or an input gate may be a slice of a wider projection; row
+ *     (b, t) is row b T + t.  Everything else is dense.  Channels, not heads, where one number of
+ *     a row stands by itself: C = H K.
+ *   - Weights, biases and scales are float32.
+ *   - cu_seqlens, num_seqs and the empty-sequence rule are those of kda_gdr_chunk_fwd (rows behind
+ *     the last sequence are left as they were, their gradients are zeros; offsets out of range or
+ *     order move boundaries, never an access).  final_state must not be initial_state.
+ *   - Pointers need the alignment of their elements; where all rows begin on 16-byte borders they
+ *     are read 16 bytes at a time, otherwise number by number.
+ *   - Fewer than 2^31 - 64 rows, at most 2^20 channels, fewer than 2^31 numbers in all sequences'
+ *     states and as many threads in a grid (KDA_ERR_UNSUPPORTED otherwise).
+ *   - Every result is the same bit for bit in every call on the same data.
+ *   - Sums, states and gates are float32; outputs are rounded once.
+ */
+
+/* silu(x) = x sigmoid(x) behind the convolution, or as the gate of a norm instead of sigmoid */
+#define KDA_SILU 8u
+
+/*
+ * kda_short_conv_fwd -- the short causal convolution of every channel by itself:
+ *     pre_t = bias + sum_{w < W} weight[:, w] x_{t - W + 1 + w},   out_t = silu(pre_t) (KDA_SILU) or pre_t
+ *   x      [B, T, D] in dtype, x_stride between rows;  out [B, T, D] in dtype
+ *   weight [D, W] float32 (the last column is the row's own);  bias [D] float32 or NULL;  W in {2, 3, 4}
+ *   initial_state [N, W - 1, D] in dtype, the rows before each sequence, oldest first, or NULL (zeros)
+ *   final_state   [N, W - 1, D] in dtype, the last W - 1 rows (of initial_state and x), or NULL
+ */
+kda_status kda_short_conv_fwd(const void *x, int64_t x_stride, kda_dtype dtype, const float *weight, const float *bias,
+                              const void *initial_state, void *final_state, const int32_t *cu_seqlens, int num_seqs, int B,
+                              int64_t T, int D, int W, unsigned flags, void *out, hipStream_t stream);
+
+/*
+ * kda_short_conv_bwd -- its gradients for L = <d_out, out> + <d_final_state, final_state>:
+ *   dx [B, T, D] in dtype, d_weight [D, W] and d_bias [D] float32 (either or both NULL: not wanted),
+ *   d_initial_state [N, W - 1, D] in dtype or NULL;  d_out [B, T, D] and d_final_state in dtype (NULL: zeros).
+ * The workspace is needed for d_weight or d_bias, 16-byte aligned scratch.
+ */
+size_t kda_short_conv_bwd_workspace_size(kda_dtype dtype, int B, int64_t T, int D, int W);
+kda_status kda_short_conv_bwd(const void *x, int64_t x_stride, kda_dtype dtype, const float *weight, const float *bias,
+                              const void *initial_state, const int32_t *cu_seqlens, int num_seqs, int B, int64_t T, int D,
+                              int W, unsigned flags, const void *d_out, const void *d_final_state, void *dx, float *d_weight,
+                              float *d_bias, void *d_initial_state, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * kda_short_conv_step -- up to S tokens for each of B requests over a pool of kept rows, states
+ * [pool, W - 1, D] in dtype, updated in place.  x, out [B, S, D].  slots, slot_cols, start and
+ * lengths are those of kda_gdr_recurrent_step.
+ */
+kda_status kda_short_conv_step(const void *x, kda_dtype dtype, const float *weight, const float *bias, void *states, int64_t pool,
+                               const int32_t *slots, int slot_cols, const int32_t *start, const int32_t *lengths, int B, int S,
+                               int D, int W, unsigned flags, void *out, hipStream_t stream);
+
+/* the input is multiplied by sqrt(1 - alpha^2), which keeps the state's size whatever the decay */
+#define KDA_GLR_NORMALIZE 1u
+
+/*
+ * kda_glr_fwd -- the gated linear recurrence of every channel by itself:
+ *     h_t = alpha_t h_{t-1} + f_t sigmoid(i_t) x_t,   out_t = h_t,   f = sqrt(1 - alpha^2) (KDA_GLR_NORMALIZE) or 1
+ *   x        [B, T, H, K] in dtype;  out [B, T, H, K] in dtype
+ *   gate     with log_scale: logits [B, T, H, K] in dtype, alpha = exp(lower_bound sigmoid(exp(log_scale[h])
+ *            (logits + bias))) as kda_bounded_decay has it (lower_bound < 0);
+ *            log_scale NULL: ln alpha itself, float32, <= 0 (-inf forgets the state)
+ *   log_scale [H], bias [H K] float32 or NULL (a bias only with log_scale)
+ *   in_gate  [B, T, H, K] in dtype (i_t), or NULL: the input as it is
+ *   initial_state, final_state [N, H, K] float32 or NULL
+ *   kept     float32, kda_glr_kept_size bytes, or NULL: the state in front of every 64 rows, for kda_glr_bwd
+ *   workspace  16-byte aligned scratch, required
+ */
+size_t kda_glr_kept_size(int B, int64_t T, int H, int K);
+size_t kda_glr_fwd_workspace_size(int B, int64_t T, int H, int K);
+kda_status kda_glr_fwd(const void *x, int64_t x_stride, kda_dtype dtype, const void *gate, int64_t gate_stride, const float *log_scale,
+                       const float *bias, float lower_bound, const void *in_gate, int64_t in_stride, unsigned flags,
+                       const float *initial_state, float *final_state, const int32_t *cu_seqlens, int num_seqs, int B, int64_t T,
+                       int H, int K, void *out, float *kept, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * kda_glr_bwd -- its gradients for L = <d_out, out> + <d_final_state, final_state>, for the inputs as
+ * given to the forward:
+ *   dx, d_in_gate [B, T, H, K] in dtype (d_in_gate only with in_gate), d_gate like gate (float32 for ln alpha),
+ *   d_log_scale [H], d_bias [H K] float32 or NULL, d_initial_state [N, H, K] float32 or NULL
+ * from d_out [B, T, H, K] in dtype and d_final_state [N, H, K] float32 or NULL (zeros).  kept: what the
+ * forward kept, or NULL (made again from the inputs).  Where alpha is 1 the derivative of
+ * sqrt(1 - alpha^2), which has none there, counts as 0.
+ */
+size_t kda_glr_bwd_workspace_size(int B, int64_t T, int H, int K, int logits, int kept);
+kda_status kda_glr_bwd(const void *x, int64_t x_stride, kda_dtype dtype, const void *gate, int64_t gate_stride, const float *log_scale,
+                       const float *bias, float lower_bound, const void *in_gate, int64_t in_stride, unsigned flags,
+                       const float *initial_state, const int32_t *cu_seqlens, int num_seqs, int B, int64_t T, int H, int K,
+                       const float *kept, const void *d_out, const float *d_final_state, void *dx, void *d_gate, void *d_in_gate,
+                       float *d_log_scale, float *d_bias, float *d_initial_state, void *workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
+/*
+ * kda_glr_step -- up to S tokens for each of B requests over a pool of states [pool, H, K] float32,
+ * updated in place.  x, gate, in_gate, out [B, S, H, K]; slots, slot_cols, start and lengths are those
+ * of kda_gdr_recurrent_step.
+ */
+kda_status kda_glr_step(const void *x, kda_dtype dtype, const void *gate, const float *log_scale, const float *bias, float lower_bound,
+                        const void *in_gate, unsigned flags, float *states, int64_t pool, const int32_t *slots, int slot_cols,
+                        const int32_t *start, const int32_t *lengths, int B, int S, int H, int K, void *out, hipStream_t stream);
+
+/* p = y / rms(y) weight_after, instead of p = y;  n = h / rms(h) weight_before is wanted */
+#define KDA_NORM_AFTER 1u
+#define KDA_NORM_BEFORE 2u
+#define KDA_NORM_MAX_D 16384
+
+/*
+ * kda_block_norm_fwd -- a block's output on its way into the residual stream and the next block, every
+ * row of D numbers by itself, rms(x) = sqrt(mean x^2 + eps):
+ *     p = y / rms(y) weight_after (KDA_NORM_AFTER) or y
+ *     h = residual + scale act(gate) p            act: sigmoid, or silu with KDA_SILU
+ *     n = h / rms(h) weight_before (KDA_NORM_BEFORE; from h before it is rounded)
+ *   y, n     [tokens, heads, D] in dtype;  residual (or NULL: 0), h [tokens, heads, D] in h_dtype: dtype or KDA_F32
+ *   gate     [tokens, heads, D] in dtype, gate_stride between tokens, or NULL: 1
+ *   weight_after, weight_before [D] float32 or NULL (ones)
+ * Without residual and KDA_NORM_BEFORE, on a recurrence's heads, it is the layer's gated output norm.
+ * A row's sum of squares must be finite.  1 <= D <= KDA_NORM_MAX_D.
+ */
+kda_status kda_block_norm_fwd(const void *y, const void *gate, int64_t gate_stride, kda_dtype dtype, const void *residual, kda_dtype h_dtype,
+                              const float *weight_after, const float *weight_before, int64_t tokens, int heads, int D, float scale,
+                              float eps, unsigned flags, void *h, void *n, hipStream_t stream);
+
+/*
+ * kda_block_norm_bwd -- its gradients for L = <d_h, h> + <d_n, n>; h as the forward wrote it (needed, as is d_n,
+ * with KDA_NORM_BEFORE only; d_h may then be NULL: zeros).
+ *   dy, d_gate (with a gate) in dtype;  d_residual in h_dtype, or NULL (without KDA_NORM_BEFORE it is d_h and is not
+ *   written);  d_weight_after, d_weight_before [D] float32 or NULL.
+ * The workspace is needed for the weights' gradients, 16-byte aligned scratch.
+ */
+size_t kda_block_norm_bwd_workspace_size(int64_t tokens, int heads, int D);
+kda_status kda_block_norm_bwd(const void *y, const void *gate, int64_t gate_stride, kda_dtype dtype, const void *h, kda_dtype h_dtype,
+                              const float *weight_after, const float *weight_before, int64_t tokens, int heads, int D, float scale,
+                              float eps, unsigned flags, const void *d_h, const void *d_n, void *dy, void *d_gate, void *d_residual,
+                              float *d_weight_after, float *d_weight_before, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* A static, human-readable name for a status code. */
 const char *kda_status_string(kda_status s);
 
