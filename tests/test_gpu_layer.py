@@ -1,0 +1,541 @@
+"""GPU parity of what stands around the recurrence in a layer -- the short convolution, the gated
+linear recurrence, the norms between blocks -- against 64-bit forms.
+
+Tolerances.  An output of type t is rounded once, by half a step at most: finfo(t).eps / 2 of its value.  What is
+rounded has been computed in float32, every operation off by 2^-24 of its result and the hardware's
+exponential, reciprocal and root by 2^-23; errors are measured against max(|y|, rms(y)).
+  - Convolution: W + 1 products and sums, and for silu an exponential whose argument is rounded (2^-24 |pre| <=
+    2^-22 for |pre| <= 4, where silu's relative slope still matters), a reciprocal and a product: 16 roundings of partial
+    sums that are at most 4 times the rms: 64 x 2^-24.  Its weight gradients are sums of n terms: by a run's and the runs'
+    order at most sqrt(n) + 40 roundings of the sum's own size, at most 4 rms: (160 + 4 sqrt(n)) 2^-24.
+  - Recurrence: a row's gates are off by 8 roundings; the state gathers 1 / (1 - a) rows of them, which is held to
+    64 here (decays of at most 0.985), so 8 x 64 x 2^-24 of the state's size; gradients go through two such sums: twice that,
+    and 1 / f grows to 6: sums of n of them as above, against the size of the terms.
+  - Norms: a mean over D numbers, each lane adding at most 32 of them and 10 levels of tree behind, a root, and eight
+    products: 64 x 2^-24; its weight gradients as the convolution's.
+"""
+import math
+
+import pytest
+import torch
+
+import gated_delta_rule_31_amd as kda
+from tests import layer_reference as ref
+from tests.layer_reference import f64
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+STEP = 2.0 ** -24
+
+
+def err(got, want, floor=0.0):
+    """The largest difference against max(|want|, its rms, floor)."""
+    assert tuple(got.shape) == tuple(want.shape), (got.shape, want.shape)
+    if not want.numel():
+        return 0.0
+    got, want = f64(got), f64(want)
+    assert torch.isfinite(got).all() and torch.isfinite(want).all()
+    rms = max(float(want.pow(2).mean().sqrt()), floor)
+    return float(((got - want).abs() / want.abs().clamp_min(rms if rms > 0 else 1.0)).max())
+
+
+def close(got, want, roundings, what="", floor=0.0):
+    tol = torch.finfo(got.dtype).eps / 2 * (1 if got.dtype != F32 else 0) + roundings * STEP
+    e = err(got, want, floor)
+    assert e <= tol, "%s: %.3g, at most %.3g" % (what, e, tol)
+
+
+def gen(seed):
+    g = torch.Generator().manual_seed(seed)
+    return lambda *s: torch.randn(*s, generator=g)
+
+
+def offsets(lens):
+    return torch.tensor([sum(lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32)
+
+
+def lead(lens, packed, pad=0):
+    return (1, sum(lens) + pad) if packed else (len(lens), lens[0])
+
+
+def gpu(x):
+    return None if x is None else x.cuda()
+
+
+def sliced(x):
+    """The same numbers as a slice of a wider tensor's rows, on the GPU."""
+    w = x.shape[-1] if x.dim() == 3 else x.shape[-1] * x.shape[-2]
+    big = torch.full((*x.shape[:2], 2 * w + 8), float("nan"), dtype=x.dtype, device="cuda")
+    view = big[:, :, 8 : 8 + w]
+    view.copy_(x.reshape(*x.shape[:2], w))
+    return view if x.dim() == 3 else view.unflatten(2, x.shape[2:])
+
+
+def leaf(x):
+    return None if x is None else f64(x).requires_grad_()
+
+
+LENS = [([1], False), ([70], False), ([33, 33], False), ([5] * 7, False), ([0, 1, 2, 3, 0, 4, 0], True), ([129, 1, 0, 250, 64, 0], True), ([31, 32, 33, 96], True)]
+
+
+# --------------------------------------------------------------------------- the short convolution
+
+def conv_case(lens, packed, D, W, dtype, bias, s0, seed):
+    r = gen(seed)
+    x = r(*lead(lens, packed), D).to(dtype)
+    return x, r(D, W) * W ** -0.5, 0.3 * r(D) if bias else None, r(len(lens), W - 1, D).to(dtype) if s0 else None
+
+
+@pytest.mark.parametrize("lens,packed", LENS)
+@pytest.mark.parametrize("dtype,D,W,bias,s0,silu,wide", [
+    (F32, 1, 2, False, True, True, False), (F32, 64, 4, True, True, True, False), (BF, 72, 4, True, False, True, True), (BF, 33, 3, False, True, False, False),
+    (F32, 7, 3, True, False, False, True), (BF, 1032, 2, False, True, True, False), (BF, 8, 4, True, True, False, True)])
+def test_conv(lens, packed, dtype, D, W, bias, s0, silu, wide):
+    x, w, b, s = conv_case(lens, packed, D, W, dtype, bias, s0, 100 + D + sum(lens))
+    r = gen(7)
+    d_out, d_fin = r(*x.shape).to(dtype), r(len(lens), W - 1, D).to(dtype)
+    cu = gpu(offsets(lens)) if packed else None
+    xs = sliced(x) if wide else gpu(x)
+    out, fin = kda.short_conv_fwd(xs, gpu(w), gpu(b), gpu(s), cu_seqlens=cu, silu=silu)
+    X, Wt, Bt, S = leaf(x), leaf(w), leaf(b), leaf(s if s0 else torch.zeros(len(lens), W - 1, D))
+    want, want_fin = ref.conv(X, Wt, Bt, S, lens, packed, silu)
+    close(out, want, 64, "out")
+    assert torch.equal(fin.cpu().double(), want_fin.detach())  # rows as they were
+    ((want * f64(d_out)).sum() + (want_fin * f64(d_fin)).sum()).backward()
+    dx, dw, db, ds = kda.short_conv_bwd(xs, gpu(w), gpu(d_out), bias=gpu(b), initial_state=gpu(s), d_final_state=gpu(d_fin), cu_seqlens=cu, silu=silu)
+    close(dx, X.grad, 64 * W, "dx")
+    close(ds, S.grad, 64 * W, "d initial")
+    n = sum(lens)
+    # a sum's size: its terms' rms times sqrt(n)
+    size = float((f64(d_out).pow(2).mean().sqrt() * f64(x).pow(2).mean().sqrt()) * math.sqrt(n))
+    close(dw, Wt.grad, 160 + 4 * math.sqrt(n), "d weight", size)
+    if bias:
+        close(db, Bt.grad, 160 + 4 * math.sqrt(n), "d bias", size)
+    else:
+        assert db is None
+
+
+def test_conv_gradient_against_differences():
+    """The gradients along one direction against central differences of the 64-bit form: (2 h)^-1 of values that are
+    exact to 1e-15 of their size leaves 1e-9, so float32's own roundings decide."""
+    lens, D, W = [5, 0, 40, 1, 2], 24, 4
+    x, w, b, s = conv_case(lens, True, D, W, F32, True, True, 3)
+    r = gen(4)
+    d_out, d_fin = r(*x.shape), r(len(lens), W - 1, D)
+    got = kda.short_conv_bwd(gpu(x), gpu(w), gpu(d_out), bias=gpu(b), initial_state=gpu(s), d_final_state=gpu(d_fin), cu_seqlens=gpu(offsets(lens)))
+    way = [r(*t.shape).double() for t in (x, w, b, s)]
+
+    def loss(h):
+        o, f = ref.conv(*[f64(t) + h * v for t, v in zip((x, w, b, s), way)], lens, True)
+        return float((o * f64(d_out)).sum() + (f * f64(d_fin)).sum())
+    want = (loss(1e-5) - loss(-1e-5)) / 2e-5
+    mine = sum(float((f64(g) * v).sum()) for g, v in zip(got, way))
+    size = sum(float((f64(g) * v).pow(2).sum()) for g, v in zip(got, way)) ** 0.5
+    assert abs(mine - want) <= 1e-5 * size  # independent errors of 64 W roundings at most: 256 x 2^-24 = 1.5e-5, mean square a third
+
+
+@pytest.mark.parametrize("dtype,D", [(F32, 8), (BF, 136), (BF, 9)])
+@pytest.mark.parametrize("pad", [1, 40, 200])
+def test_conv_behind_the_last_sequence(dtype, D, pad):
+    """Rows behind the last sequence are neither read nor written; their gradients are zeros."""
+    lens = [3, 0, 61]
+    x, w, b, s = conv_case(lens, True, D, 4, dtype, True, True, 5)
+    more = lambda t: torch.cat([gpu(t), torch.full((1, pad, D), float("nan"), dtype=dtype, device="cuda")], 1)  # noqa: E731
+    cu = gpu(offsets(lens))
+    out = torch.full((1, 64 + pad, D), 7.0, dtype=dtype, device="cuda")
+    _, fin = kda.short_conv_fwd(more(x), gpu(w), gpu(b), gpu(s), cu_seqlens=cu, out=out)
+    want, want_fin = kda.short_conv_fwd(gpu(x), gpu(w), gpu(b), gpu(s), cu_seqlens=cu)
+    assert torch.equal(out[:, :64], want) and torch.equal(fin, want_fin) and bool((out[:, 64:] == 7).all())
+    d = gen(6)(1, 64, D).to(dtype)
+    got = kda.short_conv_bwd(more(x), gpu(w), more(d), bias=gpu(b), initial_state=gpu(s), cu_seqlens=cu)
+    ref_ = kda.short_conv_bwd(gpu(x), gpu(w), gpu(d), bias=gpu(b), initial_state=gpu(s), cu_seqlens=cu)
+    assert torch.equal(got[0][:, :64], ref_[0]) and not got[0][:, 64:].any() and torch.equal(got[3], ref_[3])
+    assert err(got[1], ref_[1]) < 1e-5 and err(got[2], ref_[2]) < 1e-5  # other runs, another order
+    with torch.no_grad():
+        assert not kda.short_conv(more(x), gpu(w), gpu(b), cu_seqlens=cu)[0][:, 64:].any()
+
+
+@pytest.mark.parametrize("dtype,D,W", [(F32, 20, 2), (BF, 64, 4), (BF, 7, 3)])
+def test_conv_steps_are_the_prefill(dtype, D, W):
+    """Decoding token by token, and with drafts of which some are taken, gives the prefill's rows and states, bit for bit."""
+    B, T = 5, 12
+    x, w, b, s = conv_case([T] * B, False, D, W, dtype, True, True, 8)
+    want, fin = kda.short_conv_fwd(gpu(x), gpu(w), gpu(b), gpu(s))
+    states = gpu(s).clone()
+    for t in range(T):
+        assert torch.equal(kda.short_conv_step(gpu(x[:, t : t + 1]), gpu(w), states, gpu(b)), want[:, t : t + 1])
+    assert torch.equal(states, fin)
+    pool = torch.zeros(B * 3 + 2, W - 1, D, dtype=dtype, device="cuda")
+    slots = torch.randperm(B * 3 + 2, generator=torch.Generator().manual_seed(1))[: B * 3].reshape(B, 3).to(torch.int32)
+    pool[slots[:, 0].long()] = gpu(s)
+    at, start = [0] * B, torch.zeros(B, dtype=torch.int32)
+    while min(at) < T:
+        n = [min(3, T - a) for a in at]
+        tokens = torch.stack([torch.cat([x[i, a : a + k], x.new_zeros(3 - k, D)]) for i, (a, k) in enumerate(zip(at, n))])
+        out = kda.short_conv_step(gpu(tokens), gpu(w), pool, gpu(b), gpu(slots), gpu(start), torch.tensor(n, dtype=torch.int32, device="cuda"))
+        for i in range(B):
+            assert torch.equal(out[i, : n[i]], want[i, at[i] : at[i] + n[i]]) and not out[i, n[i] :].any()
+            took = min(n[i], 1 + (at[i] + i) % 3)  # how many of them hold
+            if n[i]:
+                start[i] = took - 1
+            at[i] += took
+    for i in range(B):
+        assert torch.equal(pool[slots[i, start[i]].long()], fin[i])
+
+
+@pytest.mark.parametrize("what", ["conv", "scan"])
+def test_step_slots(what):
+    """Slots outside the pool hold nothing, lengths are brought into range, one slot for all tokens keeps the last state."""
+    r = gen(9)
+    B, S, H, K, W = 6, 3, 2, 10, 4
+    shape = (9, W - 1, 20) if what == "conv" else (9, H, K)
+    for slots, start, lengths in [
+            (torch.tensor([[0, 1, 2], [3, -1, 4], [8, 99, 5], [-7, 6, 7], [1000, 1 << 30, -(1 << 30)], [50, 51, 52]]), None, None),
+            (torch.tensor([[0, 1, 2], [3, -1, 4], [8, 99, 5], [-7, 6, 7], [-1, -1, -1], [-1, -1, -1]]), torch.tensor([2, 1, 5, -3, 0, 1]), torch.tensor([3, 9, -4, 2, 1, 0])),
+            (torch.tensor([[3], [2], [7], [-1], [100], [0]]), None, torch.tensor([0, 1, 2, 3, 3, 3]))]:
+        states = r(*shape)
+        kw = dict(slots=gpu(slots.int()), start=None if start is None else gpu(start.int()), lengths=None if lengths is None else gpu(lengths.int()))
+        pool = gpu(states).clone()
+        if what == "conv":
+            x, w, b = r(B, S, 20), r(20, W) / 2, r(20)
+            out = kda.short_conv_step(gpu(x), gpu(w), pool, gpu(b), **kw)
+            step, rows = ref.conv_token(f64(w), f64(b)), 64
+        else:
+            x, z, i, ls, b = r(B, S, H, K), r(B, S, H, K), r(B, S, H, K), 0.3 * r(H), r(H, K)
+            out = kda.glr_step(gpu(x), gpu(z), pool, gpu(ls), gpu(b), gpu(i), **kw)
+            step, rows = ref.scan_token(f64(z), f64(ls), f64(b), f64(i), True), 64
+        want, after = ref.slots_walk(step, f64(x), f64(states), slots, start, lengths)
+        there = ~torch.isnan(want)
+        assert not out.cpu()[~there].any()
+        close(out.cpu()[there], want[there], rows, "out")
+        close(pool, after, rows, "states")
+        untouched = (after == f64(states)).flatten(1).all(1)
+        assert torch.equal(pool.cpu()[untouched], states[untouched])
+
+
+# --------------------------------------------------------------------------- the gated linear recurrence
+
+def scan_case(lens, packed, H, K, dtype, logits, gated, s0, seed, pad=0, at_most=0.985):
+    """Decays from 0.007 to `at_most`."""
+    r = gen(seed)
+    shape = (*lead(lens, packed, pad), H, K)
+    x, i = r(*shape).to(dtype), r(*shape).to(dtype) if gated else None
+    ls = b = None
+    if logits:  # the logits' sigmoid at least -log(at_most) / 5
+        z, ls, b = r(*shape).clamp(-2, 2).to(dtype), 0.2 * r(H).clamp(-2, 2), torch.rand(H, K, generator=torch.Generator().manual_seed(seed)) * 2 - 1.0
+    else:
+        z = math.log(at_most) - r(*shape).abs() * 0.5
+    return x, z, ls, b, i, 0.5 * r(len(lens), H, K) if s0 else None
+
+
+FORMS = [(F32, 2, 16, True, True, True, True, False), (F32, 1, 1, False, False, False, False, False), (BF, 3, 24, True, False, True, False, True), (BF, 5, 7, True, True, False, True, False),
+         (F32, 3, 11, False, True, True, True, True), (BF, 2, 260, False, True, True, False, False), (BF, 4, 64, True, True, True, True, True), (BF, 1, 4, False, False, True, True, False)]
+
+
+@pytest.mark.parametrize("lens,packed", LENS)
+@pytest.mark.parametrize("dtype,H,K,logits,gated,normalize,s0,wide", FORMS)
+def test_scan(lens, packed, dtype, H, K, logits, gated, normalize, s0, wide):
+    x, z, ls, b, i, s = scan_case(lens, packed, H, K, dtype, logits, gated, s0, 200 + H * K + sum(lens))
+    r = gen(11)
+    d_out, d_fin = r(*x.shape).to(dtype), r(len(lens), H, K)
+    cu = gpu(offsets(lens)) if packed else None
+    place = sliced if wide else gpu
+    xs, zs, is_ = place(x), place(z), None if i is None else place(i)
+    kw = dict(log_scale=gpu(ls), bias=gpu(b), in_gate=is_, initial_state=gpu(s), cu_seqlens=cu, normalize=normalize)
+    out, fin, kept = kda.glr_fwd(xs, zs, keep=True, **kw)
+    again = kda.glr_fwd(xs, zs, **kw)
+    assert torch.equal(out, again[0]) and torch.equal(fin, again[1])
+    X, Z, I, A, Bi, S = leaf(x), leaf(z), leaf(i), leaf(ls), leaf(b), leaf(s if s0 else torch.zeros(len(lens), H, K))
+    want, want_fin = ref.scan(X, Z, A, Bi, I, S, lens, packed, normalize)
+    close(out, want, 512, "out")
+    close(fin, want_fin, 512, "final")
+    ((want * f64(d_out)).sum() + (want_fin * f64(d_fin)).sum()).backward()
+    got = kda.glr_bwd(xs, zs, gpu(d_out), d_final_state=gpu(d_fin), kept=kept, **kw)
+    made = kda.glr_bwd(xs, zs, gpu(d_out), d_final_state=gpu(d_fin), **kw)
+    for u, v in zip(got, made):
+        assert (u is None) == (v is None) and (u is None or torch.equal(u, v))
+    n = sum(lens)
+    # gradients of the gate: a factor 1 / f of at most 6 in one term, both of the size of lambda times the state
+    back = float(f64(X.grad).pow(2).mean().sqrt()) + float(f64(d_out).pow(2).mean().sqrt())
+    close(got[0], X.grad, 1024, "dx")
+    close(got[1], Z.grad, 6 * 1024, "d gate", back if logits else 0)
+    if gated:
+        close(got[2], I.grad, 1024, "d in")
+    else:
+        assert got[2] is None
+    if logits:
+        terms = float(Z.grad.pow(2).sum(dim=(0, 1)).max().sqrt()) + back * math.sqrt(n)
+        close(got[4], Bi.grad, 6 * 1024 + 4 * math.sqrt(n), "d bias", terms)
+        close(got[3], A.grad, 6 * 1024 + 4 * math.sqrt(n * K), "d log_scale", terms * math.sqrt(K) * 3)
+    else:
+        assert got[3] is None and got[4] is None
+    close(got[5], S.grad, 1024, "d initial")
+
+
+def test_scan_gradient_against_differences():
+    """As the convolution's; errors of 6 x 1024 roundings at most, independent: 1e-4."""
+    lens, H, K = [70, 0, 1, 30], 3, 8
+    args = scan_case(lens, True, H, K, F32, True, True, True, 13)
+    r = gen(14)
+    d_out, d_fin = r(*args[0].shape), r(len(lens), H, K)
+    x, z, ls, b, i, s = map(gpu, args)
+    got = kda.glr_bwd(x, z, gpu(d_out), log_scale=ls, bias=b, in_gate=i, initial_state=s, d_final_state=gpu(d_fin), cu_seqlens=gpu(offsets(lens)))
+    got = (got[0], got[1], got[3], got[4], got[2], got[5])
+    way = [r(*t.shape).double() for t in args]
+
+    def loss(h):
+        o, f = ref.scan(*[f64(t) + h * v for t, v in zip(args, way)], lens, True)
+        return float((o * f64(d_out)).sum() + (f * f64(d_fin)).sum())
+    want = (loss(1e-5) - loss(-1e-5)) / 2e-5
+    mine = sum(float((f64(g) * v).sum()) for g, v in zip(got, way))
+    size = sum(float((f64(g) * v).pow(2).sum()) for g, v in zip(got, way)) ** 0.5
+    assert abs(mine - want) <= 1e-4 * size
+
+
+@pytest.mark.parametrize("dtype,H,K", [(F32, 2, 4), (BF, 3, 5)])
+@pytest.mark.parametrize("pad", [1, 64, 300])
+def test_scan_behind_the_last_sequence(dtype, H, K, pad):
+    lens = [60, 0, 41]
+    x, z, ls, b, i, s = scan_case(lens, True, H, K, dtype, True, True, True, 15)
+    more = lambda t: torch.cat([gpu(t), torch.full((1, pad, H, K), float("nan"), dtype=dtype, device="cuda")], 1)  # noqa: E731
+    kw = dict(log_scale=gpu(ls), bias=gpu(b), initial_state=gpu(s), cu_seqlens=gpu(offsets(lens)))
+    out = torch.full((1, 101 + pad, H, K), 7.0, dtype=dtype, device="cuda")
+    _, fin, kept = kda.glr_fwd(more(x), more(z), in_gate=more(i), out=out, keep=True, **kw)
+    want, want_fin = kda.glr_fwd(gpu(x), gpu(z), in_gate=gpu(i), **kw)
+    assert torch.equal(out[:, :101], want) and torch.equal(fin, want_fin) and bool((out[:, 101:] == 7).all())
+    d = gen(16)(1, 101, H, K).to(dtype)
+    got = kda.glr_bwd(more(x), more(z), more(d), in_gate=more(i), kept=kept, **kw)
+    ref_ = kda.glr_bwd(gpu(x), gpu(z), gpu(d), in_gate=gpu(i), **kw)
+    for n, (u, v) in enumerate(zip(got, ref_)):
+        if n < 3:
+            assert torch.equal(u[:, :101], v) and not u[:, 101:].any(), n
+        else:
+            assert torch.equal(u, v), n
+    with torch.no_grad():
+        assert not kda.gated_linear_recurrence(more(x), more(z), in_gate=more(i), **kw)[0][:, 101:].any()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_sequences_do_not_reach_each_other(bad):
+    """Numbers that are not finite in one sequence change no bit of another, forward or backward."""
+    lens, H, K = [40, 50, 0, 3, 80], 2, 8
+    x, z, ls, b, i, s = scan_case(lens, True, H, K, F32, True, True, True, 17)
+    d = gen(18)(*x.shape)
+    cu = gpu(offsets(lens))
+    kw = dict(log_scale=gpu(ls), bias=gpu(b), in_gate=gpu(i), cu_seqlens=cu)
+    w = gen(19)(16, 4)
+    conv = lambda x, d: (kda.short_conv_fwd(gpu(x).flatten(2), gpu(w), cu_seqlens=cu), kda.short_conv_bwd(gpu(x).flatten(2), gpu(w), gpu(d).flatten(2), cu_seqlens=cu))  # noqa: E731
+    scan = lambda x, d, s: (kda.glr_fwd(gpu(x), gpu(z), initial_state=gpu(s), **kw), kda.glr_bwd(gpu(x), gpu(z), gpu(d), initial_state=gpu(s), **kw))  # noqa: E731
+    x2, d2, s2 = x.clone(), d.clone(), s.clone()
+    x2[:, 45], d2[:, 60], s2[1], s2[2] = bad, bad, bad, bad
+    fine = torch.ones(sum(lens), dtype=torch.bool)
+    fine[40:90] = False
+    seqs = [0, 3, 4]
+    for one, two in ((conv(x, d), conv(x2, d2)), (scan(x, d, s), scan(x2, d2, s2))):
+        assert torch.equal(one[0][0][:, fine], two[0][0][:, fine]) and torch.equal(one[0][1][seqs], two[0][1][seqs])
+        assert torch.equal(one[1][0][:, fine], two[1][0][:, fine]) and torch.equal(one[1][-1][seqs], two[1][-1][seqs])
+        assert not torch.isfinite(two[0][0][0, 45:90].float()).all()
+    one, two = scan(x, d, s), scan(x2, d2, s2)
+    assert torch.equal(one[1][1][:, fine], two[1][1][:, fine]) and torch.equal(one[1][2][:, fine], two[1][2][:, fine])
+
+
+def test_scan_forgets_and_keeps_all():
+    """Log decays of -inf (nothing stays) and 0 (all does): values and gradients stay finite, and are the formula's."""
+    x = gen(20)(1, 130, 1, 8)
+    g = torch.zeros(1, 130, 1, 8)
+    g[:, ::7] = -float("inf")
+    d = gen(21)(1, 130, 1, 8)
+    for normalize in (False, True):
+        out, fin = kda.glr_fwd(gpu(x), gpu(g), normalize=normalize)
+        grads = kda.glr_bwd(gpu(x), gpu(g), gpu(d), normalize=normalize)
+        h, rows = torch.zeros(8).double(), []
+        for t in range(130):
+            h = f64(x)[0, t, 0] if t % 7 == 0 else h if normalize else h + f64(x)[0, t, 0]
+            rows.append(h)
+        close(out[0, :, 0], torch.stack(rows), 512, "out")
+        lam = torch.zeros(131, 8).double()
+        for t in reversed(range(130)):
+            lam[t] = f64(d)[0, t, 0] + (lam[t + 1] if (t + 1) % 7 else 0)
+        keeps = torch.tensor([t % 7 != 0 for t in range(130)])
+        close(grads[0][0, :, 0], lam[:130] * (~keeps[:, None] | (not normalize)), 1024, "dx")
+        before = torch.cat([torch.zeros(1, 8).double(), torch.stack(rows)[:-1]])
+        close(grads[1][0, :, 0], lam[:130] * before * keeps[:, None], 1024, "dg")  # the root's derivative at 1 counts as 0
+
+
+def test_scan_logits_far_out():
+    """Logits whose sigmoid is 0 or 1 in float32: the gate's limits, and no NaN."""
+    z = torch.tensor([-1e4, -300.0, -100.0, -88.0, -50.0, -20.0, 0.0, 20.0, 90.0, 300.0, 1e4]).reshape(1, 11, 1, 1).expand(1, 11, 1, 4).contiguous()
+    x, i = gen(22)(1, 11, 1, 4), 50 * gen(23)(1, 11, 1, 4)
+    out, _ = kda.glr_fwd(gpu(x), gpu(z), log_scale=torch.zeros(1).cuda(), in_gate=gpu(i))
+    want, _ = ref.scan(f64(x), f64(z), torch.zeros(1).double(), None, f64(i), None, [11], False)
+    close(out, want, 512, "out")
+    grads = kda.glr_bwd(gpu(x), gpu(z), torch.ones_like(gpu(x)), log_scale=torch.zeros(1).cuda(), in_gate=gpu(i))
+    assert all(torch.isfinite(g).all() for g in grads if g is not None)
+
+
+def test_scan_goes_on_from_its_final_state():
+    """A row in two calls is the row in one."""
+    x, z, ls, b, i, s = map(gpu, scan_case([200], False, 3, 20, F32, True, True, True, 24))
+    kw = dict(log_scale=ls, bias=b)
+    whole, fin = kda.glr_fwd(x, z, in_gate=i, initial_state=s, **kw)
+    for cut in (1, 63, 64, 65, 199):
+        a, mid = kda.glr_fwd(x[:, :cut], z[:, :cut], in_gate=i[:, :cut], initial_state=s, **kw)
+        c, end = kda.glr_fwd(x[:, cut:], z[:, cut:], in_gate=i[:, cut:], initial_state=mid, **kw)
+        close(torch.cat([a, c], 1), whole, 512)
+        close(end, fin, 512)
+
+
+@pytest.mark.parametrize("T,H,K,dtype", [(20000, 2, 32, F32), (70001, 1, 16, BF), (33333, 3, 1, F32)])
+def test_scan_long_rows(T, H, K, dtype):
+    """Long rows against the 64-bit recurrence by spans of a thousand rows, and every call the same bits."""
+    lens = [T // 2 + 1, 0, T - T // 2 - 1]
+    x, z, ls, b, i, s = scan_case(lens, True, H, K, dtype, True, True, True, 25)
+    kw = dict(log_scale=gpu(ls), bias=gpu(b), in_gate=gpu(i), initial_state=gpu(s), cu_seqlens=gpu(offsets(lens)))
+    out, fin, kept = kda.glr_fwd(gpu(x), gpu(z), keep=True, **kw)
+    g = ref.decay(f64(z), f64(ls), f64(b))
+    a, u = torch.exp(g)[0], (torch.sigmoid(f64(i)) * f64(x) * torch.sqrt(-torch.expm1(2 * g)))[0]
+    h, want = f64(s)[0], torch.empty_like(u)
+    for t in range(T):
+        if t == lens[0]:
+            close(fin[0], h, 512)
+            h = f64(s)[2]
+        h = a[t] * h + u[t]
+        want[t] = h
+    close(out[0], want, 512)
+    close(fin[2], h, 512)
+    assert torch.equal(fin[1], gpu(s)[1])
+    d = gen(26)(*x.shape).to(dtype)
+    first = kda.glr_bwd(gpu(x), gpu(z), gpu(d), kept=kept, **kw)
+    m, back = torch.zeros(H, K).double(), torch.empty_like(u)
+    for t in reversed(range(T)):
+        if t == lens[0] - 1:
+            m = torch.zeros_like(m)
+        lam = f64(d)[0, t] + m
+        m = a[t] * lam
+        back[t] = lam
+    close(first[0][0], back * torch.sigmoid(f64(i))[0] * torch.sqrt(-torch.expm1(2 * g))[0], 1024)
+    for _ in range(3):
+        o, f, k = kda.glr_fwd(gpu(x), gpu(z), keep=True, **kw)
+        assert torch.equal(o, out) and torch.equal(f, fin) and torch.equal(k, kept)
+        for u_, v in zip(kda.glr_bwd(gpu(x), gpu(z), gpu(d), kept=kept, **kw), first):
+            assert torch.equal(u_, v)
+
+
+# --------------------------------------------------------------------------- norms
+
+def norm_case(shape, dtype, res, gate, wa, wb, seed):
+    r = gen(seed)
+    y = (1.5 * r(*shape)).to(dtype)
+    return (y, r(*shape).to(dtype) if gate else None, None if res is None else (2 * r(*shape)).to(res), 1 + 0.3 * r(shape[-1]) if wa else None,
+            1 + 0.3 * r(shape[-1]) if wb else None)
+
+
+WIDTHS = [1, 2, 7, 8, 40, 64, 100, 128, 136, 256, 264, 500, 512, 1000, 1032, 2048, 4096, 4104, 7168, 8200, 16383, 16384]
+
+
+@pytest.mark.parametrize("D", WIDTHS)
+@pytest.mark.parametrize("dtype,res,gate,after,before,silu", [(F32, F32, True, True, True, False), (BF, F32, True, True, True, True), (BF, BF, False, True, True, False),
+                                                             (BF, None, True, True, False, True)])
+def test_norm_widths(D, dtype, res, gate, after, before, silu):
+    norm_check((3, 2, D), dtype, res, gate, after, before, silu, True, 0.5)
+
+
+@pytest.mark.parametrize("gate,silu", [(False, False), (True, False), (True, True)])
+@pytest.mark.parametrize("res", [None, F32, BF])
+@pytest.mark.parametrize("after,before", [(True, True), (True, False), (False, True), (False, False)])
+@pytest.mark.parametrize("weights", [True, False])
+def test_norm_forms(gate, silu, res, after, before, weights):
+    for shape in ((5, 1, 24), (70, 24), (2, 9, 3, 33)):
+        norm_check(shape, BF, res, gate, after, before, silu, weights, 1.7)
+
+
+@pytest.mark.parametrize("rows,D", [(1, 8), (515, 8), (1031, 300), (5000, 128), (2049, 1024)])
+def test_norm_many_rows(rows, D):
+    norm_check((rows, D), F32, F32, True, True, True, True, True, 0.25)
+
+
+def norm_check(shape, dtype, res, gate, after, before, silu, weights, scale):
+    y, z, x, wa, wb = norm_case(shape, dtype, res, gate, weights and after, weights and before, 300 + shape[-1])
+    kw = dict(weight_after=gpu(wa), weight_before=gpu(wb), norm_after=after, norm_before=before, scale=scale, eps=1e-6, silu=silu)
+    zs = None
+    if gate:  # a slice of a wider tensor
+        big = torch.full((*shape[:-2], shape[-2] * shape[-1] * 2 + 8) if len(shape) > 2 else (shape[0], 2 * shape[1] + 8), float("nan"), dtype=dtype, device="cuda")
+        cut = big[..., 8 : 8 + (shape[-1] * shape[-2] if len(shape) > 2 else shape[-1])]
+        cut.copy_(z.reshape(cut.shape))
+        zs = cut.unflatten(-1, shape[-2:]) if len(shape) > 2 else cut
+    h, n = kda.block_norm_fwd(gpu(y), gate=zs, residual=gpu(x), **kw)
+    Y, Z, X, A, Bw = leaf(y), leaf(z), leaf(x), leaf(wa), leaf(wb)
+    want_h, want_n = ref.block_norm(Y, Z, X, A, Bw, after, before, scale, 1e-6, silu)
+    close(h, want_h, 64, "h")
+    assert h.dtype == (res or dtype) and (n is None) == (not before)
+    if before:
+        close(n, want_n, 64, "n")
+    r = gen(31)
+    d_h, d_n = r(*shape).to(h.dtype), r(*shape).to(dtype) if before else None
+    # the norm before reads the stream as it was stored
+    if before:
+        stored = f64(h).requires_grad_()
+        (ref.block_norm(stored, None, None, Bw, None, True, False, 1.0, 1e-6, False)[0] * f64(d_n)).sum().backward()
+        total = f64(d_h) + stored.grad
+    else:
+        total = f64(d_h)
+    (want_h * total).sum().backward()
+    dy, dz, dr, dwa, dwb = kda.block_norm_bwd(gpu(y), gpu(d_h), d_n=gpu(d_n), h=h if before else None, gate=zs, **kw)
+    rows = total.numel() // shape[-1]
+    size = float(total.pow(2).mean().sqrt()) * scale * math.sqrt(rows)
+    close(dr, total, 64, "d residual")
+    # dy = r (dp w - v <dp w v>) is a difference, which for rows of one or two numbers is next to nothing of its terms (for
+    # one number 1 - v^2 = eps r^2 of them), and so is the gradient of h that it is made of, d_h + r' (d_n w' - u <d_n w' u>):
+    # the roundings are 64 of the terms' size, row by row and number by number
+    sized = f64(d_h).abs()
+    if before:
+        rh = 1 / torch.sqrt(f64(h).pow(2).mean(-1, keepdim=True) + 1e-6)
+        dw, u = (f64(d_n) * (1 if Bw is None else Bw.detach())).abs(), (f64(h) * rh).abs()
+        sized = sized + rh * (dw + u * (dw * u).mean(-1, keepdim=True))
+    act = 1 if not gate else ref.silu(f64(z)) if silu else torch.sigmoid(f64(z))
+    root = 1 / torch.sqrt(f64(y).pow(2).mean(-1, keepdim=True) + 1e-6) if after else 1
+    term = (sized * scale * act * (1 if A is None else A.detach())).abs()
+    term = root * (term + ((f64(y) * root).abs() * (term * (f64(y) * root).abs()).mean(-1, keepdim=True) if after else 0))
+    tol = (torch.finfo(dtype).eps / 2 if dtype != F32 else 0) * Y.grad.abs() + 64 * STEP * term
+    assert ((f64(dy) - Y.grad).abs() <= tol).all(), "dy"
+    if gate:
+        close(dz, Z.grad, 128, "d gate")
+    assert (dwa is None) == (A is None) and (dwb is None) == (Bw is None)
+    if A is not None:
+        close(dwa, A.grad, 160 + 4 * math.sqrt(rows), "d weight_after", size)
+    if Bw is not None:
+        close(dwb, Bw.grad, 160 + 4 * math.sqrt(rows), "d weight_before", math.sqrt(rows))
+
+
+def test_norm_of_zeros():
+    """Rows of zeros have the root of eps: outputs zeros, gradients finite."""
+    y = torch.zeros(4, 64)
+    h, n = kda.block_norm_fwd(gpu(y), residual=gpu(y))
+    assert not h.any() and not n.any()
+    d = gen(32)(4, 64)
+    dy, _, dr, _, _ = kda.block_norm_bwd(gpu(y), gpu(d), d_n=gpu(d), h=h)
+    close(dr, f64(d) * 1001, 64)
+    close(dy, f64(d) * 1001 * 1000, 64)
+
+
+def test_norm_recorded():
+    """block_norm and gated_norm through autograd are the raw calls, also where only one of h and n is used."""
+    shape = (6, 4, 40)
+    y, z, x, wa, wb = (gpu(t).requires_grad_() for t in norm_case(shape, BF, BF, True, True, True, 33))
+    kw = dict(scale=0.5, silu=True)
+    raw = lambda *g, **k: kda.block_norm_bwd(y.detach(), *g, gate=z.detach(), weight_after=wa.detach(), **kw, **k)  # noqa: E731
+    h, n = kda.block_norm(y, z, x, wa, wb, **kw)
+    dh, dn = (gpu(gen(34 + k)(*shape).to(BF)) for k in range(2))
+    for use_h, use_n in ((1, 1), (1, 0), (0, 1)):
+        got = torch.autograd.grad([t for t, on in ((h, use_h), (n, use_n)) if on], [y, z, x, wa, wb], [t for t, on in ((dh, use_h), (dn, use_n)) if on], retain_graph=True,
+                                  allow_unused=True)
+        if use_n:
+            want = raw(dh if use_h else None, dn, h.detach(), weight_before=wb.detach())
+        else:
+            want = raw(dh, norm_before=False)
+        for u, v in zip(got, want):
+            assert torch.equal(u, v) if v is not None else not u.any()
+    g = kda.gated_norm(y, z, wa)
+    got = torch.autograd.grad(g, [y, z, wa], dh)
+    want = kda.block_norm_bwd(y.detach(), dh, gate=z.detach(), weight_after=wa.detach(), norm_before=False)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[3])
