@@ -1,18 +1,16 @@
 // kda_glr_fwd.hip -- the gated linear recurrence over long rows (gfx950), and its decode step.
 //
-// Three launches: every tile of 64 rows gives its A and H, one pass over the tiles carries the
-// state through them, and every tile goes through its rows from the state in front of it.  A
-// workgroup is four waves of 16 rows each for 64 VEC channels.
+// One pass (kda_glr.h): a workgroup of eight waves, 16 rows each, for 64 VEC channels holds its rows' decays
+// and inputs in registers while the state in front of them is found.
 #include "kda_glr.h"
 
 namespace kda {
 namespace {
 
-constexpr int WAVES = 4, L = GLR_TILE / WAVES;
+constexpr int WAVES = 8, L = 16, ROWS = WAVES * L;
 
-template <typename T, int VEC, bool LOGITS, bool NORM, bool GATED, int MODE>
-__global__ __launch_bounds__(64 * WAVES) void glr_fwd_kernel(const GlrArgs a, int blocks) {
-    constexpr int U = VEC == 1 ? 1 : VEC;
+template <typename T, int VEC, bool LOGITS, bool NORM, bool GATED>
+__global__ __launch_bounds__(64 * WAVES, 4) void glr_fwd_kernel(const GlrArgs a, int blocks) {
     if ((int)blockIdx.x >= blocks) {  // sequences without a row hand on what they got
         const int64_t i = (int64_t)(blockIdx.x - blocks) * blockDim.x + threadIdx.x;
         if (i < (int64_t)a.seqs.N * a.C) {
@@ -21,47 +19,50 @@ __global__ __launch_bounds__(64 * WAVES) void glr_fwd_kernel(const GlrArgs a, in
         }
         return;
     }
-    __shared__ float sA[WAVES][64][U], sH[WAVES][64][U];
+    __shared__ LookBack<VEC, WAVES> lds;
+    typedef gate_t<T, LOGITS> Z;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
-    const int ctiles = (a.C + 64 * VEC - 1) / (64 * VEC), tile = blockIdx.x / ctiles, c = (blockIdx.x % ctiles * 64 + lane) * VEC;
+    const bool alone = a.look.n == 1;
+    const int ticket = alone ? (int)blockIdx.x : lds.take(a.look.ticket);
+    const int tile = ticket / a.look.columns, column = ticket % a.look.columns;
+    const int c = (column * 64 + lane) * VEC, cc = c < a.C ? c : 0;
     const bool there = c < a.C;
-    const int64_t t0 = (int64_t)tile * GLR_TILE + wave * L, limit = a.seqs.limit();
+    const int64_t t0 = (int64_t)tile * ROWS + wave * L, limit = a.seqs.limit();
     const int count = (int)(a.seqs.rows - t0 < 0 ? 0 : a.seqs.rows - t0 < L ? a.seqs.rows - t0 : L);
-    uint64_t first, last;
-    a.seqs.marks(t0, count, first, last);
+    uint64_t first = 0, last = 0;
     float av[L][VEC], bv[L][VEC], A[VEC], H[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
         A[i] = 1.f;
         H[i] = 0.f;
     }
-    if (there && count > 0) {
-        GateConst<VEC, LOGITS> k;
-        k.load(a.gates, c);
-        const T *x = static_cast<const T *>(a.x) + t0 * a.x_stride + c, *in = static_cast<const T *>(a.gates.in_gate) + t0 * a.gates.in_stride + c;
-        const gate_t<T, LOGITS> *z = static_cast<const gate_t<T, LOGITS> *>(a.gates.gate) + t0 * a.gates.gate_stride + c;
+    if (count > 0) {
+        a.seqs.marks(t0, count, first, last);
+        const T *x = static_cast<const T *>(a.x) + t0 * a.x_stride, *in = static_cast<const T *>(a.gates.in_gate) + t0 * a.gates.in_stride;
+        const Z *z = static_cast<const Z *>(a.gates.gate) + t0 * a.gates.gate_stride;
+        Raw<T, VEC> rx[L], ri[L];
+        Raw<Z, VEC> rz[L];
 #pragma unroll
         for (int u = 0; u < L; ++u) {
             const int64_t at = u < count ? u : count - 1;
-            Raw<T, VEC> rx, ri;
-            Raw<gate_t<T, LOGITS>, VEC> rz;
-            rx.load(x + at * a.x_stride);
-            rz.load(z + at * a.gates.gate_stride);
-            if constexpr (GATED) ri.load(in + at * a.gates.in_stride);
-            else ri.zero();
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const Gate g = make_gate<LOGITS, NORM, GATED>(rz.get(i), ri.get(i), k.scale2[i], k.bias2[i], a.gates.lower);
-                av[u][i] = g.a;
-                bv[u][i] = g.f * g.i * rx.get(i);
-            }
+            rz[u].load(z + at * a.gates.gate_stride + cc);
+            rx[u].load(x + at * a.x_stride + cc);
+            if constexpr (GATED) ri[u].load(in + at * a.gates.in_stride + cc);
+            else ri[u].zero();
         }
+        GateConst<VEC, LOGITS> k;
+        k.load(a.gates, cc);
 #pragma unroll
         for (int u = 0; u < L; ++u) {
-            if (u >= count) break;
-            if (first >> u & 1) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const Gate g = make_gate<LOGITS, NORM, GATED>(rz[u].get(i), ri[u].get(i), k.scale2[i], k.bias2[i], a.gates.lower);
+                av[u][i] = u < count ? g.a : 1.f;  // rows behind the end leave the state as it is
+                bv[u][i] = u < count ? g.f * g.i * rx[u].get(i) : 0.f;
+            }
+            if (first >> u & 1) {  // the state in front of it is the sequence's own
                 float s0[VEC] = {};
-                if (a.s0) load_f32<VEC>(s0, a.s0 + (int64_t)a.seqs.of(t0 + u) * a.C + c);
+                if (a.s0) load_f32<VEC>(s0, a.s0 + (int64_t)a.seqs.of(t0 + u) * a.C + cc);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     bv[u][i] = fmaf(av[u][i], s0[i], bv[u][i]);
@@ -77,61 +78,46 @@ __global__ __launch_bounds__(64 * WAVES) void glr_fwd_kernel(const GlrArgs a, in
     }
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-        sA[wave][lane][i] = A[i];
-        sH[wave][lane][i] = H[i];
+        lds.A[wave][lane][i] = A[i];
+        lds.H[wave][lane][i] = H[i];
     }
     __syncthreads();
-    if (!there) return;
-    if constexpr (MODE == GLR_AGGREGATE) {
-        if (wave) return;
-        float *agg = a.agg + (int64_t)tile * 2 * a.C + c;
+    if (!alone) lds.front(a.look, a.C, tile, column, cc, there, wave, lane);
+    if (!there || count <= 0) return;
+    float h[VEC];
+    lds.state(h, wave, lane, alone);
+    if (a.kept && t0 % GLR_KEPT == 0) {
+        Raw<float, VEC> s;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s.set(i, h[i]);
+        s.store(a.kept + t0 / GLR_KEPT * a.C + c);
+    }
+    if (!a.out) return;
+    T *out = static_cast<T *>(a.out) + t0 * a.C;
+#pragma unroll
+    for (int u = 0; u < L; ++u) {
+        if (first >> u & 1)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) h[i] = 0.f;
+        Raw<T, VEC> y;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            for (int w = 1; w < WAVES; ++w) {
-                H[i] = join(sA[w][lane][i], sH[w][lane][i], H[i]);
-                A[i] *= sA[w][lane][i];
-            }
-            agg[i] = A[i];
-            agg[a.C + i] = H[i];
+            h[i] = fmaf(av[u][i], h[i], bv[u][i]);
+            y.set(i, h[i]);
         }
-    } else {
-        float h[VEC];
-        load_f32<VEC>(h, a.kept + (int64_t)tile * a.C + c);
-        for (int w = 0; w < wave; ++w)
+        if (t0 + u < limit) y.store(out + (int64_t)u * a.C + c);
+        if (a.sf && last >> u & 1) {
+            Raw<float, VEC> s;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) h[i] = join(sA[w][lane][i], sH[w][lane][i], h[i]);
-        T *out = static_cast<T *>(a.out) + t0 * a.C + c;
-#pragma unroll
-        for (int u = 0; u < L; ++u) {
-            if (u >= count) break;
-            if (first >> u & 1)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) h[i] = 0.f;
-            Raw<T, VEC> y;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                h[i] = fmaf(av[u][i], h[i], bv[u][i]);
-                y.set(i, h[i]);
-            }
-            if (t0 + u < limit) y.store(out + (int64_t)u * a.C);
-            if (a.sf && last >> u & 1) {
-                float *sf = a.sf + (int64_t)a.seqs.of(t0 + u) * a.C + c;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) sf[i] = h[i];
-            }
+            for (int i = 0; i < VEC; ++i) s.set(i, h[i]);
+            s.store(a.sf + (int64_t)a.seqs.of(t0 + u) * a.C + c);
         }
     }
 }
 
-__global__ __launch_bounds__(64) void glr_carry_kernel(const float *agg, float *kept, int tiles, int C, int reverse) {
-    const int c = blockIdx.x * 64 + threadIdx.x;
-    if (c >= C) return;
-    float h = 0.f;
-    for (int j = 0; j < tiles; ++j) {
-        const int64_t t = reverse ? tiles - 1 - j : j;
-        kept[t * C + c] = h;
-        h = join(agg[t * 2 * C + c], agg[t * 2 * C + C + c], h);
-    }
+__global__ __launch_bounds__(256) void glr_clear_kernel(uint32_t *p, int64_t n) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n) p[i] = 0;
 }
 
 template <typename T, int VEC, bool LOGITS>
@@ -170,24 +156,21 @@ __global__ __launch_bounds__(64) void glr_step_kernel(const GlrStepArgs a) {
     }
 }
 
-template <typename T, int VEC, int MODE, bool LOGITS, bool NORM>
+template <typename T, int VEC, bool LOGITS, bool NORM>
 hipError_t by_input(const GlrArgs &a, hipStream_t stream) {
-    const int64_t blocks = (int64_t)((a.C + 64 * VEC - 1) / (64 * VEC)) * a.tiles;
-    const int64_t more = MODE == GLR_APPLY && a.seqs.cu && a.sf ? ((int64_t)a.seqs.N * a.C + 64 * WAVES - 1) / (64 * WAVES) : 0;
+    const int64_t blocks = (int64_t)a.look.n * a.look.columns;
+    const int64_t more = a.seqs.cu && a.sf ? ((int64_t)a.seqs.N * a.C + 64 * WAVES - 1) / (64 * WAVES) : 0;
     const dim3 grid((unsigned)(blocks + more)), block(64 * WAVES);
-    if (a.gates.in_gate) hipLaunchKernelGGL((glr_fwd_kernel<T, VEC, LOGITS, NORM, true, MODE>), grid, block, 0, stream, a, (int)blocks);
-    else hipLaunchKernelGGL((glr_fwd_kernel<T, VEC, LOGITS, NORM, false, MODE>), grid, block, 0, stream, a, (int)blocks);
+    if (a.gates.in_gate) hipLaunchKernelGGL((glr_fwd_kernel<T, VEC, LOGITS, NORM, true>), grid, block, 0, stream, a, (int)blocks);
+    else hipLaunchKernelGGL((glr_fwd_kernel<T, VEC, LOGITS, NORM, false>), grid, block, 0, stream, a, (int)blocks);
     return hipGetLastError();
 }
-template <typename T, int VEC, int MODE>
-hipError_t by_gate(const GlrArgs &a, hipStream_t stream) {
-    if (a.gates.log_scale) return a.gates.normalize ? by_input<T, VEC, MODE, true, true>(a, stream) : by_input<T, VEC, MODE, true, false>(a, stream);
-    return a.gates.normalize ? by_input<T, VEC, MODE, false, true>(a, stream) : by_input<T, VEC, MODE, false, false>(a, stream);
-}
-template <int MODE>
-hipError_t by_type(const GlrArgs &a, bool fp32, bool wide, hipStream_t stream) {
-    if (wide) return fp32 ? by_gate<float, 4, MODE>(a, stream) : by_gate<__bf16, 4, MODE>(a, stream);
-    return fp32 ? by_gate<float, 1, MODE>(a, stream) : by_gate<__bf16, 1, MODE>(a, stream);
+template <typename T, int VEC>
+hipError_t by_gate(GlrArgs a, hipStream_t stream) {
+    const hipError_t e = launch_glr_begin(a.look, (a.C + 64 * VEC - 1) / (64 * VEC), stream);
+    if (e != hipSuccess) return e;
+    if (a.gates.log_scale) return a.gates.normalize ? by_input<T, VEC, true, true>(a, stream) : by_input<T, VEC, true, false>(a, stream);
+    return a.gates.normalize ? by_input<T, VEC, false, true>(a, stream) : by_input<T, VEC, false, false>(a, stream);
 }
 
 template <typename T, int VEC>
@@ -200,37 +183,46 @@ hipError_t step_by_gate(const GlrStepArgs &a, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_glr_carry(const float *agg, float *kept, int tiles, int C, bool reverse, hipStream_t stream) {
-    hipLaunchKernelGGL(glr_carry_kernel, dim3((unsigned)((C + 63) / 64)), dim3(64), 0, stream, agg, kept, tiles, C, reverse ? 1 : 0);
+hipError_t launch_glr_begin(GlrLook &g, int columns, hipStream_t stream) {
+    g.columns = columns;
+    g.group_there = g.tile_there + (int64_t)g.n * columns;
+    if (g.n == 1) return hipSuccess;
+    const int64_t n = g.words();
+    hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, g.ticket, n);
     return hipGetLastError();
 }
 
-hipError_t launch_glr_tiles(const GlrArgs &a, bool fp32, bool wide, int mode, hipStream_t stream) {
-    return mode == GLR_AGGREGATE ? by_type<GLR_AGGREGATE>(a, fp32, wide, stream) : by_type<GLR_APPLY>(a, fp32, wide, stream);
+// Groups of about the root of half the tiles: a tile looks at up to `group` tiles with one wave, and at the groups in
+// front with seven.
+void glr_plan(GlrLook &g, int64_t rows, int tile_rows) {
+    g.n = (int)((rows + tile_rows - 1) / tile_rows);
+    g.group = 4;
+    while ((int64_t)g.group * g.group * 2 < g.n) g.group *= 2;
+}
+
+void carve_glr_look(GlrLook &g, Pieces &w, int C) {
+    g.columns = (C + 63) / 64;  // the most there are
+    w.take(g.ticket, g.words());
+    g.tile_there = g.ticket ? g.ticket + 1 : nullptr;
+    w.take(g.tile, (int64_t)g.n * C);
+    w.take(g.whole, (int64_t)g.groups() * C);
 }
 
 size_t carve_glr_fwd(GlrArgs &a, void *base) {
     Pieces w{static_cast<char *>(base)};
-    w.take(a.agg, (int64_t)a.tiles * 2 * a.C);
-    float *kept;
-    w.take(kept, (int64_t)a.tiles * a.C);
-    if (!a.kept) a.kept = kept;
+    glr_plan(a.look, a.seqs.rows, ROWS);
+    carve_glr_look(a.look, w, a.C);
     return w.used;
 }
 
-hipError_t launch_glr_states(const GlrArgs &a, bool fp32, bool wide, hipStream_t stream) {
-    const hipError_t e = launch_glr_tiles(a, fp32, wide, GLR_AGGREGATE, stream);
-    return e == hipSuccess ? launch_glr_carry(a.agg, a.kept, a.tiles, a.C, false, stream) : e;
-}
-
 hipError_t launch_glr_fwd(const GlrArgs &a, bool fp32, bool wide, hipStream_t stream) {
-    const hipError_t e = launch_glr_states(a, fp32, wide, stream);
-    return e == hipSuccess ? launch_glr_tiles(a, fp32, wide, GLR_APPLY, stream) : e;
+    if (wide) return fp32 ? by_gate<float, 2>(a, stream) : by_gate<__bf16, 2>(a, stream);
+    return fp32 ? by_gate<float, 1>(a, stream) : by_gate<__bf16, 1>(a, stream);
 }
 
 hipError_t launch_glr_step(GlrStepArgs a, bool fp32, bool wide, hipStream_t stream) {
-    a.vecs = wide ? a.C / 4 : a.C;
-    if (wide) return fp32 ? step_by_gate<float, 4>(a, stream) : step_by_gate<__bf16, 4>(a, stream);
+    a.vecs = wide ? a.C / 2 : a.C;
+    if (wide) return fp32 ? step_by_gate<float, 2>(a, stream) : step_by_gate<__bf16, 2>(a, stream);
     return fp32 ? step_by_gate<float, 1>(a, stream) : step_by_gate<__bf16, 1>(a, stream);
 }
 

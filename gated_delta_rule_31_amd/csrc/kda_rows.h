@@ -204,6 +204,16 @@ struct GlrGates {
     int normalize;
     int K;                       // channels that share a log_scale
 };
+// How the tiles of a channel's rows tell one another what they do to the state (kda_glr.h): n tiles in
+// groups of `group`, in `columns` columns of channels.
+struct GlrLook {
+    int n, group, columns;
+    uint32_t *ticket;                // tickets taken; behind it the flags, all zero before the launch
+    uint32_t *tile_there, *group_there;  // [n, columns], [groups, columns]
+    uint64_t *tile, *whole;          // [n, C], [groups, C]: A and H of a tile, of a group
+    __host__ __device__ int groups() const { return (n + group - 1) / group; }
+    __host__ __device__ int64_t words() const { return 1 + (int64_t)(n + groups()) * columns; }
+};
 struct GlrArgs {
     const void *x;               // [rows, C]
     int64_t x_stride;
@@ -211,10 +221,10 @@ struct GlrArgs {
     const float *s0;             // [N, C] or null
     float *sf;                   // [N, C] or null
     Seqs seqs;
-    int C, tiles;
-    void *out;                   // [rows, C]
-    float *kept;                 // [tiles, C] or null: the state in front of every tile
-    float *agg;                  // workspace
+    int C;
+    void *out;                   // [rows, C], or null: only what is kept is wanted
+    float *kept;                 // [ceil(rows / GLR_KEPT), C] or null: the state in front of every GLR_KEPT rows
+    GlrLook look;                // workspace
     // gradients
     const void *d_out;           // [rows, C]
     const float *d_sf;           // [N, C] or null
@@ -230,13 +240,12 @@ struct GlrStepArgs {
     int B, S, C, vecs;
     void *out;
 };
-constexpr int GLR_TILE = 64;     // rows of a tile
+constexpr int GLR_KEPT = 64;     // rows between two kept states
 size_t carve_glr_fwd(GlrArgs &a, void *base);
-size_t carve_glr_bwd(GlrArgs &a, void *base, bool kept, float *&sums);
+size_t carve_glr_bwd(GlrArgs &a, void *base, bool kept, float *&sums, void *&more);
+// wide: two channels at a time
 hipError_t launch_glr_fwd(const GlrArgs &a, bool fp32, bool wide, hipStream_t stream);
-// a.kept, the states in front of the tiles, by themselves
-hipError_t launch_glr_states(const GlrArgs &a, bool fp32, bool wide, hipStream_t stream);
-hipError_t launch_glr_bwd(const GlrArgs &a, bool fp32, bool wide, float *sums, float *d_log_scale, float *d_bias, hipStream_t stream);
+hipError_t launch_glr_bwd(const GlrArgs &a, bool fp32, bool wide, float *sums, void *more, float *d_log_scale, float *d_bias, hipStream_t stream);
 hipError_t launch_glr_step(GlrStepArgs a, bool fp32, bool wide, hipStream_t stream);
 
 // ------------------------------------------------------------------ norms between blocks

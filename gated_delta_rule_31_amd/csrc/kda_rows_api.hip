@@ -27,8 +27,16 @@ struct Wide {
         ok = ok && (uintptr_t)p % 16 == 0;
         return *this;
     }
-    Wide &stride(int64_t n, int64_t unit = 0) {
-        ok = ok && n % (unit ? unit : (int64_t)(16 / size)) == 0;
+    Wide &stride(int64_t n) {
+        ok = ok && n % (int64_t)(16 / size) == 0;
+        return *this;
+    }
+};
+// Likewise two channels at a time, for `n` numbers of `size` bytes apart.
+struct Pairs {
+    bool ok = true;
+    Pairs &rows(const void *p, size_t size, int64_t n) {
+        ok = ok && (!p || ((uintptr_t)p % (2 * size) == 0 && n % 2 == 0));
         return *this;
     }
 };
@@ -113,10 +121,10 @@ kda_status glr_gates(kda::GlrGates &g, const void *gate, int64_t gate_stride, co
     return KDA_OK;
 }
 bool glr_fits(const kda::Seqs &s, int C) {
-    const int64_t tiles = (s.rows + kda::GLR_TILE - 1) / kda::GLR_TILE;
+    const int64_t tiles = (s.rows + kda::GLR_KEPT - 1) / kda::GLR_KEPT;
     return tiles * ((C + 63) / 64) * 512 < MAX_GRID && (int64_t)s.N * C < MAX_GRID;
 }
-int glr_tiles(int64_t rows) { return (int)((rows + kda::GLR_TILE - 1) / kda::GLR_TILE); }
+int64_t glr_kept_rows(int64_t rows) { return ((rows + kda::GLR_KEPT - 1) / kda::GLR_KEPT); }
 
 kda_status norm_shape(kda_dtype dtype, kda_dtype h_dtype, int64_t tokens, int heads, int D, float eps, unsigned flags) {
     if (tokens < 0 || heads <= 0 || D <= 0) return KDA_ERR_BAD_SHAPE;
@@ -254,7 +262,7 @@ size_t kda_glr_kept_size(int B, int64_t T, int H, int K) {
     kda::Seqs s{};
     bool empty;
     if (H <= 0 || K <= 0 || (int64_t)H * K > MAX_CHANNELS || batch(s, nullptr, 0, B, T, &empty) != KDA_OK || empty) return 0;
-    return (size_t)glr_tiles(s.rows) * H * K * sizeof(float);
+    return (size_t)glr_kept_rows(s.rows) * H * K * sizeof(float);
 }
 
 size_t kda_glr_fwd_workspace_size(int B, int64_t T, int H, int K) {
@@ -262,7 +270,6 @@ size_t kda_glr_fwd_workspace_size(int B, int64_t T, int H, int K) {
     bool empty;
     if (H <= 0 || K <= 0 || (int64_t)H * K > MAX_CHANNELS || batch(a.seqs, nullptr, 0, B, T, &empty) != KDA_OK || empty) return 0;
     a.C = H * K;
-    a.tiles = glr_tiles(a.seqs.rows);
     return glr_fits(a.seqs, a.C) ? kda::carve_glr_fwd(a, nullptr) : 0;
 }
 
@@ -271,11 +278,11 @@ size_t kda_glr_bwd_workspace_size(int B, int64_t T, int H, int K, int logits, in
     bool empty;
     if (H <= 0 || K <= 0 || (int64_t)H * K > MAX_CHANNELS || batch(a.seqs, nullptr, 0, B, T, &empty) != KDA_OK || empty) return 0;
     a.C = H * K;
-    a.tiles = glr_tiles(a.seqs.rows);
     static const float some = 0.f;
     a.gates.log_scale = logits ? &some : nullptr;
     float *sums;
-    return glr_fits(a.seqs, a.C) ? kda::carve_glr_bwd(a, nullptr, kept != 0, sums) : 0;
+    void *more;
+    return glr_fits(a.seqs, a.C) ? kda::carve_glr_bwd(a, nullptr, kept != 0, sums, more) : 0;
 }
 
 kda_status kda_glr_fwd(const void *x, int64_t x_stride, kda_dtype dtype, const void *gate, int64_t gate_stride, const float *log_scale,
@@ -305,14 +312,14 @@ kda_status kda_glr_fwd(const void *x, int64_t x_stride, kda_dtype dtype, const v
     a.x_stride = x_stride;
     a.s0 = initial_state;
     a.sf = final_state;
-    a.tiles = glr_tiles(a.seqs.rows);
     a.out = out;
     a.kept = kept;
     if (workspace_bytes < kda_glr_fwd_workspace_size(B, T, H, K)) return KDA_ERR_BAD_ARGUMENT;
     kda::carve_glr_fwd(a, workspace);
-    Wide w{size_of(dtype)};
-    w.ptr(x).ptr(gate).ptr(in_gate).ptr(initial_state).ptr(final_state).ptr(out).ptr(kept).stride(C, 4).stride(x_stride).stride(gate_stride, 16 / gate_size);
-    if (in_gate) w.stride(in_stride);
+    const size_t e = size_of(dtype);
+    Pairs w;
+    w.rows(x, e, x_stride).rows(gate, gate_size, gate_stride).rows(in_gate, e, in_stride).rows(out, e, C);
+    w.rows(initial_state, 4, C).rows(final_state, 4, C).rows(kept, 4, C);
     return done(kda::launch_glr_fwd(a, dtype == KDA_F32, w.ok, stream));
 }
 
@@ -350,7 +357,6 @@ kda_status kda_glr_bwd(const void *x, int64_t x_stride, kda_dtype dtype, const v
     a.x = x;
     a.x_stride = x_stride;
     a.s0 = initial_state;
-    a.tiles = glr_tiles(a.seqs.rows);
     a.kept = const_cast<float *>(kept);
     a.d_out = d_out;
     a.d_sf = d_final_state;
@@ -359,16 +365,14 @@ kda_status kda_glr_bwd(const void *x, int64_t x_stride, kda_dtype dtype, const v
     a.d_in = d_in_gate;
     a.ds0 = d_initial_state;
     float *sums;
+    void *more;
     if (workspace_bytes < kda_glr_bwd_workspace_size(B, T, H, K, log_scale != nullptr, kept != nullptr)) return KDA_ERR_BAD_ARGUMENT;
-    kda::carve_glr_bwd(a, workspace, kept != nullptr, sums);
+    kda::carve_glr_bwd(a, workspace, kept != nullptr, sums, more);
     if (!d_log_scale && !d_bias) a.part = nullptr;
-    Wide w{e};
-    w.ptr(x).ptr(gate).ptr(in_gate).ptr(initial_state).ptr(kept).ptr(d_out).ptr(d_final_state).ptr(dx).ptr(d_gate).ptr(d_initial_state);
-    w.stride(C).stride(x_stride).stride(gate_stride, 16 / gate_size);
-    if (in_gate) w.ptr(d_in_gate).stride(in_stride);
-    hipError_t err = hipSuccess;
-    if (!kept) err = kda::launch_glr_states(a, dtype == KDA_F32, w.ok, stream);
-    return done(err != hipSuccess ? err : kda::launch_glr_bwd(a, dtype == KDA_F32, w.ok, sums, d_log_scale, d_bias, stream));
+    Pairs w;
+    w.rows(x, e, x_stride).rows(gate, gate_size, gate_stride).rows(in_gate, e, in_stride).rows(d_out, e, C).rows(dx, e, C).rows(d_gate, gate_size, C);
+    w.rows(in_gate ? d_in_gate : nullptr, e, C).rows(initial_state, 4, C).rows(kept, 4, C).rows(d_final_state, 4, C).rows(d_initial_state, 4, C);
+    return done(kda::launch_glr_bwd(a, dtype == KDA_F32, w.ok, sums, more, d_log_scale, d_bias, stream));
 }
 
 kda_status kda_glr_step(const void *x, kda_dtype dtype, const void *gate, const float *log_scale, const float *bias, float lower_bound,
@@ -394,8 +398,8 @@ kda_status kda_glr_step(const void *x, kda_dtype dtype, const void *gate, const 
     a.B = B;
     a.S = S;
     a.out = out;
-    Wide w{e};
-    w.ptr(x).ptr(gate).ptr(in_gate).ptr(states).ptr(out).stride(C);
+    Pairs w;
+    w.rows(x, e, C).rows(gate, gate_size, C).rows(in_gate, e, C).rows(states, 4, C).rows(out, e, C);
     return done(kda::launch_glr_step(a, dtype == KDA_F32, w.ok, stream));
 }
 
