@@ -69,139 +69,73 @@ __device__ __forceinline__ float join(float a, float h, float before) { return a
 template <typename T, bool LOGITS>
 using gate_t = std::conditional_t<LOGITS, T, float>;
 
-// ------------------------------------------------------------------ one pass over a long row
-//
-// A workgroup holds a tile of rows in registers, publishes the tile's A and H, and waits for what the
-// tiles in front do to the state; so a row is read once, however long the sequence.  Tiles come in
-// groups: a group's last tile publishes the A and H of the whole group as soon as the tiles of its
-// group are there.  The state in front of a tile is that of the groups before its own, joined in
-// their order, and then the tiles before it in its group: about the root of the number of tiles to
-// look at, two publications deep however many tiles there are, and always the same sums in the
-// same order.  (With a state carried from group to group every group would wait for the one before.)
-//
-// Workgroups take their tile by a ticket, the first tile first: one only waits for tiles whose
-// workgroups have taken theirs, are running, and wait for smaller tickets alone.  So the smallest
-// ticket that has not finished always can, and every wait ends.
-//
-// What is published is written, and read, by relaxed atomics of device scope, which do not stay in an XCD's
-// cache.  The flag is stored when the wave's earlier stores have been acknowledged (vmcnt 0), so
-// whoever sees the flag reads what is behind it.  (A release of device scope would write back the
-// XCD's whole cache, outputs and all, for every tile.)
+// Launches.  Rows are cut into tiles, and a wave goes through a tile's rows for 64 VEC channels:
+//   1. A and H of every tile (with one tile: not needed)
+//   2. the state in front of every tile (with few tiles their readers join the words themselves)
+//   3. the rows themselves, from the state in front of their tile
+// so the rows are read twice, the second time partly from the last-level cache.  One pass in which a tile
+// waits for what the tiles in front publish was measured: 8192 x 4096 in 97-102 us, of which 63 are
+// the rows' own and the rest the waiting.  These launches wait for nothing.
 
-__device__ __forceinline__ void publish_word(uint64_t *p, float a, float h) {
-    __hip_atomic_store(p, (uint64_t)__builtin_bit_cast(uint32_t, h) << 32 | __builtin_bit_cast(uint32_t, a), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ void publish_flag(uint32_t *flag, int lane) {
-    __builtin_amdgcn_s_waitcnt(0);
-    asm volatile("" ::: "memory");
-    if (lane == 0) __hip_atomic_store(flag, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
+constexpr int GLR_FEW = 16;  // tiles that readers join themselves
+constexpr int U = 8;         // rows that a wave has on their way
 
-// One wave: A and H of the entries lo <= i < hi joined in their order, for VEC channels a lane.  Waits for all of them.
+// A wave's tile: its column of channels, rows and marks.
+struct GlrPlace {
+    int tile, c, count, own;     // count: rows of the tile; own: those of them that belong to a sequence
+    int64_t t0;
+    uint64_t first, last;
+    bool there;
+};
 template <int VEC>
-__device__ __forceinline__ void look(float (&A)[VEC], float (&H)[VEC], const uint64_t *entry, const uint32_t *there, int columns, int C, int lo, int hi,
-                                     int lane, bool on) {
+__device__ __forceinline__ GlrPlace glr_place(const GlrArgs &a, int wave) {
+    GlrPlace p;
+    p.tile = wave / a.tiles.columns;
+    p.c = (wave % a.tiles.columns * 64 + (threadIdx.x & 63)) * VEC;
+    p.there = p.c < a.C;
+    p.t0 = (int64_t)p.tile * a.tiles.rows;
+    const int64_t left = a.seqs.rows - p.t0, used = (int64_t)__builtin_amdgcn_readfirstlane((int)a.seqs.limit()) - p.t0;
+    p.count = (int)(left < a.tiles.rows ? left : a.tiles.rows);
+    p.own = (int)(used < 0 ? 0 : used < p.count ? used : p.count);
+    uniform_marks(a.seqs, p.t0, p.count, p.first, p.last);
+    return p;
+}
+
+// The state in front of a tile (reverse: behind it).
+template <int VEC>
+__device__ __forceinline__ void glr_front(float (&h)[VEC], const GlrArgs &a, const float *front, int tile, int c, bool reverse) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) h[i] = 0.f;
+    if (a.tiles.n == 1) return;
+    if (front) return load_f32<VEC>(h, front + (int64_t)tile * a.C + c);
+    const int n = reverse ? a.tiles.n - 1 - tile : tile;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+        float w[2 * VEC];
+        load_f32<2 * VEC>(w, a.tiles.words + ((int64_t)(reverse ? a.tiles.n - 1 - j : j) * a.C + c) * 2);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) h[i] = join(w[2 * i], w[2 * i + 1], h[i]);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void glr_word(const GlrArgs &a, int tile, int c, const float (&A)[VEC], const float (&H)[VEC]) {
+    Raw<float, 2 * VEC> w;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-        A[i] = 1.f;
-        H[i] = 0.f;
+        w.set(2 * i, A[i]);
+        w.set(2 * i + 1, H[i]);
     }
-    for (int at = lo; at < hi; at += 64) {
-        const int e = at + lane;
-        while (!__all(e >= hi || __hip_atomic_load(there + (int64_t)e * columns, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))) __builtin_amdgcn_s_sleep(2);
-    }
-    asm volatile("" ::: "memory");
-    if (!on) return;
-    constexpr int U = 8;
-    for (int at = lo; at < hi; at += U) {
-        uint64_t w[U][VEC];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                w[u][i] = __hip_atomic_load(entry + (int64_t)(at + u < hi ? at + u : hi - 1) * C + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (at + u < hi)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float a = __builtin_bit_cast(float, (uint32_t)w[u][i]), h = __builtin_bit_cast(float, (uint32_t)(w[u][i] >> 32));
-                    H[i] = join(a, h, H[i]);
-                    A[i] *= a;
-                }
-    }
+    w.store(a.tiles.words + ((int64_t)tile * a.C + c) * 2);
 }
 
-// The whole of it, for a workgroup of WAVES waves whose parts of the tile have left their A and H in
-// sA, sH (a barrier behind them), in the order in which the state goes through them.  On return, behind a
-// barrier, `state` (...) gives the state in front of the part of any wave.
-template <int VEC, int WAVES>
-struct LookBack {
-    float A[WAVES][64][VEC], H[WAVES][64][VEC];    // of the tile's parts, first part first
-    float LA[WAVES][64][VEC], LH[WAVES][64][VEC];  // of what is in front: groups by waves 1.., the own group's tiles by wave 0
-    int ticket;
-
-    // the tile that this workgroup takes
-    __device__ __forceinline__ int take(uint32_t *counter) {
-        if (threadIdx.x == 0) ticket = (int)__hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        return __builtin_amdgcn_readfirstlane(ticket);
-    }
-
-    __device__ __forceinline__ void front(const GlrLook &g, int C, int tile, int column, int c, bool on, int wave, int lane) {
-        const int group = tile / g.group, begin = group * g.group, groups = g.groups();
-        float a[VEC], h[VEC];
-        if (wave == 0) {
-            float ta[VEC], th[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                ta[i] = 1.f;
-                th[i] = 0.f;
-                for (int w = 0; w < WAVES; ++w) {
-                    th[i] = join(A[w][lane][i], H[w][lane][i], th[i]);
-                    ta[i] *= A[w][lane][i];
-                }
-                if (on) publish_word(g.tile + (int64_t)tile * C + c + i, ta[i], th[i]);
-            }
-            publish_flag(g.tile_there + (int64_t)tile * g.columns + column, lane);
-            look<VEC>(a, h, g.tile + c, g.tile_there + column, g.columns, C, begin, tile, lane, on);
-            if (tile + 1 == begin + g.group && group + 1 < groups) {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    if (on) publish_word(g.whole + (int64_t)group * C + c + i, a[i] * ta[i], join(ta[i], th[i], h[i]));
-                publish_flag(g.group_there + (int64_t)group * g.columns + column, lane);
-            }
-        } else {
-            const int each = (group + WAVES - 2) / (WAVES - 1), lo = (wave - 1) * each, hi = lo + each < group ? lo + each : group;
-            look<VEC>(a, h, g.whole + c, g.group_there + column, g.columns, C, lo, hi, lane, on);
-        }
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            LA[wave][lane][i] = a[i];
-            LH[wave][lane][i] = h[i];
-        }
-        __syncthreads();
-    }
-
-    // the state in front of part `part`
-    __device__ __forceinline__ void state(float (&x)[VEC], int part, int lane, bool alone) const {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            float s = 0.f;
-            if (!alone) {
-                for (int w = 1; w < WAVES; ++w) s = join(LA[w][lane][i], LH[w][lane][i], s);
-                s = join(LA[0][lane][i], LH[0][lane][i], s);
-            }
-            for (int w = 0; w < part; ++w) s = join(A[w][lane][i], H[w][lane][i], s);
-            x[i] = s;
-        }
-    }
-};
-
-// the columns of channels of a launch, and zeros where its flags and the ticket are
-hipError_t launch_glr_begin(GlrLook &g, int columns, hipStream_t stream);
-// tiles of a call and their groups
-void glr_plan(GlrLook &g, int64_t rows, int tile_rows);
-void carve_glr_look(GlrLook &g, Pieces &w, int C);
+// the tiles of a call, and of a launch whose lanes take `vec` channels each
+void glr_plan(GlrArgs &a);
+void carve_glr_tiles(GlrArgs &a, Pieces &w);
+inline int64_t glr_waves(GlrArgs &a, int vec) {
+    a.tiles.columns = (a.C + 64 * vec - 1) / (64 * vec);
+    return (int64_t)a.tiles.n * a.tiles.columns;
+}
+// a.tiles.front from the words, if there are enough tiles for it to be wanted
+hipError_t launch_glr_carry(const GlrArgs &a, bool reverse, hipStream_t stream);
 
 }  // namespace kda

@@ -1,16 +1,17 @@
 // kda_glr_fwd.hip -- the gated linear recurrence over long rows (gfx950), and its decode step.
 //
-// One pass (kda_glr.h): a workgroup of eight waves, 16 rows each, for 64 VEC channels holds its rows' decays
-// and inputs in registers while the state in front of them is found.
+// Bound by memory and the vector units: a row's gates take six transcendental instructions a channel.
 #include "kda_glr.h"
 
 namespace kda {
 namespace {
 
-constexpr int WAVES = 8, L = 16, ROWS = WAVES * L;
+constexpr int WAVES = 4;
 
-template <typename T, int VEC, bool LOGITS, bool NORM, bool GATED>
-__global__ __launch_bounds__(64 * WAVES, 4) void glr_fwd_kernel(const GlrArgs a, int blocks) {
+// The rows of a wave's tile, U at a time with the next U on their way.  OUT: out, final and kept states, from the state in
+// front of the tile; otherwise the tile's A and H.
+template <typename T, int VEC, bool LOGITS, bool NORM, bool GATED, bool OUT>
+__global__ __launch_bounds__(64 * WAVES) void glr_fwd_kernel(const GlrArgs a, int blocks) {
     if ((int)blockIdx.x >= blocks) {  // sequences without a row hand on what they got
         const int64_t i = (int64_t)(blockIdx.x - blocks) * blockDim.x + threadIdx.x;
         if (i < (int64_t)a.seqs.N * a.C) {
@@ -19,105 +20,117 @@ __global__ __launch_bounds__(64 * WAVES, 4) void glr_fwd_kernel(const GlrArgs a,
         }
         return;
     }
-    __shared__ LookBack<VEC, WAVES> lds;
     typedef gate_t<T, LOGITS> Z;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
-    const bool alone = a.look.n == 1;
-    const int ticket = alone ? (int)blockIdx.x : lds.take(a.look.ticket);
-    const int tile = ticket / a.look.columns, column = ticket % a.look.columns;
-    const int c = (column * 64 + lane) * VEC, cc = c < a.C ? c : 0;
-    const bool there = c < a.C;
-    const int64_t t0 = (int64_t)tile * ROWS + wave * L, limit = a.seqs.limit();
-    const int count = (int)(a.seqs.rows - t0 < 0 ? 0 : a.seqs.rows - t0 < L ? a.seqs.rows - t0 : L);
-    uint64_t first = 0, last = 0;
-    float av[L][VEC], bv[L][VEC], A[VEC], H[VEC];
+    const int wave = blockIdx.x * WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    if (wave >= a.tiles.n * a.tiles.columns) return;
+    const GlrPlace p = glr_place<VEC>(a, wave);
+    if (!p.there) return;
+    const int64_t sx = a.x_stride * sizeof(T), sz = a.gates.gate_stride * sizeof(Z), si = a.gates.in_stride * sizeof(T);
+    const char *x = static_cast<const char *>(a.x) + p.t0 * sx, *z = static_cast<const char *>(a.gates.gate) + p.t0 * sz;
+    const char *in = static_cast<const char *>(a.gates.in_gate) + p.t0 * si;
+    Raw<T, VEC> nx[U], ni[U];
+    Raw<Z, VEC> nz[U];
+    auto fetch = [&](int r) {
+        load_run(nz, z + r * sz, sz, p.c * (uint32_t)sizeof(Z), p.count - r);
+        load_run(nx, x + r * sx, sx, p.c * (uint32_t)sizeof(T), p.count - r);
+        if constexpr (GATED) load_run(ni, in + r * si, si, p.c * (uint32_t)sizeof(T), p.count - r);
+    };
+    fetch(0);
+    GateConst<VEC, LOGITS> k;
+    k.load(a.gates, p.c);
+    float A[VEC], h[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        A[i] = 1.f;
-        H[i] = 0.f;
+    for (int i = 0; i < VEC; ++i) A[i] = 1.f;
+    if constexpr (OUT) {
+        glr_front<VEC>(h, a, a.tiles.front, p.tile, p.c, false);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) h[i] = 0.f;
     }
-    if (count > 0) {
-        a.seqs.marks(t0, count, first, last);
-        const T *x = static_cast<const T *>(a.x) + t0 * a.x_stride, *in = static_cast<const T *>(a.gates.in_gate) + t0 * a.gates.in_stride;
-        const Z *z = static_cast<const Z *>(a.gates.gate) + t0 * a.gates.gate_stride;
-        Raw<T, VEC> rx[L], ri[L];
-        Raw<Z, VEC> rz[L];
+    char *out = static_cast<char *>(a.out) + p.t0 * a.C * sizeof(T);
+    float *kept = a.kept + (p.t0 / GLR_KEPT) * a.C + p.c;
+    for (int r = 0; r < p.count; r += U) {
+        float av[U][VEC], bv[U][VEC];
 #pragma unroll
-        for (int u = 0; u < L; ++u) {
-            const int64_t at = u < count ? u : count - 1;
-            rz[u].load(z + at * a.gates.gate_stride + cc);
-            rx[u].load(x + at * a.x_stride + cc);
-            if constexpr (GATED) ri[u].load(in + at * a.gates.in_stride + cc);
-            else ri[u].zero();
-        }
-        GateConst<VEC, LOGITS> k;
-        k.load(a.gates, cc);
-#pragma unroll
-        for (int u = 0; u < L; ++u) {
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const Gate g = make_gate<LOGITS, NORM, GATED>(rz[u].get(i), ri[u].get(i), k.scale2[i], k.bias2[i], a.gates.lower);
-                av[u][i] = u < count ? g.a : 1.f;  // rows behind the end leave the state as it is
-                bv[u][i] = u < count ? g.f * g.i * rx[u].get(i) : 0.f;
+                const Gate g = make_gate<LOGITS, NORM, GATED>(nz[u].get(i), GATED ? ni[u].get(i) : 0.f, k.scale2[i], k.bias2[i], a.gates.lower);
+                av[u][i] = g.a;
+                bv[u][i] = g.f * g.i * nx[u].get(i);
             }
-            if (first >> u & 1) {  // the state in front of it is the sequence's own
-                float s0[VEC] = {};
-                if (a.s0) load_f32<VEC>(s0, a.s0 + (int64_t)a.seqs.of(t0 + u) * a.C + cc);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    bv[u][i] = fmaf(av[u][i], s0[i], bv[u][i]);
-                    av[u][i] = A[i] = H[i] = 0.f;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                A[i] *= av[u][i];
-                H[i] = fmaf(av[u][i], H[i], bv[u][i]);
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        lds.A[wave][lane][i] = A[i];
-        lds.H[wave][lane][i] = H[i];
-    }
-    __syncthreads();
-    if (!alone) lds.front(a.look, a.C, tile, column, cc, there, wave, lane);
-    if (!there || count <= 0) return;
-    float h[VEC];
-    lds.state(h, wave, lane, alone);
-    if (a.kept && t0 % GLR_KEPT == 0) {
-        Raw<float, VEC> s;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) s.set(i, h[i]);
-        s.store(a.kept + t0 / GLR_KEPT * a.C + c);
-    }
-    if (!a.out) return;
-    T *out = static_cast<T *>(a.out) + t0 * a.C;
-#pragma unroll
-    for (int u = 0; u < L; ++u) {
-        if (first >> u & 1)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) h[i] = 0.f;
-        Raw<T, VEC> y;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            h[i] = fmaf(av[u][i], h[i], bv[u][i]);
-            y.set(i, h[i]);
-        }
-        if (t0 + u < limit) y.store(out + (int64_t)u * a.C + c);
-        if (a.sf && last >> u & 1) {
+        if (r + U < p.count) fetch(r + U);
+        if (OUT && a.kept) {
             Raw<float, VEC> s;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) s.set(i, h[i]);
-            s.store(a.sf + (int64_t)a.seqs.of(t0 + u) * a.C + c);
+            s.store(kept + (int64_t)(r / GLR_KEPT) * a.C);
         }
+        const uint32_t first = (uint32_t)(p.first >> r) & ((1u << U) - 1), last = (uint32_t)(p.last >> r) & ((1u << U) - 1);
+        // HERE: a sequence begins or ends among these rows, or the rows end
+        auto rows = [&](auto here) {
+            constexpr bool HERE = decltype(here)::value;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (HERE && r + u >= p.count) continue;
+                if (HERE && first >> u & 1) {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) A[i] = h[i] = 0.f;
+                    if (a.s0) load_f32<VEC>(h, a.s0 + (int64_t)a.seqs.of(p.t0 + r + u) * a.C + p.c);
+                }
+                Raw<T, VEC> y;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    h[i] = fmaf(av[u][i], h[i], bv[u][i]);
+                    if constexpr (OUT) y.set(i, h[i]);
+                    else A[i] *= av[u][i];
+                }
+                if constexpr (OUT) {
+                    if (a.out && (!HERE || r + u < p.own)) y.store(out + (int64_t)(r + u) * a.C * sizeof(T), p.c * (uint32_t)sizeof(T));
+                    if (HERE && a.sf && last >> u & 1) {
+                        Raw<float, VEC> s;
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) s.set(i, h[i]);
+                        s.store(a.sf + (int64_t)a.seqs.of(p.t0 + r + u) * a.C + p.c);
+                    }
+                }
+            }
+        };
+        if (first | last || r + U > p.own) rows(std::true_type{});
+        else rows(std::false_type{});
     }
+    if constexpr (!OUT) glr_word<VEC>(a, p.tile, p.c, A, h);
 }
 
-__global__ __launch_bounds__(256) void glr_clear_kernel(uint32_t *p, int64_t n) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i < n) p[i] = 0;
+// The state in front of every tile: 64 groups of tiles for 16 channels, each group's A and H first, then its tiles from the
+// state that the groups before it leave.
+constexpr int CARRY_C = 16, CARRY_G = 64;
+__global__ __launch_bounds__(CARRY_C * CARRY_G) void glr_carry_kernel(const float *words, float *front, int n, int C, int reverse) {
+    __shared__ float sA[CARRY_G][CARRY_C], sH[CARRY_G][CARRY_C];
+    const int lane = threadIdx.x % CARRY_C, group = threadIdx.x / CARRY_C, c = blockIdx.x * CARRY_C + lane;
+    const int each = (n + CARRY_G - 1) / CARRY_G, lo = group * each, hi = lo + each < n ? lo + each : n;
+    float A = 1.f, H = 0.f;
+    if (c < C) {
+#pragma unroll 4
+        for (int j = lo; j < hi; ++j) {
+            const float *w = words + ((int64_t)(reverse ? n - 1 - j : j) * C + c) * 2;
+            H = join(w[0], w[1], H);
+            A *= w[0];
+        }
+    }
+    sA[group][lane] = A;
+    sH[group][lane] = H;
+    __syncthreads();
+    if (c >= C || lo >= hi) return;
+    float h = 0.f;
+#pragma unroll 8
+    for (int g = 0; g < group; ++g) h = join(sA[g][lane], sH[g][lane], h);
+#pragma unroll 4
+    for (int j = lo; j < hi; ++j) {
+        const int64_t t = reverse ? n - 1 - j : j;
+        front[t * C + c] = h;
+        h = join(words[(t * C + c) * 2], words[(t * C + c) * 2 + 1], h);
+    }
 }
 
 template <typename T, int VEC, bool LOGITS>
@@ -156,21 +169,24 @@ __global__ __launch_bounds__(64) void glr_step_kernel(const GlrStepArgs a) {
     }
 }
 
-template <typename T, int VEC, bool LOGITS, bool NORM>
-hipError_t by_input(const GlrArgs &a, hipStream_t stream) {
-    const int64_t blocks = (int64_t)a.look.n * a.look.columns;
-    const int64_t more = a.seqs.cu && a.sf ? ((int64_t)a.seqs.N * a.C + 64 * WAVES - 1) / (64 * WAVES) : 0;
+template <bool OUT, typename T, int VEC, bool LOGITS, bool NORM>
+hipError_t by_input(GlrArgs &a, hipStream_t stream) {
+    const int64_t blocks = (glr_waves(a, VEC) + WAVES - 1) / WAVES;
+    const int64_t more = OUT && a.seqs.cu && a.sf ? ((int64_t)a.seqs.N * a.C + 64 * WAVES - 1) / (64 * WAVES) : 0;
     const dim3 grid((unsigned)(blocks + more)), block(64 * WAVES);
-    if (a.gates.in_gate) hipLaunchKernelGGL((glr_fwd_kernel<T, VEC, LOGITS, NORM, true>), grid, block, 0, stream, a, (int)blocks);
-    else hipLaunchKernelGGL((glr_fwd_kernel<T, VEC, LOGITS, NORM, false>), grid, block, 0, stream, a, (int)blocks);
+    if (a.gates.in_gate) hipLaunchKernelGGL((glr_fwd_kernel<T, VEC, LOGITS, NORM, true, OUT>), grid, block, 0, stream, a, (int)blocks);
+    else hipLaunchKernelGGL((glr_fwd_kernel<T, VEC, LOGITS, NORM, false, OUT>), grid, block, 0, stream, a, (int)blocks);
     return hipGetLastError();
 }
-template <typename T, int VEC>
-hipError_t by_gate(GlrArgs a, hipStream_t stream) {
-    const hipError_t e = launch_glr_begin(a.look, (a.C + 64 * VEC - 1) / (64 * VEC), stream);
-    if (e != hipSuccess) return e;
-    if (a.gates.log_scale) return a.gates.normalize ? by_input<T, VEC, true, true>(a, stream) : by_input<T, VEC, true, false>(a, stream);
-    return a.gates.normalize ? by_input<T, VEC, false, true>(a, stream) : by_input<T, VEC, false, false>(a, stream);
+template <bool OUT, typename T, int VEC>
+hipError_t by_gate(GlrArgs &a, hipStream_t stream) {
+    if (a.gates.log_scale) return a.gates.normalize ? by_input<OUT, T, VEC, true, true>(a, stream) : by_input<OUT, T, VEC, true, false>(a, stream);
+    return a.gates.normalize ? by_input<OUT, T, VEC, false, true>(a, stream) : by_input<OUT, T, VEC, false, false>(a, stream);
+}
+template <bool OUT>
+hipError_t by_type(GlrArgs a, bool fp32, bool wide, hipStream_t stream) {
+    if (wide) return fp32 ? by_gate<OUT, float, 2>(a, stream) : by_gate<OUT, __bf16, 2>(a, stream);
+    return fp32 ? by_gate<OUT, float, 1>(a, stream) : by_gate<OUT, __bf16, 1>(a, stream);
 }
 
 template <typename T, int VEC>
@@ -183,41 +199,40 @@ hipError_t step_by_gate(const GlrStepArgs &a, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_glr_begin(GlrLook &g, int columns, hipStream_t stream) {
-    g.columns = columns;
-    g.group_there = g.tile_there + (int64_t)g.n * columns;
-    if (g.n == 1) return hipSuccess;
-    const int64_t n = g.words();
-    hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, g.ticket, n);
+hipError_t launch_glr_carry(const GlrArgs &a, bool reverse, hipStream_t stream) {
+    if (!a.tiles.front) return hipSuccess;
+    hipLaunchKernelGGL(glr_carry_kernel, dim3((unsigned)((a.C + CARRY_C - 1) / CARRY_C)), dim3(CARRY_C * CARRY_G), 0, stream, a.tiles.words, a.tiles.front,
+                       a.tiles.n, a.C, reverse ? 1 : 0);
     return hipGetLastError();
 }
 
-// Groups of about the root of half the tiles: a tile looks at up to `group` tiles with one wave, and at the groups in
-// front with seven.
-void glr_plan(GlrLook &g, int64_t rows, int tile_rows) {
-    g.n = (int)((rows + tile_rows - 1) / tile_rows);
-    g.group = 4;
-    while ((int64_t)g.group * g.group * 2 < g.n) g.group *= 2;
+// Tiles of 64 rows, or shorter ones where those leave compute units idle.
+void glr_plan(GlrArgs &a) {
+    const int64_t columns = (a.C + 127) / 128;
+    a.tiles.rows = 64;
+    while (a.tiles.rows > 16 && (a.seqs.rows + a.tiles.rows - 1) / a.tiles.rows * columns < 2048) a.tiles.rows /= 2;
+    a.tiles.n = (int)((a.seqs.rows + a.tiles.rows - 1) / a.tiles.rows);
 }
 
-void carve_glr_look(GlrLook &g, Pieces &w, int C) {
-    g.columns = (C + 63) / 64;  // the most there are
-    w.take(g.ticket, g.words());
-    g.tile_there = g.ticket ? g.ticket + 1 : nullptr;
-    w.take(g.tile, (int64_t)g.n * C);
-    w.take(g.whole, (int64_t)g.groups() * C);
+void carve_glr_tiles(GlrArgs &a, Pieces &w) {
+    const int64_t n = (int64_t)a.tiles.n * a.C;
+    w.take(a.tiles.words, a.tiles.n > 1 ? 2 * n : 0);
+    w.take(a.tiles.front, a.tiles.n > GLR_FEW ? n : 0);
+    if (a.tiles.n <= GLR_FEW) a.tiles.front = nullptr;
 }
 
 size_t carve_glr_fwd(GlrArgs &a, void *base) {
     Pieces w{static_cast<char *>(base)};
-    glr_plan(a.look, a.seqs.rows, ROWS);
-    carve_glr_look(a.look, w, a.C);
+    glr_plan(a);
+    carve_glr_tiles(a, w);
     return w.used;
 }
 
 hipError_t launch_glr_fwd(const GlrArgs &a, bool fp32, bool wide, hipStream_t stream) {
-    if (wide) return fp32 ? by_gate<float, 2>(a, stream) : by_gate<__bf16, 2>(a, stream);
-    return fp32 ? by_gate<float, 1>(a, stream) : by_gate<__bf16, 1>(a, stream);
+    hipError_t e = hipSuccess;
+    if (a.tiles.n > 1) e = by_type<false>(a, fp32, wide, stream);
+    if (e == hipSuccess) e = launch_glr_carry(a, false, stream);
+    return e == hipSuccess ? by_type<true>(a, fp32, wide, stream) : e;
 }
 
 hipError_t launch_glr_step(GlrStepArgs a, bool fp32, bool wide, hipStream_t stream) {

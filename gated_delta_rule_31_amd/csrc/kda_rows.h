@@ -73,6 +73,14 @@ struct Seqs {
     }
 };
 
+// Seqs::marks in scalar registers.
+__device__ __forceinline__ void uniform_marks(const Seqs &s, int64_t t0, int count, uint64_t &first, uint64_t &last) {
+    uint64_t f, l;
+    s.marks(t0, count, f, l);
+    first = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(f >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)f);
+    last = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(l >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)l);
+}
+
 // VEC neighbouring numbers of type T in the registers that a load gives them.
 template <typename T, int VEC>
 struct Raw {
@@ -80,6 +88,9 @@ struct Raw {
     vec v;
     __device__ __forceinline__ void load(const T *p) { v = *reinterpret_cast<const vec *>(p); }
     __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<vec *>(p) = v; }
+    // `off` bytes behind a row that all lanes share
+    __device__ __forceinline__ void load(const char *row, uint32_t off) { v = *reinterpret_cast<const vec *>(row + off); }
+    __device__ __forceinline__ void store(char *row, uint32_t off) const { *reinterpret_cast<vec *>(row + off) = v; }
     __device__ __forceinline__ void stream(T *p) const { __builtin_nontemporal_store(v, reinterpret_cast<vec *>(p)); }
     __device__ __forceinline__ float get(int i) const { return to_f32(v[i]); }
     __device__ __forceinline__ void set(int i, float x) { v[i] = from_f32<T>(x); }
@@ -90,11 +101,24 @@ struct Raw<T, 1> {
     T v;
     __device__ __forceinline__ void load(const T *p) { v = *p; }
     __device__ __forceinline__ void store(T *p) const { *p = v; }
+    __device__ __forceinline__ void load(const char *row, uint32_t off) { v = *reinterpret_cast<const T *>(row + off); }
+    __device__ __forceinline__ void store(char *row, uint32_t off) const { *reinterpret_cast<T *>(row + off) = v; }
     __device__ __forceinline__ void stream(T *p) const { *p = v; }
     __device__ __forceinline__ float get(int) const { return to_f32(v); }
     __device__ __forceinline__ void set(int, float x) { v = from_f32<T>(x); }
     __device__ __forceinline__ void zero() { v = T{}; }
 };
+// N rows `stride` bytes apart, of which the last `N - count` are the last of the `count` (> 0) again.
+template <int N, typename R>
+__device__ __forceinline__ void load_run(R (&r)[N], const char *row, int64_t stride, uint32_t off, int count) {
+    if (count >= N) {
+#pragma unroll
+        for (int u = 0; u < N; ++u, row += stride) r[u].load(row, off);
+    } else {
+#pragma unroll
+        for (int u = 0; u < N; ++u, row += u < count ? stride : 0) r[u].load(row, off);
+    }
+}
 template <int VEC>
 __device__ __forceinline__ void load_f32(float (&x)[VEC], const float *p) {
     Raw<float, VEC> r;
@@ -204,15 +228,11 @@ struct GlrGates {
     int normalize;
     int K;                       // channels that share a log_scale
 };
-// How the tiles of a channel's rows tell one another what they do to the state (kda_glr.h): n tiles in
-// groups of `group`, in `columns` columns of channels.
-struct GlrLook {
-    int n, group, columns;
-    uint32_t *ticket;                // tickets taken; behind it the flags, all zero before the launch
-    uint32_t *tile_there, *group_there;  // [n, columns], [groups, columns]
-    uint64_t *tile, *whole;          // [n, C], [groups, C]: A and H of a tile, of a group
-    __host__ __device__ int groups() const { return (n + group - 1) / group; }
-    __host__ __device__ int64_t words() const { return 1 + (int64_t)(n + groups()) * columns; }
+// The tiles that the rows are cut into, and what passes between the launches.
+struct GlrTiles {
+    int rows, n, columns;        // rows of a tile, tiles, columns of channels
+    float *words;                // [n, C, 2]: A and H of every tile
+    float *front;                // [n, C]: the state in front of every tile; null: made of the words by whoever needs it
 };
 struct GlrArgs {
     const void *x;               // [rows, C]
@@ -224,13 +244,13 @@ struct GlrArgs {
     int C;
     void *out;                   // [rows, C], or null: only what is kept is wanted
     float *kept;                 // [ceil(rows / GLR_KEPT), C] or null: the state in front of every GLR_KEPT rows
-    GlrLook look;                // workspace
+    GlrTiles tiles;              // workspace
     // gradients
     const void *d_out;           // [rows, C]
     const float *d_sf;           // [N, C] or null
     void *dx, *d_gate, *d_in;    // [rows, C]
     float *ds0;                  // [N, C] or null
-    float *part;                 // [tiles, 2, C] or null
+    float *part;                 // [n, 2, C] or null
 };
 struct GlrStepArgs {
     const void *x;               // [B, S, C]
@@ -240,12 +260,12 @@ struct GlrStepArgs {
     int B, S, C, vecs;
     void *out;
 };
-constexpr int GLR_KEPT = 64;     // rows between two kept states
+constexpr int GLR_KEPT = 8;      // rows between two kept states
 size_t carve_glr_fwd(GlrArgs &a, void *base);
-size_t carve_glr_bwd(GlrArgs &a, void *base, bool kept, float *&sums, void *&more);
+size_t carve_glr_bwd(GlrArgs &a, void *base, bool kept, float *&sums);
 // wide: two channels at a time
 hipError_t launch_glr_fwd(const GlrArgs &a, bool fp32, bool wide, hipStream_t stream);
-hipError_t launch_glr_bwd(const GlrArgs &a, bool fp32, bool wide, float *sums, void *more, float *d_log_scale, float *d_bias, hipStream_t stream);
+hipError_t launch_glr_bwd(const GlrArgs &a, bool fp32, bool wide, bool kept, float *sums, float *d_log_scale, float *d_bias, hipStream_t stream);
 hipError_t launch_glr_step(GlrStepArgs a, bool fp32, bool wide, hipStream_t stream);
 
 // ------------------------------------------------------------------ norms between blocks

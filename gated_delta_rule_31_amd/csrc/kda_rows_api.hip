@@ -121,10 +121,10 @@ kda_status glr_gates(kda::GlrGates &g, const void *gate, int64_t gate_stride, co
     return KDA_OK;
 }
 bool glr_fits(const kda::Seqs &s, int C) {
-    const int64_t tiles = (s.rows + kda::GLR_KEPT - 1) / kda::GLR_KEPT;
-    return tiles * ((C + 63) / 64) * 512 < MAX_GRID && (int64_t)s.N * C < MAX_GRID;
+    const int64_t tiles = (s.rows + 63) / 64;  // where there are many
+    return tiles * ((C + 63) / 64 * 64) < MAX_GRID && (int64_t)s.N * C < MAX_GRID;
 }
-int64_t glr_kept_rows(int64_t rows) { return ((rows + kda::GLR_KEPT - 1) / kda::GLR_KEPT); }
+int64_t glr_kept_rows(int64_t rows) { return (rows + kda::GLR_KEPT - 1) / kda::GLR_KEPT; }
 
 kda_status norm_shape(kda_dtype dtype, kda_dtype h_dtype, int64_t tokens, int heads, int D, float eps, unsigned flags) {
     if (tokens < 0 || heads <= 0 || D <= 0) return KDA_ERR_BAD_SHAPE;
@@ -281,8 +281,7 @@ size_t kda_glr_bwd_workspace_size(int B, int64_t T, int H, int K, int logits, in
     static const float some = 0.f;
     a.gates.log_scale = logits ? &some : nullptr;
     float *sums;
-    void *more;
-    return glr_fits(a.seqs, a.C) ? kda::carve_glr_bwd(a, nullptr, kept != 0, sums, more) : 0;
+    return glr_fits(a.seqs, a.C) ? kda::carve_glr_bwd(a, nullptr, kept != 0, sums) : 0;
 }
 
 kda_status kda_glr_fwd(const void *x, int64_t x_stride, kda_dtype dtype, const void *gate, int64_t gate_stride, const float *log_scale,
@@ -365,14 +364,13 @@ kda_status kda_glr_bwd(const void *x, int64_t x_stride, kda_dtype dtype, const v
     a.d_in = d_in_gate;
     a.ds0 = d_initial_state;
     float *sums;
-    void *more;
     if (workspace_bytes < kda_glr_bwd_workspace_size(B, T, H, K, log_scale != nullptr, kept != nullptr)) return KDA_ERR_BAD_ARGUMENT;
-    kda::carve_glr_bwd(a, workspace, kept != nullptr, sums, more);
+    kda::carve_glr_bwd(a, workspace, kept != nullptr, sums);
     if (!d_log_scale && !d_bias) a.part = nullptr;
     Pairs w;
     w.rows(x, e, x_stride).rows(gate, gate_size, gate_stride).rows(in_gate, e, in_stride).rows(d_out, e, C).rows(dx, e, C).rows(d_gate, gate_size, C);
     w.rows(in_gate ? d_in_gate : nullptr, e, C).rows(initial_state, 4, C).rows(kept, 4, C).rows(d_final_state, 4, C).rows(d_initial_state, 4, C);
-    return done(kda::launch_glr_bwd(a, dtype == KDA_F32, w.ok, sums, more, d_log_scale, d_bias, stream));
+    return done(kda::launch_glr_bwd(a, dtype == KDA_F32, w.ok, kept != nullptr, sums, d_log_scale, d_bias, stream));
 }
 
 kda_status kda_glr_step(const void *x, kda_dtype dtype, const void *gate, const float *log_scale, const float *bias, float lower_bound,

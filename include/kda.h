@@ -525,7 +525,7 @@ kda_status kda_short_conv_step(const void *x, kda_dtype dtype, const float *weig
  *   log_scale [H], bias [H K] float32 or NULL (a bias only with log_scale)
  *   in_gate  [B, T, H, K] in dtype (i_t), or NULL: the input as it is
  *   initial_state, final_state [N, H, K] float32 or NULL
- *   kept     float32, kda_glr_kept_size bytes, or NULL: the state in front of every 64 rows, for kda_glr_bwd
+ *   kept     float32, kda_glr_kept_size bytes, or NULL: the state in front of every 8 rows, for kda_glr_bwd
  *   workspace  16-byte aligned scratch, required
  */
 size_t kda_glr_kept_size(int B, int64_t T, int H, int K);

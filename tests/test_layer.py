@@ -54,7 +54,7 @@ def test_workspaces(lib):
     assert size(torch.bfloat16, 1, 0, 64, 4) == 0 and size(torch.bfloat16, 1, 64, 64, 5) == 0 and size(torch.bfloat16, 1 << 20, 1 << 62, 64, 4) == 0
     need = size(torch.bfloat16, 1, 64, 64, 4)
     assert _conv_bwd(lib, wsz=need - 1) == 5
-    assert kda.glr_kept_size(2, 65, 3, 5) == 3 * 15 * 4  # 130 rows, a state in front of every 64
+    assert kda.glr_kept_size(2, 65, 3, 5) == 17 * 15 * 4  # 130 rows, a state in front of every 8
     assert kda.glr_kept_size(2, 0, 3, 5) == 0 and kda.glr_fwd_workspace_size(0, 5, 1, 1) == 0 and kda.glr_fwd_workspace_size(1, 1 << 31, 1, 1) == 0
     assert kda.glr_bwd_workspace_size(1, 64, 2, 16, True, False) > kda.glr_bwd_workspace_size(1, 64, 2, 16, True, True) > kda.glr_bwd_workspace_size(1, 64, 2, 16, False, True) > 0
     assert _glr(lib, wsz=kda.glr_fwd_workspace_size(1, 64, 2, 16) - 1) == 5
