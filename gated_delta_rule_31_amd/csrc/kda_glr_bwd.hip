@@ -55,8 +55,8 @@ __global__ __launch_bounds__(64 * WAVES) void glr_back_kernel(const GlrArgs a) {
                 }
             if (r > 0) fetch(r - U);
             const uint32_t last = (uint32_t)(p.last >> r) & ((1u << U) - 1);
-            auto rows = [&](auto here) {
-                constexpr bool HERE = decltype(here)::value;
+            auto rows = [&](auto marked) {
+                constexpr bool HERE = decltype(marked)::value;
 #pragma unroll
                 for (int u = U - 1; u >= 0; --u) {
                     if (HERE && r + u >= p.own) continue;
@@ -124,38 +124,26 @@ __global__ __launch_bounds__(64 * WAVES) void glr_bwd_kernel(const GlrArgs a, in
     }
     GateConst<VEC, LOGITS> k;
     k.load(a.gates, p.c);
-    float m[VEC], dz_sum[VEC] = {}, u_sum[VEC] = {};
+    float m[VEC], dz_sum[VEC] = {}, u_sum[VEC] = {}, slope[VEC];  // u_sum: of log2(e) u dz
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) slope[i] = k.scale2[i] * (a.gates.lower / LOG2E);  // lower e^A
     glr_front<VEC>(m, a, a.tiles.front, p.tile, p.c, true);
     if (p.own > 0)
         for (int r = begin; r >= 0; r -= U) {
-            // decay; input, then the state in front; f i; i; a^2 / f^2; p (1 - p)
-            float av[U][VEC], bv[U][VEC], fi[U][VEC], iv[U][VEC], wv[U][VEC], pq[U][VEC], h[VEC];
-            Raw<T, VEC> rx[U], rd[U];
+            // What a row's lambda is multiplied by: a for m, f i for dx, f i (1 - i) x for d in, and for dz
+            // (a h_{t-1} - f i x a^2 / f^2) lower p (1 - p) e^A (without logits the bracket alone)
+            float av[U][VEC], xv[U][VEC], iv[U][VEC], gv[U][VEC], h[VEC];
+            Raw<T, VEC> rd[U];
             Raw<Z, VEC> rz[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                rx[u] = nx[u];
-                rd[u] = nd[u];
-                rz[u] = nz[u];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const Gate g = make_gate<LOGITS, NORM, GATED>(nz[u].get(i), GATED ? ni[u].get(i) : 0.f, k.scale2[i], k.bias2[i], a.gates.lower);
-                    av[u][i] = g.a;
-                    fi[u][i] = g.f * g.i;
-                    iv[u][i] = g.i;
-                    pq[u][i] = g.p * g.q;
-                    if constexpr (NORM) wv[u][i] = g.f > 0.f ? g.a * g.a * __builtin_amdgcn_rcpf(g.f * g.f) : 0.f;
-                    bv[u][i] = fi[u][i] * rx[u].get(i);
-                }
-            }
+            const uint32_t first = (uint32_t)(p.first >> r) & ((1u << U) - 1), last = (uint32_t)(p.last >> r) & ((1u << U) - 1);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) h[i] = nh.get(i);
-            if (r > 0) fetch(r - U);
-            const uint32_t first = (uint32_t)(p.first >> r) & ((1u << U) - 1), last = (uint32_t)(p.last >> r) & ((1u << U) - 1);
-            auto rows = [&](auto here) {
-                constexpr bool HERE = decltype(here)::value;
+            auto rows = [&](auto marked) {
+                constexpr bool HERE = decltype(marked)::value;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
+                    rd[u] = nd[u];
+                    rz[u] = nz[u];
                     if (HERE && first >> u & 1) {
 #pragma unroll
                         for (int i = 0; i < VEC; ++i) h[i] = 0.f;
@@ -163,11 +151,19 @@ __global__ __launch_bounds__(64 * WAVES) void glr_bwd_kernel(const GlrArgs a, in
                     }
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) {
-                        const float next = fmaf(av[u][i], h[i], bv[u][i]);
-                        bv[u][i] = h[i];
-                        h[i] = next;
+                        const Gate g = make_gate<LOGITS, NORM, GATED>(rz[u].get(i), GATED ? ni[u].get(i) : 0.f, k.scale2[i], k.bias2[i], a.gates.lower);
+                        const float fi = g.f * g.i, b = fi * nx[u].get(i);
+                        av[u][i] = g.a;
+                        xv[u][i] = fi;
+                        if constexpr (GATED) iv[u][i] = b * g.j;
+                        float w = g.a * h[i];
+                        h[i] = w + b;
+                        if constexpr (NORM) w = fmaf(-b, g.f > 0.f ? g.a * g.a * __builtin_amdgcn_rcpf(g.f * g.f) : 0.f, w);
+                        gv[u][i] = LOGITS ? w * slope[i] * g.p * g.q : w;
                     }
                 }
+                if (r > 0) fetch(r - U);
+                const uint32_t ot = here(ct), og = here(cz);
 #pragma unroll
                 for (int u = U - 1; u >= 0; --u) {
                     if (HERE && r + u >= p.own) continue;
@@ -182,23 +178,18 @@ __global__ __launch_bounds__(64 * WAVES) void glr_bwd_kernel(const GlrArgs a, in
                     for (int i = 0; i < VEC; ++i) {
                         const float lam = rd[u].get(i) + m[i];
                         m[i] = av[u][i] * lam;
-                        const float v = lam * fi[u][i], b = v * rx[u].get(i);
-                        ox.set(i, v);
-                        if constexpr (GATED) oi.set(i, fmaf(-b, iv[u][i], b));
-                        float dg = m[i] * bv[u][i];
-                        if constexpr (NORM) dg = fmaf(-b, wv[u][i], dg);
+                        ox.set(i, lam * xv[u][i]);
+                        if constexpr (GATED) oi.set(i, lam * iv[u][i]);
+                        const float t = lam * gv[u][i];
+                        oz.set(i, t);
                         if constexpr (LOGITS) {
-                            const float du = dg * a.gates.lower * pq[u][i], t = (k.scale2[i] * (1.f / LOG2E)) * du;
-                            u_sum[i] = fmaf(fmaf(k.scale2[i], rz[u].get(i), k.bias2[i]), du, u_sum[i]);
+                            u_sum[i] = fmaf(fmaf(k.scale2[i], rz[u].get(i), k.bias2[i]), t, u_sum[i]);
                             dz_sum[i] += t;
-                            oz.set(i, t);
-                        } else {
-                            oz.set(i, dg);
                         }
                     }
-                    ox.store(dx + (r + u) * st, ct);
-                    oz.store(dz + (r + u) * sg, cz);
-                    if constexpr (GATED) oi.store(di + (r + u) * st, ct);
+                    ox.store(dx + (r + u) * st, ot);
+                    oz.store(dz + (r + u) * sg, og);
+                    if constexpr (GATED) oi.store(di + (r + u) * st, ot);
                     if (HERE && a.ds0 && first >> u & 1) {
                         Raw<float, VEC> s;
 #pragma unroll
@@ -215,7 +206,7 @@ __global__ __launch_bounds__(64 * WAVES) void glr_bwd_kernel(const GlrArgs a, in
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
             s.set(i, dz_sum[i]);
-            t.set(i, u_sum[i] * (1.f / LOG2E));
+            t.set(i, k.scale2[i] > 0.f ? u_sum[i] / k.scale2[i] : 0.f);  // sum u du, du = dz e^-A
         }
         s.store(a.part + (int64_t)p.tile * 2 * a.C + p.c);
         t.store(a.part + (int64_t)p.tile * 2 * a.C + a.C + p.c);

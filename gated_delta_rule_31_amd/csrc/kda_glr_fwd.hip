@@ -68,8 +68,9 @@ __global__ __launch_bounds__(64 * WAVES) void glr_fwd_kernel(const GlrArgs a, in
         }
         const uint32_t first = (uint32_t)(p.first >> r) & ((1u << U) - 1), last = (uint32_t)(p.last >> r) & ((1u << U) - 1);
         // HERE: a sequence begins or ends among these rows, or the rows end
-        auto rows = [&](auto here) {
-            constexpr bool HERE = decltype(here)::value;
+        auto rows = [&](auto marked) {
+            constexpr bool HERE = decltype(marked)::value;
+            const uint32_t ot = here(p.c * (uint32_t)sizeof(T));
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (HERE && r + u >= p.count) continue;
@@ -86,7 +87,7 @@ __global__ __launch_bounds__(64 * WAVES) void glr_fwd_kernel(const GlrArgs a, in
                     else A[i] *= av[u][i];
                 }
                 if constexpr (OUT) {
-                    if (a.out && (!HERE || r + u < p.own)) y.store(out + (int64_t)(r + u) * a.C * sizeof(T), p.c * (uint32_t)sizeof(T));
+                    if (a.out && (!HERE || r + u < p.own)) y.store(out + (int64_t)(r + u) * a.C * sizeof(T), ot);
                     if (HERE && a.sf && last >> u & 1) {
                         Raw<float, VEC> s;
 #pragma unroll

@@ -108,16 +108,19 @@ struct Raw<T, 1> {
     __device__ __forceinline__ void set(int, float x) { v = from_f32<T>(x); }
     __device__ __forceinline__ void zero() { v = T{}; }
 };
+// The same offset, made anew where it is used: the compiler then addresses by a scalar base and a 32-bit
+// offset, where it would keep (and add up) 64-bit addresses in vector registers.
+__device__ __forceinline__ uint32_t here(uint32_t off) {
+    asm volatile("" : "+v"(off));
+    return off;
+}
+
 // N rows `stride` bytes apart, of which the last `N - count` are the last of the `count` (> 0) again.
 template <int N, typename R>
 __device__ __forceinline__ void load_run(R (&r)[N], const char *row, int64_t stride, uint32_t off, int count) {
-    if (count >= N) {
+    const uint32_t at = here(off);
 #pragma unroll
-        for (int u = 0; u < N; ++u, row += stride) r[u].load(row, off);
-    } else {
-#pragma unroll
-        for (int u = 0; u < N; ++u, row += u < count ? stride : 0) r[u].load(row, off);
-    }
+    for (int u = 0; u < N; ++u, row += u < count ? stride : 0) r[u].load(row, at);
 }
 template <int VEC>
 __device__ __forceinline__ void load_f32(float (&x)[VEC], const float *p) {
