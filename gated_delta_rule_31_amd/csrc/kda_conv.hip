@@ -70,24 +70,26 @@ __global__ __launch_bounds__(64 * WAVES) void conv_fwd_kernel(const ConvArgs a, 
         return empty_states(a.seqs, blockIdx.x - blocks, (int64_t)(W - 1) * a.D, static_cast<const T *>(a.s0), static_cast<T *>(a.sf));
     const int wave = blockIdx.x * WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
     const int tiles = (a.vecs + 63) / 64, run = wave / tiles, v = wave % tiles * 64 + lane, c = v * VEC;
-    const int64_t t0 = (int64_t)run * a.run, limit = a.seqs.limit();
+    const int64_t t0 = (int64_t)run * a.run, limit = __builtin_amdgcn_readfirstlane((int)a.seqs.limit());
     if (run >= a.runs || v >= a.vecs || t0 >= limit) return;
     const int count = (int)(limit - t0 < a.run ? limit - t0 : a.run);
     uint64_t first, last;
-    a.seqs.marks(t0, count, first, last);
+    uniform_marks(a.seqs, t0, count, first, last);
     float w[W][VEC], b[VEC], f[W - 1][VEC];
     taps<VEC, W>(w, b, a.weight, a.bias, c);
     window<T, VEC, W>(f, a, t0, c);
-    const T *x = static_cast<const T *>(a.x) + t0 * a.x_stride + c;
-    T *out = static_cast<T *>(a.out) + t0 * a.D + c;
-    constexpr int U = 8;
+    const int64_t sx = a.x_stride * sizeof(T), sd = a.D * sizeof(T);
+    const char *x = static_cast<const char *>(a.x) + t0 * sx;
+    char *out = static_cast<char *>(a.out) + t0 * sd;
+    const uint32_t ct = c * (uint32_t)sizeof(T);
+    constexpr int U = 16;
     for (int t = 0; t < count; t += U) {
         Raw<T, VEC> r[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) r[u].load(x + (int64_t)(t + u < count ? t + u : count - 1) * a.x_stride);
+        load_run(r, x + t * sx, sx, ct, count - t);
+        const uint32_t ot = here(ct);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (t + u >= count) break;
+            if (t + u >= count) continue;
             if (t + u > 0 && first >> (t + u) & 1) window<T, VEC, W>(f, a, t0 + t + u, c);
             Raw<T, VEC> y;
 #pragma unroll
@@ -96,7 +98,7 @@ __global__ __launch_bounds__(64 * WAVES) void conv_fwd_kernel(const ConvArgs a, 
                 y.set(i, a.silu ? pre * sigmoid_f32(pre) : pre);
                 shift<VEC, W>(f, xi, i);
             }
-            y.store(out + (int64_t)(t + u) * a.D);
+            y.store(out + (t + u) * sd, ot);
             if (a.sf && last >> (t + u) & 1) {
                 T *to = static_cast<T *>(a.sf) + (int64_t)a.seqs.of(t0 + t + u) * (W - 1) * a.D + c;
 #pragma unroll
@@ -123,7 +125,7 @@ __global__ __launch_bounds__(64 * WAVES) void conv_bwd_kernel(const ConvArgs a, 
     const int wave = blockIdx.x * WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
     const int tiles = (a.vecs + 63) / 64, run = wave / tiles, v = wave % tiles * 64 + lane, c = v * VEC;
     if (run >= a.runs || v >= a.vecs) return;
-    const int64_t t0 = (int64_t)run * a.run, limit = a.seqs.limit();
+    const int64_t t0 = (int64_t)run * a.run, limit = __builtin_amdgcn_readfirstlane((int)a.seqs.limit());
     const int rows = (int)(a.seqs.rows - t0 < a.run ? a.seqs.rows - t0 : a.run);          // of this run
     const int own = (int)(limit - t0 < 0 ? 0 : limit - t0 < rows ? limit - t0 : rows);     // of them in a sequence
     const int count = (int)(limit - t0 < 0 ? 0 : limit - t0 < own + W - 1 ? limit - t0 : own + W - 1);
@@ -131,13 +133,15 @@ __global__ __launch_bounds__(64 * WAVES) void conv_bwd_kernel(const ConvArgs a, 
     float dw[W][VEC] = {}, db[VEC] = {};
     if (own > 0) {
         uint64_t first, last;
-        a.seqs.marks(t0, count, first, last);
+        uniform_marks(a.seqs, t0, count, first, last);
         float w[W][VEC], b[VEC], f[W - 1][VEC], acc[W][VEC] = {};
         taps<VEC, W>(w, b, a.weight, a.bias, c);
         window<T, VEC, W>(f, a, t0, c);
         int n = a.seqs.of(t0);
         int64_t begin = a.seqs.begin(n, t0) - t0;  // of the sequence, counted from t0 as t below
-        const T *x = static_cast<const T *>(a.x) + t0 * a.x_stride + c, *d_out = static_cast<const T *>(a.d_out) + t0 * a.D + c;
+        const int64_t sx = a.x_stride * sizeof(T), sd = a.D * sizeof(T);
+        const char *x = static_cast<const char *>(a.x) + t0 * sx, *d_out = static_cast<const char *>(a.d_out) + t0 * sd;
+        const uint32_t ct = c * (uint32_t)sizeof(T);
         auto close = [&](int64_t s, const float(&g)[VEC]) {  // the sum of row s is whole
             Raw<T, VEC> r;
 #pragma unroll
@@ -151,15 +155,11 @@ __global__ __launch_bounds__(64 * WAVES) void conv_bwd_kernel(const ConvArgs a, 
         constexpr int U = 4;
         for (int t = 0; t < count; t += U) {
             Raw<T, VEC> rx[U], rd[U];
+            load_run(rx, x + t * sx, sx, ct, count - t);
+            load_run(rd, d_out + t * sd, sd, ct, count - t);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t at = t + u < count ? t + u : count - 1;
-                rx[u].load(x + at * a.x_stride);
-                rd[u].load(d_out + at * a.D);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (t + u >= count) break;
+                if (t + u >= count) continue;
                 if (t + u > 0 && first >> (t + u) & 1) {
                     window<T, VEC, W>(f, a, t0 + t + u, c);
                     n = a.seqs.of(t0 + t + u);
@@ -214,14 +214,13 @@ __global__ __launch_bounds__(64 * WAVES) void conv_bwd_kernel(const ConvArgs a, 
     Raw<T, VEC> zero;
     zero.zero();
     for (int t = own; t < rows; ++t) zero.store(dx + (int64_t)t * a.D);
-    if (a.part) {
-        float *part = a.part + (int64_t)run * (W + 1) * a.D + c;
+    if (!a.part) return;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
+    for (int j = 0; j <= W; ++j) {
+        Raw<float, VEC> s;
 #pragma unroll
-            for (int j = 0; j < W; ++j) part[(int64_t)j * a.D + i] = dw[j][i];
-            part[(int64_t)W * a.D + i] = db[i];
-        }
+        for (int i = 0; i < VEC; ++i) s.set(i, j < W ? dw[j < W ? j : 0][i] : db[i]);
+        s.store(a.part + ((int64_t)run * (W + 1) + j) * a.D + c);
     }
 }
 
@@ -241,9 +240,13 @@ __global__ __launch_bounds__(64) void conv_step_kernel(const ConvStepArgs a) {
         f[j].zero();
         if (from >= 0) f[j].load(states + (from * (W - 1) + j) * a.D);
     }
+    Raw<T, VEC> next;
+    next.load(x);
     for (int t = 0; t < len; ++t) {
-        Raw<T, VEC> r, y;
-        r.load(x + (int64_t)t * a.D);
+        const Raw<T, VEC> r = next;
+        Raw<T, VEC> y;
+        if (t + 1 < len) next.load(x + (int64_t)(t + 1) * a.D);
+        const int64_t to = a.slots.to(b, t, len);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
             float pre = bias[i];
@@ -256,7 +259,6 @@ __global__ __launch_bounds__(64) void conv_step_kernel(const ConvStepArgs a) {
 #pragma unroll
         for (int j = 0; j + 1 < W - 1; ++j) f[j] = f[j + 1];
         f[W - 2] = r;
-        const int64_t to = a.slots.to(b, t, len);
         if (to >= 0)
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) f[j].store(states + (to * (W - 1) + j) * a.D);
@@ -266,8 +268,7 @@ __global__ __launch_bounds__(64) void conv_step_kernel(const ConvStepArgs a) {
 enum { FWD, BWD };
 template <int KIND, typename T, int VEC>
 hipError_t by_taps(const ConvArgs &a, hipStream_t stream) {
-    const int64_t waves = (int64_t)((a.vecs + 63) / 64) * a.runs;
-    const int blocks = (int)((waves + WAVES - 1) / WAVES);
+    const int blocks = (int)(((int64_t)((a.vecs + 63) / 64) * a.runs + WAVES - 1) / WAVES);
     const bool states = a.seqs.cu && (KIND == FWD ? a.sf : a.ds0);
     const int64_t more = states ? ((int64_t)a.seqs.N * (a.W - 1) * a.D + 64 * WAVES - 1) / (64 * WAVES) : 0;
     const dim3 grid((unsigned)(blocks + more)), block(64 * WAVES);
@@ -282,9 +283,10 @@ hipError_t by_taps(const ConvArgs &a, hipStream_t stream) {
 }
 template <int KIND>
 hipError_t by_type(ConvArgs &a, bool fp32, bool wide, hipStream_t stream) {
-    a.vecs = wide ? a.D / (fp32 ? 4 : 8) : a.D;
+    constexpr int VEC = KIND == FWD ? CONV_FWD_VEC : CONV_BWD_VEC;
+    a.vecs = wide ? a.D / VEC : a.D;
     conv_runs(a.seqs.rows, a.vecs, a.run, a.runs);
-    if (wide) return fp32 ? by_taps<KIND, float, 4>(a, stream) : by_taps<KIND, __bf16, 8>(a, stream);
+    if (wide) return fp32 ? by_taps<KIND, float, VEC>(a, stream) : by_taps<KIND, __bf16, VEC>(a, stream);
     return fp32 ? by_taps<KIND, float, 1>(a, stream) : by_taps<KIND, __bf16, 1>(a, stream);
 }
 
@@ -318,8 +320,8 @@ hipError_t launch_conv_bwd(ConvArgs a, bool fp32, bool wide, float *d_weight, fl
 }
 
 hipError_t launch_conv_step(ConvStepArgs a, bool fp32, bool wide, hipStream_t stream) {
-    a.vecs = wide ? a.D / (fp32 ? 4 : 8) : a.D;
-    if (wide) return fp32 ? step_by_taps<float, 4>(a, stream) : step_by_taps<__bf16, 8>(a, stream);
+    a.vecs = wide ? a.D / CONV_STEP_VEC : a.D;
+    if (wide) return fp32 ? step_by_taps<float, CONV_STEP_VEC>(a, stream) : step_by_taps<__bf16, CONV_STEP_VEC>(a, stream);
     return fp32 ? step_by_taps<float, 1>(a, stream) : step_by_taps<__bf16, 1>(a, stream);
 }
 

@@ -214,6 +214,7 @@ struct ConvStepArgs {
     int B, S, D, W, silu, vecs;
     void *out;
 };
+constexpr int CONV_FWD_VEC = 2, CONV_BWD_VEC = 4, CONV_STEP_VEC = 2;  // channels of a lane, where rows allow it
 void conv_runs(int64_t rows, int vecs, int &run, int &runs);
 hipError_t launch_conv_fwd(ConvArgs a, bool fp32, bool wide, hipStream_t stream);
 hipError_t launch_conv_bwd(ConvArgs a, bool fp32, bool wide, float *d_weight, float *d_bias, hipStream_t stream);

@@ -32,11 +32,12 @@ struct Wide {
         return *this;
     }
 };
-// Likewise two channels at a time, for `n` numbers of `size` bytes apart.
-struct Pairs {
+// Likewise `unit` channels at a time, for rows `n` numbers of `size` bytes apart.
+struct Units {
+    int unit;
     bool ok = true;
-    Pairs &rows(const void *p, size_t size, int64_t n) {
-        ok = ok && (!p || ((uintptr_t)p % (2 * size) == 0 && n % 2 == 0));
+    Units &rows(const void *p, size_t size, int64_t n) {
+        ok = ok && (!p || ((uintptr_t)p % (unit * size) == 0 && n % unit == 0));
         return *this;
     }
 };
@@ -100,7 +101,6 @@ bool conv_fits(const kda::Seqs &s, int D, int W) {
     kda::conv_runs(s.rows, D, run, runs);
     return (int64_t)runs * ((D + 63) / 64 * 64) < MAX_GRID && (int64_t)s.N * (W - 1) * D < MAX_GRID;
 }
-int conv_vecs(kda_dtype dtype, int D) { return dtype == KDA_F32 ? D / 4 : D / 8; }
 
 kda_status glr_gates(kda::GlrGates &g, const void *gate, int64_t gate_stride, const float *log_scale, const float *bias, float lower_bound,
                      const void *in_gate, int64_t in_stride, unsigned flags, int H, int K) {
@@ -166,8 +166,9 @@ kda_status kda_short_conv_fwd(const void *x, int64_t x_stride, kda_dtype dtype, 
     a.W = W;
     a.silu = (flags & KDA_SILU) != 0;
     a.out = out;
-    Wide w{size_of(dtype)};
-    w.ptr(x).ptr(initial_state).ptr(final_state).ptr(out).stride(x_stride).stride(D);
+    const size_t e = size_of(dtype);
+    Units w{kda::CONV_FWD_VEC};
+    w.rows(x, e, x_stride).rows(initial_state, e, D).rows(final_state, e, D).rows(out, e, D);
     return done(kda::launch_conv_fwd(a, dtype == KDA_F32, w.ok, stream));
 }
 
@@ -177,7 +178,7 @@ size_t kda_short_conv_bwd_workspace_size(kda_dtype dtype, int B, int64_t T, int 
     if (conv_shape(dtype, D, W, 0) != KDA_OK || batch(s, nullptr, 0, B, T, &empty) != KDA_OK || empty || !conv_fits(s, D, W)) return 0;
     // the widest and the narrowest loads go by runs of their own length; both fit
     int run, wide, narrow;
-    kda::conv_runs(s.rows, conv_vecs(dtype, D) > 0 ? conv_vecs(dtype, D) : 1, run, wide);
+    kda::conv_runs(s.rows, D / kda::CONV_BWD_VEC > 0 ? D / kda::CONV_BWD_VEC : 1, run, wide);
     kda::conv_runs(s.rows, D, run, narrow);
     return (size_t)(wide > narrow ? wide : narrow) * (W + 1) * D * sizeof(float);
 }
@@ -222,8 +223,9 @@ kda_status kda_short_conv_bwd(const void *x, int64_t x_stride, kda_dtype dtype, 
     a.dx = dx;
     a.ds0 = d_initial_state;
     a.part = sums ? static_cast<float *>(workspace) : nullptr;
-    Wide w{size_of(dtype)};
-    w.ptr(x).ptr(initial_state).ptr(d_out).ptr(d_final_state).ptr(dx).ptr(d_initial_state).stride(x_stride).stride(D);
+    const size_t e = size_of(dtype);
+    Units w{kda::CONV_BWD_VEC};
+    w.rows(x, e, x_stride).rows(initial_state, e, D).rows(d_out, e, D).rows(d_final_state, e, D).rows(dx, e, D).rows(d_initial_state, e, D);
     return done(kda::launch_conv_bwd(a, dtype == KDA_F32, w.ok, d_weight, d_bias, stream));
 }
 
@@ -253,8 +255,9 @@ kda_status kda_short_conv_step(const void *x, kda_dtype dtype, const float *weig
     a.W = W;
     a.silu = (flags & KDA_SILU) != 0;
     a.out = out;
-    Wide w{size_of(dtype)};
-    w.ptr(x).ptr(states).ptr(out).stride(D);
+    const size_t e = size_of(dtype);
+    Units w{kda::CONV_STEP_VEC};
+    w.rows(x, e, D).rows(states, e, D).rows(out, e, D);
     return done(kda::launch_conv_step(a, dtype == KDA_F32, w.ok, stream));
 }
 
@@ -316,7 +319,7 @@ kda_status kda_glr_fwd(const void *x, int64_t x_stride, kda_dtype dtype, const v
     if (workspace_bytes < kda_glr_fwd_workspace_size(B, T, H, K)) return KDA_ERR_BAD_ARGUMENT;
     kda::carve_glr_fwd(a, workspace);
     const size_t e = size_of(dtype);
-    Pairs w;
+    Units w{2};
     w.rows(x, e, x_stride).rows(gate, gate_size, gate_stride).rows(in_gate, e, in_stride).rows(out, e, C);
     w.rows(initial_state, 4, C).rows(final_state, 4, C).rows(kept, 4, C);
     return done(kda::launch_glr_fwd(a, dtype == KDA_F32, w.ok, stream));
@@ -367,7 +370,7 @@ kda_status kda_glr_bwd(const void *x, int64_t x_stride, kda_dtype dtype, const v
     if (workspace_bytes < kda_glr_bwd_workspace_size(B, T, H, K, log_scale != nullptr, kept != nullptr)) return KDA_ERR_BAD_ARGUMENT;
     kda::carve_glr_bwd(a, workspace, kept != nullptr, sums);
     if (!d_log_scale && !d_bias) a.part = nullptr;
-    Pairs w;
+    Units w{2};
     w.rows(x, e, x_stride).rows(gate, gate_size, gate_stride).rows(in_gate, e, in_stride).rows(d_out, e, C).rows(dx, e, C).rows(d_gate, gate_size, C);
     w.rows(in_gate ? d_in_gate : nullptr, e, C).rows(initial_state, 4, C).rows(kept, 4, C).rows(d_final_state, 4, C).rows(d_initial_state, 4, C);
     return done(kda::launch_glr_bwd(a, dtype == KDA_F32, w.ok, kept != nullptr, sums, d_log_scale, d_bias, stream));
@@ -396,7 +399,7 @@ kda_status kda_glr_step(const void *x, kda_dtype dtype, const void *gate, const 
     a.B = B;
     a.S = S;
     a.out = out;
-    Pairs w;
+    Units w{2};
     w.rows(x, e, C).rows(gate, gate_size, C).rows(in_gate, e, C).rows(states, 4, C).rows(out, e, C);
     return done(kda::launch_glr_step(a, dtype == KDA_F32, w.ok, stream));
 }
