@@ -157,11 +157,11 @@ def _load():
     lib.kda_glr_bwd.restype = i32
     lib.kda_glr_step.argtypes = [vp, i32, vp, vp, vp, f32, vp, u32, vp, i64, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp]
     lib.kda_glr_step.restype = i32
-    lib.kda_block_norm_fwd.argtypes = [vp, vp, i64, i32, vp, i32, vp, vp, i64, i32, i32, f32, f32, u32, vp, vp, vp]
+    lib.kda_block_norm_fwd.argtypes = [vp, vp, i64, i64, i32, vp, i32, vp, vp, i64, i32, i32, f32, f32, u32, vp, vp, vp]
     lib.kda_block_norm_fwd.restype = i32
     lib.kda_block_norm_bwd_workspace_size.argtypes = [i64, i32, i32]
     lib.kda_block_norm_bwd_workspace_size.restype = sz
-    lib.kda_block_norm_bwd.argtypes = [vp, vp, i64, i32, vp, i32, vp, vp, i64, i32, i32, f32, f32, u32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.kda_block_norm_bwd.argtypes = [vp, vp, i64, i64, i32, vp, i32, vp, vp, i64, i32, i32, f32, f32, u32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.kda_block_norm_bwd.restype = i32
     lib.kda_status_string.argtypes = [i32]
     lib.kda_status_string.restype = ctypes.c_char_p

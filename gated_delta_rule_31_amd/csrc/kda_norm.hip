@@ -65,6 +65,11 @@ __device__ __forceinline__ void load_rows(Raw<T, VEC> (&r)[NV], const void *p, i
     }
 }
 
+__device__ __forceinline__ int64_t gate_row(const NormArgs &a, int64_t row) {
+    const uint32_t token = (uint32_t)row / (uint32_t)a.heads, head = (uint32_t)row - token * (uint32_t)a.heads;  // fewer than 2^31 rows
+    return token * a.gate_stride + head * a.gate_head;
+}
+
 // T: y, the gate and n; R: the residual stream
 template <typename T, typename R, int VEC, int LANES, int NV>
 __global__ __launch_bounds__(THREADS<LANES>) void norm_fwd_kernel(const NormArgs a) {
@@ -80,7 +85,7 @@ __global__ __launch_bounds__(THREADS<LANES>) void norm_fwd_kernel(const NormArgs
         Raw<T, VEC> y[NV], z[NV];
         Raw<R, VEC> x[NV];
         load_rows<T, VEC, LANES, NV>(y, a.y, row * a.D, lane, vecs);
-        if (a.gate) load_rows<T, VEC, LANES, NV>(z, a.gate, row / a.heads * a.gate_stride + row % a.heads * a.D, lane, vecs);
+        if (a.gate) load_rows<T, VEC, LANES, NV>(z, a.gate, gate_row(a, row), lane, vecs);
         if (a.residual) load_rows<R, VEC, LANES, NV>(x, a.residual, row * a.D, lane, vecs);
         float r = a.scale;
         if (a.after) {
@@ -142,7 +147,7 @@ __global__ __launch_bounds__(THREADS<LANES>) void norm_bwd_kernel(const NormArgs
         Raw<T, VEC> y[NV], z[NV], dn[NV];
         Raw<R, VEC> h[NV], dh[NV];
         load_rows<T, VEC, LANES, NV>(y, a.y, at, lane, vecs);
-        if (a.gate) load_rows<T, VEC, LANES, NV>(z, a.gate, row / a.heads * a.gate_stride + row % a.heads * a.D, lane, vecs);
+        if (a.gate) load_rows<T, VEC, LANES, NV>(z, a.gate, gate_row(a, row), lane, vecs);
         if (a.d_h) load_rows<R, VEC, LANES, NV>(dh, a.d_h, at, lane, vecs);
         if (a.before) {
             load_rows<R, VEC, LANES, NV>(h, a.h_in, at, lane, vecs);

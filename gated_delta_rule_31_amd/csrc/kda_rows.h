@@ -275,8 +275,8 @@ hipError_t launch_glr_step(GlrStepArgs a, bool fp32, bool wide, hipStream_t stre
 // ------------------------------------------------------------------ norms between blocks
 
 struct NormArgs {
-    const void *y, *gate;        // [rows, D]; gate: or null, gate_stride between tokens of `heads` rows
-    int64_t gate_stride;
+    const void *y, *gate;        // [rows, D]; gate: or null, with strides between tokens of `heads` rows and between those
+    int64_t gate_stride, gate_head;
     const void *residual;        // [rows, D] or null
     const float *wa, *wb;        // [D] or null (ones)
     int64_t rows;

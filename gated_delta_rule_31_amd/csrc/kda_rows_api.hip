@@ -404,14 +404,14 @@ kda_status kda_glr_step(const void *x, kda_dtype dtype, const void *gate, const 
     return done(kda::launch_glr_step(a, dtype == KDA_F32, w.ok, stream));
 }
 
-kda_status kda_block_norm_fwd(const void *y, const void *gate, int64_t gate_stride, kda_dtype dtype, const void *residual, kda_dtype h_dtype,
+kda_status kda_block_norm_fwd(const void *y, const void *gate, int64_t gate_stride, int64_t gate_head_stride, kda_dtype dtype, const void *residual, kda_dtype h_dtype,
                               const float *weight_after, const float *weight_before, int64_t tokens, int heads, int D, float scale,
                               float eps, unsigned flags, void *h, void *n, hipStream_t stream) {
     const kda_status st = norm_shape(dtype, h_dtype, tokens, heads, D, eps, flags);
     if (st != KDA_OK) return st;
     const bool before = (flags & KDA_NORM_BEFORE) != 0, after = (flags & KDA_NORM_AFTER) != 0;
     if ((weight_after && !after) || (weight_before && !before)) return KDA_ERR_BAD_ARGUMENT;
-    if (gate && gate_stride < (int64_t)heads * D) return KDA_ERR_BAD_SHAPE;
+    if (gate && (gate_stride < D || (heads > 1 && gate_head_stride < D))) return KDA_ERR_BAD_SHAPE;
     if (tokens == 0) return KDA_OK;
     if (!y || !h || (before && !n)) return KDA_ERR_NULL_POINTER;
     const void *ins[] = {y, gate, residual, weight_after, weight_before}, *outs[] = {h, before ? n : nullptr};
@@ -422,6 +422,7 @@ kda_status kda_block_norm_fwd(const void *y, const void *gate, int64_t gate_stri
     a.y = y;
     a.gate = gate;
     a.gate_stride = gate_stride;
+    a.gate_head = heads > 1 ? gate_head_stride : 0;
     a.residual = residual;
     a.wa = weight_after;
     a.wb = weight_before;
@@ -438,7 +439,7 @@ kda_status kda_block_norm_fwd(const void *y, const void *gate, int64_t gate_stri
     Wide w{e};
     w.ptr(y).ptr(gate).ptr(residual).ptr(h).stride(D);
     if (before) w.ptr(n);
-    if (gate) w.stride(gate_stride);
+    if (gate) w.stride(gate_stride).stride(a.gate_head);
     return done(kda::launch_norm_fwd(a, dtype == KDA_F32, h_dtype == KDA_F32, w.ok, stream));
 }
 
@@ -447,7 +448,7 @@ size_t kda_block_norm_bwd_workspace_size(int64_t tokens, int heads, int D) {
     return (size_t)kda::norm_groups(tokens * heads, D) * 2 * D * sizeof(float);
 }
 
-kda_status kda_block_norm_bwd(const void *y, const void *gate, int64_t gate_stride, kda_dtype dtype, const void *h, kda_dtype h_dtype,
+kda_status kda_block_norm_bwd(const void *y, const void *gate, int64_t gate_stride, int64_t gate_head_stride, kda_dtype dtype, const void *h, kda_dtype h_dtype,
                               const float *weight_after, const float *weight_before, int64_t tokens, int heads, int D, float scale,
                               float eps, unsigned flags, const void *d_h, const void *d_n, void *dy, void *d_gate, void *d_residual,
                               float *d_weight_after, float *d_weight_before, void *workspace, size_t workspace_bytes, hipStream_t stream) {
@@ -455,7 +456,7 @@ kda_status kda_block_norm_bwd(const void *y, const void *gate, int64_t gate_stri
     if (st != KDA_OK) return st;
     const bool before = (flags & KDA_NORM_BEFORE) != 0, after = (flags & KDA_NORM_AFTER) != 0;
     if ((!after && (weight_after || d_weight_after)) || (!before && (weight_before || d_weight_before))) return KDA_ERR_BAD_ARGUMENT;
-    if (gate && gate_stride < (int64_t)heads * D) return KDA_ERR_BAD_SHAPE;
+    if (gate && (gate_stride < D || (heads > 1 && gate_head_stride < D))) return KDA_ERR_BAD_SHAPE;
     if (tokens == 0) {
         st = fill(d_weight_after, nullptr, D, sizeof(float), stream);
         return st == KDA_OK ? fill(d_weight_before, nullptr, D, sizeof(float), stream) : st;
@@ -473,6 +474,7 @@ kda_status kda_block_norm_bwd(const void *y, const void *gate, int64_t gate_stri
     a.y = y;
     a.gate = gate;
     a.gate_stride = gate_stride;
+    a.gate_head = heads > 1 ? gate_head_stride : 0;
     a.wa = weight_after;
     a.wb = weight_before;
     a.rows = tokens * heads;
@@ -493,7 +495,7 @@ kda_status kda_block_norm_bwd(const void *y, const void *gate, int64_t gate_stri
     a.groups = kda::norm_groups(a.rows, D);
     Wide w{e};
     w.ptr(y).ptr(gate).ptr(d_h).ptr(dy).stride(D);
-    if (gate) w.ptr(d_gate).stride(gate_stride);
+    if (gate) w.ptr(d_gate).stride(gate_stride).stride(a.gate_head);
     if (before) w.ptr(h).ptr(d_n).ptr(d_residual);
     return done(kda::launch_norm_bwd(a, dtype == KDA_F32, h_dtype == KDA_F32, w.ok, d_weight_after, d_weight_before, stream));
 }

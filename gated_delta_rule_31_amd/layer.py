@@ -390,27 +390,27 @@ def _tokens_heads(shape):
 
 
 def _gate_rows(gate, y, tokens, heads):
-    """The gate and the distance between its tokens; one that is a slice of a wider tensor is not copied."""
+    """The gate, and the distances between its tokens and between a token's heads; one that is a slice of a wider
+    tensor, tokens at one distance, is not copied."""
     if gate is None:
-        return None, 0
+        return None, 0, 0
     if isinstance(gate, torch.Tensor) and gate.shape != y.shape:
         raise ValueError("gate must be shaped like y")
     D = y.shape[-1]
     if isinstance(gate, torch.Tensor) and gate.dim() >= 2 and gate.numel() and not gate.is_contiguous():
         lead, strides = (gate.shape[:-2], gate.stride()[:-2]) if gate.dim() > 2 else (gate.shape[:1], gate.stride()[:1])
-        dense = (D == 1 or gate.stride(-1) == 1) and (heads == 1 or gate.stride(-2) == D)
-        stride, n = None, 1
-        for size, s in zip(reversed(lead), reversed(strides)):  # the tokens' own dimensions at one distance
+        head = gate.stride(-2) if heads > 1 else D
+        dense, stride, n = (D == 1 or gate.stride(-1) == 1) and head >= D, None, 1
+        for size, s in zip(reversed(lead), reversed(strides)):
             if size > 1:
                 stride = s if stride is None else stride
                 dense = dense and s == stride * n
                 n *= size
         stride = heads * D if stride is None else stride
-        if dense and stride >= heads * D:
+        if dense and stride >= D:
             _input(gate[tuple(slice(0, 1) for _ in range(gate.dim()))], "gate", y, y.dtype, 1)
-            return gate, stride
-    gate = _input(gate, "gate", y, y.dtype, 1)
-    return gate, heads * D
+            return gate, stride, head
+    return _input(gate, "gate", y, y.dtype, 1), heads * D, D
 
 
 def _norm_inputs(y, gate, weight_after, weight_before, norm_after, norm_before, silu):
@@ -420,11 +420,11 @@ def _norm_inputs(y, gate, weight_after, weight_before, norm_after, norm_before, 
     if y.dim() < 2 or y.shape[-1] < 1 or 0 in y.shape[1:]:
         raise ValueError("y must be [tokens, D] or [..., heads, D]")
     tokens, heads = _tokens_heads(y.shape)
-    gate, gate_stride = _gate_rows(gate, y, tokens, heads)
+    gate, *gate_strides = _gate_rows(gate, y, tokens, heads)
     weight_after = _like(weight_after, "weight_after", y, torch.float32, y.shape[-1:])
     weight_before = _like(weight_before, "weight_before", y, torch.float32, y.shape[-1:])
     flags = (NORM_AFTER if norm_after else 0) | (NORM_BEFORE if norm_before else 0) | (SILU if silu else 0)
-    return y, gate, gate_stride, weight_after, weight_before, flags, (tokens, heads, y.shape[-1])
+    return y, gate, gate_strides, weight_after, weight_before, flags, (tokens, heads, y.shape[-1])
 
 
 def block_norm_fwd(y: torch.Tensor, gate: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
@@ -437,14 +437,14 @@ def block_norm_fwd(y: torch.Tensor, gate: Optional[torch.Tensor] = None, residua
     float32 or bfloat16 (the gate a slice of a wider tensor without a copy); residual like y or
     float32; weights [D] float32, None for ones.  Returns (h like the residual, or like y without
     one; n like y, or None).  ``out``: where h is written."""
-    y, gate, gate_stride, weight_after, weight_before, flags, (tokens, heads, D) = _norm_inputs(y, gate, weight_after, weight_before, norm_after,
+    y, gate, gate_strides, weight_after, weight_before, flags, (tokens, heads, D) = _norm_inputs(y, gate, weight_after, weight_before, norm_after,
                                                                                                norm_before, silu)
     residual = _input(residual, "residual", y, None, 1)
     if residual is not None and residual.shape != y.shape:
         raise ValueError("residual must be shaped like y")
     h = _made(out, "out", y.shape, y.dtype if residual is None else residual.dtype, y.device)
     n = torch.empty(y.shape, dtype=y.dtype, device=y.device) if norm_before else None
-    _call(_load().kda_block_norm_fwd, y.device, _p(y), _p(gate), gate_stride, _dtype_code(y.dtype), _p(residual), _dtype_code(h.dtype),
+    _call(_load().kda_block_norm_fwd, y.device, _p(y), _p(gate), *gate_strides, _dtype_code(y.dtype), _p(residual), _dtype_code(h.dtype),
           _p(weight_after), _p(weight_before), tokens, heads, D, float(scale), float(eps), flags, _p(h), _p(n))
     return h, n
 
@@ -461,7 +461,7 @@ def block_norm_bwd(y: torch.Tensor, d_h: Optional[torch.Tensor], d_n: Optional[t
     """Gradients of ``block_norm_fwd`` for L = <d_h, h> + <d_n, n>: (dy, d_gate, d_residual, d_weight_after,
     d_weight_before), None for what was not given.  h as the forward returned it, d_h like h (None:
     zeros) and d_n like y; without ``norm_before`` h and d_n are not used, and d_residual is d_h."""
-    y, gate, gate_stride, weight_after, weight_before, flags, (tokens, heads, D) = _norm_inputs(y, gate, weight_after, weight_before, norm_after,
+    y, gate, gate_strides, weight_after, weight_before, flags, (tokens, heads, D) = _norm_inputs(y, gate, weight_after, weight_before, norm_after,
                                                                                                norm_before, silu)
     dev = y.device
     d_h = _input(d_h, "d_h", y, None, 1)
@@ -479,7 +479,7 @@ def block_norm_bwd(y: torch.Tensor, d_h: Optional[torch.Tensor], d_n: Optional[t
     dz = dz.contiguous() if dz is not None else None
     d_res = torch.empty(y.shape, dtype=like.dtype, device=dev) if norm_before else d_h
     workspace = _workspace(workspace, block_norm_bwd_workspace_size(tokens, heads, D), dev)
-    _call(_load().kda_block_norm_bwd, dev, _p(y), _p(gate), gate_stride, _dtype_code(y.dtype), _p(h) if norm_before else None,
+    _call(_load().kda_block_norm_bwd, dev, _p(y), _p(gate), *gate_strides, _dtype_code(y.dtype), _p(h) if norm_before else None,
           _dtype_code(like.dtype), _p(weight_after), _p(weight_before), tokens, heads, D, float(scale), float(eps), flags, _p(d_h),
           _p(d_n) if norm_before else None, _p(dy), _p(dz), _p(d_res) if norm_before else None, _p(dwa), _p(dwb), _p(workspace), workspace.numel())
     return dy, dz, d_res, dwa, dwb

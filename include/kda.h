@@ -573,13 +573,14 @@ kda_status kda_glr_step(const void *x, kda_dtype dtype, const void *gate, const 
  *     h = residual + scale act(gate) p            act: sigmoid, or silu with KDA_SILU
  *     n = h / rms(h) weight_before (KDA_NORM_BEFORE; from h before it is rounded)
  *   y, n     [tokens, heads, D] in dtype;  residual (or NULL: 0), h [tokens, heads, D] in h_dtype: dtype or KDA_F32
- *   gate     [tokens, heads, D] in dtype, gate_stride between tokens, or NULL: 1
+ *   gate     [tokens, heads, D] in dtype, gate_stride between tokens and gate_head_stride between a token's heads (at least
+ *            D each, in any order), or NULL: 1
  *   weight_after, weight_before [D] float32 or NULL (ones)
  * Without residual and KDA_NORM_BEFORE, on a recurrence's heads, it is the layer's gated output norm.
  * A row's sum of squares must be finite.  1 <= D <= KDA_NORM_MAX_D.
  */
-kda_status kda_block_norm_fwd(const void *y, const void *gate, int64_t gate_stride, kda_dtype dtype, const void *residual, kda_dtype h_dtype,
-                              const float *weight_after, const float *weight_before, int64_t tokens, int heads, int D, float scale,
+kda_status kda_block_norm_fwd(const void *y, const void *gate, int64_t gate_stride, int64_t gate_head_stride, kda_dtype dtype,
+                              const void *residual, kda_dtype h_dtype, const float *weight_after, const float *weight_before, int64_t tokens, int heads, int D, float scale,
                               float eps, unsigned flags, void *h, void *n, hipStream_t stream);
 
 /*
@@ -590,8 +591,8 @@ kda_status kda_block_norm_fwd(const void *y, const void *gate, int64_t gate_stri
  * The workspace is needed for the weights' gradients, 16-byte aligned scratch.
  */
 size_t kda_block_norm_bwd_workspace_size(int64_t tokens, int heads, int D);
-kda_status kda_block_norm_bwd(const void *y, const void *gate, int64_t gate_stride, kda_dtype dtype, const void *h, kda_dtype h_dtype,
-                              const float *weight_after, const float *weight_before, int64_t tokens, int heads, int D, float scale,
+kda_status kda_block_norm_bwd(const void *y, const void *gate, int64_t gate_stride, int64_t gate_head_stride, kda_dtype dtype,
+                              const void *h, kda_dtype h_dtype, const float *weight_after, const float *weight_before, int64_t tokens, int heads, int D, float scale,
                               float eps, unsigned flags, const void *d_h, const void *d_n, void *dy, void *d_gate, void *d_residual,
                               float *d_weight_after, float *d_weight_before, void *workspace, size_t workspace_bytes, hipStream_t stream);
 

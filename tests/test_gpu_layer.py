@@ -539,3 +539,15 @@ def test_norm_recorded():
     got = torch.autograd.grad(g, [y, z, wa], dh)
     want = kda.block_norm_bwd(y.detach(), dh, gate=z.detach(), weight_after=wa.detach(), norm_before=False)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[3])
+
+
+@pytest.mark.parametrize("D", [16, 24, 33])
+def test_norm_gate_layouts(D):
+    """The gate as a slice of every head's row, and with heads outside of tokens, is the gate copied."""
+    r = gen(35)
+    y, d = r(7, 3, D).to(BF).cuda(), r(7, 3, D).to(BF).cuda()
+    for wide in (r(7, 3, 2 * D + 8).to(BF).cuda()[..., 8 : 8 + D], r(3, 7, D).to(BF).cuda().transpose(0, 1)):
+        assert not wide.is_contiguous()
+        assert torch.equal(kda.block_norm_fwd(y, gate=wide, norm_before=False)[0], kda.block_norm_fwd(y, gate=wide.contiguous(), norm_before=False)[0])
+        for u, v in zip(kda.block_norm_bwd(y, d, gate=wide, norm_before=False)[:2], kda.block_norm_bwd(y, d, gate=wide.contiguous(), norm_before=False)[:2]):
+            assert torch.equal(u, v)

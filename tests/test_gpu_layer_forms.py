@@ -1,0 +1,265 @@
+"""What stands around the recurrence in a layer, in the forms in which it is trained and served: a whole
+block against its 64-bit form, decoding with drafts through one table of slots, captured and
+replayed calls, several streams, rows and pools past 32-bit offsets."""
+import pytest
+import torch
+
+import gated_delta_rule_31_amd as kda
+from tests import layer_reference as ref
+from tests.layer_reference import f64
+from tests.test_gpu_layer import close, conv_case, gen, gpu, norm_case, offsets, scan_case
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+# --------------------------------------------------------------------------- together
+
+def _block(op, y, x, w1, w2, conv_w, conv_b, log_scale, bias, norm_a, norm_b, heads, width):
+    """norm between blocks -> projection -> convolution -> recurrence -> gated head norm -> projection -> norm between blocks"""
+    h, n = op.block_norm(y, residual=x, weight_after=norm_a, weight_before=norm_b, scale=0.5)
+    u = n @ w1  # recurrence's input, its gate's logits, its input gate and the output gate side by side
+    C = heads * width
+    v, _ = op.short_conv(u[..., :C], conv_w, conv_b)
+    part = lambda k: u[..., k * C : (k + 1) * C].unflatten(-1, (heads, width))  # noqa: E731
+    r, final = op.scan(v.unflatten(-1, (heads, width)), part(1), log_scale, bias, part(2))
+    o = op.gated_norm(r, part(3))
+    h, n = op.block_norm(o.flatten(-2) @ w2, residual=h, weight_after=norm_b, weight_before=norm_a, scale=0.5, gate=n)
+    return h, n, final
+
+
+class _Ours:
+    def __init__(self, lens):
+        self.cu = gpu(offsets(lens))
+
+    def block_norm(self, y, **kw):
+        return kda.block_norm(y, silu=True, **kw)
+
+    def gated_norm(self, y, gate):
+        return kda.gated_norm(y, gate)
+
+    def short_conv(self, x, w, b):
+        return kda.short_conv(x, w, b, cu_seqlens=self.cu)
+
+    def scan(self, x, z, a, b, i):
+        return kda.gated_linear_recurrence(x, z, a, b, i, cu_seqlens=self.cu)
+
+
+class _Plain:
+    def __init__(self, lens):
+        self.lens = lens
+
+    def block_norm(self, y, residual, weight_after, weight_before, scale, gate=None):
+        return ref.block_norm(y, gate, residual, weight_after, weight_before, True, True, scale, 1e-6, True)
+
+    def gated_norm(self, y, gate):
+        return ref.block_norm(y, gate, None, None, None, True, False, 1.0, 1e-6, False)[0]
+
+    def short_conv(self, x, w, b):
+        return ref.conv(x, w, b, None, self.lens, True)
+
+    def scan(self, x, z, a, b, i):
+        return ref.scan(x, z, a, b, i, None, self.lens, True)
+
+
+@pytest.mark.parametrize("lens", [[70, 0, 33, 1], [200]])
+def test_recurrent_block_trains(lens):
+    """A block's outputs and all its gradients.  Each of its seven stages is off by at most 6 x 1024 roundings of 2^-24 in an
+    element, 3.7e-4 of the rms, and as these are independent by a tenth of that in the 2-norm: 7 x 3.7e-5 = 2.6e-4."""
+    D, H, K, T = 48, 2, 24, sum(lens)
+    r = gen(40)
+    C = H * K
+    data = [r(1, T, D), 2 * r(1, T, D), r(D, 4 * C) * D ** -0.5, r(C, D) * C ** -0.5, r(C, 4) * 0.5, 0.2 * r(C), 0.2 * r(H), r(H, K) - 1, 1 + 0.2 * r(D), 1 + 0.2 * r(D)]
+    gh, gn, gf = r(1, T, D), r(1, T, D), r(len(lens), H, K)
+    mine, plain = [gpu(t).requires_grad_() for t in data], [f64(t).requires_grad_() for t in data]
+    got, want = _block(_Ours(lens), *mine, H, K), _block(_Plain(lens), *plain, H, K)
+    for u, v, name in zip(got, want, ("h", "n", "final")):
+        assert float((f64(u) - v.detach()).norm() / v.detach().norm()) <= 2.6e-4, name
+    grads = torch.autograd.grad(sum((u * gpu(g)).sum() for u, g in zip(got, (gh, gn, gf))), mine)
+    refs = torch.autograd.grad(sum((u * f64(g)).sum() for u, g in zip(want, (gh, gn, gf))), plain)
+    for k, (u, v) in enumerate(zip(grads, refs)):
+        assert float((f64(u) - v).norm() / v.norm()) <= 2.6e-4, k
+
+
+def test_layer_decodes_with_drafts():
+    """Convolution, gated delta rule and linear recurrence go by one table of slots through rounds of drafts, and give what
+    their prefills give.  Float32: 512 roundings (test_gpu_layer) for the linear parts, 1e-4 for the delta rule's."""
+    B, T, S, H, K = 4, 17, 3, 2, 16
+    r = gen(41)
+    C = H * K
+    x, w, g, beta, z = r(B, T, C), r(C, 4) / 2, -0.5 * r(B, T, H).abs(), torch.sigmoid(r(B, T, H)), r(B, T, H, K)
+    ls, b = 0.1 * r(H), r(H, K)
+    x, w, g, beta, z, ls, b = map(gpu, (x, w, g, beta, z, ls, b))
+    unit = lambda t: t / t.norm(dim=-1, keepdim=True)  # noqa: E731
+    conv = kda.short_conv_fwd(x, w)[0].unflatten(-1, (H, K))
+    q = unit(conv)
+    want = kda.gdr_chunk_fwd(q, q, conv, g, beta)[0], kda.glr_fwd(conv, z, ls, b)[0]
+    pool = B * S
+    slots = torch.randperm(pool, generator=torch.Generator().manual_seed(3)).reshape(B, S).int().cuda()
+    rows, deltas, states = (torch.zeros(pool, *s, device="cuda") for s in ((3, C), (H, K, K), (H, K)))
+    at, start = [0] * B, torch.zeros(B, dtype=torch.int32, device="cuda")
+    while min(at) < T:
+        n = [min(S, T - t) for t in at]
+        cut = lambda t: torch.stack([torch.cat([t[i, a : a + k], t.new_zeros(S - k, *t.shape[2:])]) for i, (a, k) in enumerate(zip(at, n))])  # noqa: E731
+        kw = dict(slots=slots, start=start, lengths=torch.tensor(n, dtype=torch.int32, device="cuda"))
+        c = kda.short_conv_step(cut(x), w, rows, **kw).unflatten(-1, (H, K))
+        u = unit(c.where(c != 0, torch.full_like(c, 1e-20)))
+        outs = kda.gdr_recurrent_step(u, u, c, cut(g), cut(beta), deltas, **kw), kda.glr_step(c, cut(z), states, ls, b, **kw)
+        for i in range(B):
+            if n[i]:
+                close(outs[0][i, : n[i]], want[0][i, at[i] : at[i] + n[i]], 1700)
+                close(outs[1][i, : n[i]], want[1][i, at[i] : at[i] + n[i]], 512)
+                took = min(n[i], 1 + (at[i] + i) % S)
+                start[i] = took - 1
+                at[i] += took
+
+
+# --------------------------------------------------------------------------- captured calls, streams
+
+def _calls():
+    """name -> (inputs, call of them that gives a list of tensors)"""
+    lens = [70, 0, 130, 1]
+    cu = gpu(offsets(lens))
+    x, w, b, s = map(gpu, conv_case(lens, True, 40, 4, BF, True, True, 50))
+    d = gpu(gen(51)(*x.shape).to(BF))
+    X, z, ls, bi, i, s0 = map(gpu, scan_case(lens, True, 3, 24, BF, True, True, True, 52))
+    D = gpu(gen(53)(*X.shape).to(BF))
+    y, g, res, wa, wb = map(gpu, norm_case((50, 2, 136), BF, F32, True, True, True, 54))
+    dh, dn = gpu(gen(55)(*y.shape)), gpu(gen(56)(*y.shape).to(BF))
+    flat = lambda t: [u for u in t if u is not None]  # noqa: E731
+
+    def scan(X, z, i, s0, D):
+        out, fin, kept = kda.glr_fwd(X, z, ls, bi, i, initial_state=s0, cu_seqlens=cu, keep=True)
+        return flat([out[:, : sum(lens)], fin] + list(kda.glr_bwd(X, z, D, ls, bi, i, initial_state=s0, cu_seqlens=cu, kept=kept)))
+
+    def steps(x, X, z, i):
+        rows, states = torch.zeros(70, 3, 40, dtype=BF, device="cuda"), torch.zeros(70, 3, 24, device="cuda")
+        return [kda.short_conv_step(x[:, :70].transpose(0, 1).contiguous(), w, rows, b), rows, kda.glr_step(*(t[:, :70].transpose(0, 1).contiguous() for t in (X, z)), states,
+                                                                                                       ls, bi, i[:, :70].transpose(0, 1).contiguous()), states]
+    return {"conv": ([x, s, d], lambda x, s, d: flat(kda.short_conv_fwd(x, w, b, s, cu_seqlens=cu) + kda.short_conv_bwd(x, w, d, b, s, cu_seqlens=cu))),
+            "scan": ([X, z, i, s0, D], scan), "steps": ([x, X, z, i], steps),
+            "norm": ([y, g, res, dh, dn], lambda y, g, res, dh, dn: flat(kda.block_norm_fwd(y, g, res, wa, wb) + kda.block_norm_bwd(y, dh, dn, res, g, wa, wb)))}
+
+
+@pytest.mark.parametrize("name", ["conv", "scan", "steps", "norm"])
+def test_captured(name):
+    """A captured call, replayed with other inputs between the program's own work, gives the eager call's bits every time."""
+    inputs, call = _calls()[name]
+    static = [t.clone() for t in inputs]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(*static)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = call(*static)
+    for k in range(4):
+        new = [t * (1 + 0.25 * k) if t.is_floating_point() else t for t in inputs]
+        for a, b in zip(static, new):
+            a.copy_(b)
+        want = call(*new)
+        graph.replay()
+        torch.cuda.synchronize()
+        for u, v in zip(outs, want):
+            assert torch.equal(u, v), k
+
+
+def test_two_graphs_share_a_workspace():
+    """Captured calls that share a caller's workspace, replayed one after the other, give the eager calls' bits."""
+    lens, H, K = [300], 2, 16
+    x, z, ls, b, i, s = map(gpu, scan_case(lens, False, H, K, F32, True, True, False, 57))
+    x2 = x.flip(1).contiguous()
+    d = gpu(gen(58)(*x.shape))
+    ws = torch.empty(max(kda.glr_fwd_workspace_size(1, 300, H, K), kda.glr_bwd_workspace_size(1, 300, H, K, True, False)), dtype=torch.uint8, device="cuda")
+    calls = [lambda: kda.glr_fwd(x, z, ls, b, i, workspace=ws), lambda: kda.glr_bwd(x2, z, d, ls, b, i, workspace=ws)]
+    want = [[t.clone() for t in c() if t is not None] for c in calls]
+    graphs, outs = [], []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append([t for t in c() if t is not None])
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+        ws.fill_(255)  # the program's own use of it
+        torch.cuda.synchronize()
+        for got, ref_ in zip(outs, want):
+            for u, v in zip(got, ref_):
+                assert torch.equal(u, v)
+
+
+def test_streams():
+    """All calls at once on streams of their own, several times over, give what each gives alone."""
+    calls = _calls()
+    want = {n: call(*inputs) for n, (inputs, call) in calls.items()}
+    torch.cuda.synchronize()
+    streams = {n: torch.cuda.Stream() for n in calls}
+    got = {n: [] for n in calls}
+    for _ in range(3):
+        for n, (inputs, call) in calls.items():
+            with torch.cuda.stream(streams[n]):
+                got[n].append(call(*inputs))
+    torch.cuda.synchronize()
+    for n in calls:
+        for outs in got[n]:
+            for u, v in zip(outs, want[n]):
+                assert torch.equal(u, v), n
+
+
+# --------------------------------------------------------------------------- past 32-bit offsets
+
+def _far(rows, width, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(1, rows, width, generator=g, device="cuda", dtype=dtype)
+
+
+def test_conv_past_32_bit_offsets():
+    """The last rows of 2.4 x 10^9 numbers, and a pool of 2.3 x 10^9, are those of a small call."""
+    T, D = 300_000, 8192
+    x, w = _far(T, D, BF, 60), gpu(gen(61)(D, 4) / 2)
+    tail = x[:, -100:].contiguous()
+    out, fin = kda.short_conv_fwd(x, w)
+    want, want_fin = kda.short_conv_fwd(tail, w, initial_state=x[:, -103:-100].contiguous())
+    assert torch.equal(out[:, -100:], want) and torch.equal(fin, want_fin)
+    dx, _, _, _ = kda.short_conv_bwd(x, w, out)
+    ref_ = kda.short_conv_bwd(tail, w, want, initial_state=x[:, -103:-100].contiguous())[0]
+    assert torch.equal(dx[:, -100:], ref_)
+    del out, dx
+    pool = torch.zeros(95_000, 3, D, dtype=BF, device="cuda")
+    slots = torch.tensor([[94_999], [0], [90_000]], dtype=torch.int32, device="cuda")
+    small = torch.zeros(3, 3, D, dtype=BF, device="cuda")
+    for t in range(2):
+        a = kda.short_conv_step(tail[:, 3 * t : 3 * t + 3].transpose(0, 1).contiguous(), w, pool, slots=slots)
+        assert torch.equal(a, kda.short_conv_step(tail[:, 3 * t : 3 * t + 3].transpose(0, 1).contiguous(), w, small))
+    assert torch.equal(pool[slots[:, 0].long()], small)
+
+
+def test_scan_past_32_bit_offsets():
+    T, H, K = 300_000, 64, 128
+    x = _far(T, H * K, BF, 62).unflatten(-1, (H, K))
+    ls = torch.zeros(H, device="cuda")
+    out, fin, kept = kda.glr_fwd(x, x, ls, keep=True)
+    cut = T - 104  # where a state is kept
+    state = kept.view(-1, H, K)[cut // 8].unsqueeze(0)
+    tail = x[:, cut:].contiguous()
+    want, want_fin = kda.glr_fwd(tail, tail, ls, initial_state=state)
+    close(out[:, cut:], want, 512)
+    close(fin, want_fin, 512)
+    grads = kda.glr_bwd(x, x, out, ls, kept=kept)
+    refs = kda.glr_bwd(tail, tail, out[:, cut:].contiguous(), ls, initial_state=state)
+    for k in (0, 1):
+        close(grads[k][:, cut:], refs[k], 6 * 1024)
+
+
+def test_norm_past_32_bit_offsets():
+    T, D = 300_000, 8192
+    y = _far(T, D, BF, 63)
+    h, n = kda.block_norm_fwd(y, gate=y, residual=y)
+    want = kda.block_norm_fwd(y[:, -50:].contiguous(), gate=y[:, -50:].contiguous(), residual=y[:, -50:].contiguous())
+    assert torch.equal(h[:, -50:], want[0]) and torch.equal(n[:, -50:], want[1])
+    got = kda.block_norm_bwd(y, y, d_n=n, h=h, gate=y)
+    ref_ = kda.block_norm_bwd(y[:, -50:].contiguous(), y[:, -50:].contiguous(), d_n=want[1], h=want[0], gate=y[:, -50:].contiguous())
+    for k in range(3):
+        assert torch.equal(got[k][:, -50:], ref_[k])

@@ -93,21 +93,21 @@ def test_glr_bwd_refusals(lib, kw, status):
     assert _glr_bwd(lib, **kw) == status
 
 
-def _norm(lib, y=0x1000, g=0x2000, gs=32, dt=1, r=0x3000, ht=1, wa=0x4000, wb=0x5000, n=64, heads=2, D=16, eps=1e-6, fl=3, h=0x6000, o=0x7000):
-    return lib.kda_block_norm_fwd(y, g, gs, dt, r, ht, wa, wb, n, heads, D, 1.0, eps, fl, h, o, None)
+def _norm(lib, y=0x1000, g=0x2000, gs=32, gh=16, dt=1, r=0x3000, ht=1, wa=0x4000, wb=0x5000, n=64, heads=2, D=16, eps=1e-6, fl=3, h=0x6000, o=0x7000):
+    return lib.kda_block_norm_fwd(y, g, gs, gh, dt, r, ht, wa, wb, n, heads, D, 1.0, eps, fl, h, o, None)
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(n=-1), 2), (dict(heads=0), 2), (dict(D=0), 2), (dict(dt=2), 3), (dict(ht=2), 3), (dict(dt=0, ht=1), 3), (dict(fl=4), 5), (dict(eps=-1.0), 5), (dict(eps=float("nan")), 5),
-    (dict(D=16385, gs=1 << 20), 4), (dict(n=1 << 31), 4), (dict(fl=1), 5), (dict(fl=2), 5), (dict(gs=31), 2), (dict(y=None), 1), (dict(h=None), 1), (dict(o=None), 1), (dict(h=0x3000), 6),
+    (dict(D=16385, gs=1 << 20), 4), (dict(n=1 << 31), 4), (dict(fl=1), 5), (dict(fl=2), 5), (dict(gs=15), 2), (dict(gh=15), 2), (dict(y=None), 1), (dict(h=None), 1), (dict(o=None), 1), (dict(h=0x3000), 6),
     (dict(o=0x6000), 6), (dict(o=0x1000), 6), (dict(y=0x1001), 5), (dict(ht=0, r=0x3002), 5), (dict(n=0, y=None, h=None), 0)])
 def test_norm_refusals(lib, kw, status):
     assert _norm(lib, **kw) == status
 
 
-def _norm_bwd(lib, y=0x1000, g=0x2000, gs=32, dt=1, h=0x3000, ht=1, wa=0x4000, wb=0x5000, n=64, heads=2, D=16, eps=1e-6, fl=3, dh=0x6000, dn=0x7000, dy=0x8000, dg=0x9000, dr=0xa000,
+def _norm_bwd(lib, y=0x1000, g=0x2000, gs=32, gh=16, dt=1, h=0x3000, ht=1, wa=0x4000, wb=0x5000, n=64, heads=2, D=16, eps=1e-6, fl=3, dh=0x6000, dn=0x7000, dy=0x8000, dg=0x9000, dr=0xa000,
               dwa=0xb000, dwb=0xc000, ws=0xd000, wsz=1 << 20):
-    return lib.kda_block_norm_bwd(y, g, gs, dt, h, ht, wa, wb, n, heads, D, 1.0, eps, fl, dh, dn, dy, dg, dr, dwa, dwb, ws, wsz, None)
+    return lib.kda_block_norm_bwd(y, g, gs, gh, dt, h, ht, wa, wb, n, heads, D, 1.0, eps, fl, dh, dn, dy, dg, dr, dwa, dwb, ws, wsz, None)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -167,18 +167,19 @@ def test_rows_of_a_wider_tensor(make, stride, monkeypatch):
     assert torch.equal(flat, x.reshape(-1, width))
 
 
-@pytest.mark.parametrize("make,stride", [
-    (lambda b: b[..., 8:24].unflatten(-1, (2, 8)), 40), (lambda b: b[..., ::2].unflatten(-1, (4, 5)), None), (lambda b: b[:, :3, :16].unflatten(-1, (2, 8)), None),
-    (lambda b: b[..., :20].unflatten(-1, (2, 10))[..., :8], None), (lambda b: b[1:2, :, 1:17].unflatten(-1, (1, 16)), 40), (lambda b: b[:, 0, 4:12], 200)])
-def test_gate_of_a_wider_tensor(make, stride, monkeypatch):
+@pytest.mark.parametrize("make,stride,head", [
+    (lambda b: b[..., 8:24].unflatten(-1, (2, 8)), 40, 8), (lambda b: b[..., ::2].unflatten(-1, (4, 5)), None, None), (lambda b: b[:, :3, :16].unflatten(-1, (2, 8)), None, None),
+    (lambda b: b[..., :20].unflatten(-1, (2, 10))[..., :8], 40, 10), (lambda b: b[1:2, :, 1:17].unflatten(-1, (1, 16)), 40, 16), (lambda b: b[:, 0, 4:12], 200, 8),
+    (lambda b: b[..., 4:12], 200, 40), (lambda b: b[0].unflatten(-1, (8, 5)).transpose(0, 1), 5, 40), (lambda b: b[:, :, :1].expand(3, 5, 8), None, None)])
+def test_gate_of_a_wider_tensor(make, stride, head, monkeypatch):
     import gated_delta_rule_31_amd.layer as layer
     monkeypatch.setattr(layer, "_input", lambda x, *a: x.contiguous())
     g = make(torch.arange(600.0).reshape(3, 5, 40))
     tokens, heads = layer._tokens_heads(g.shape)
-    got, n = _gate_rows(g, g, tokens, heads)
-    width = heads * g.shape[-1]
-    assert n == (stride or width) and (got.data_ptr() == g.data_ptr()) == (stride is not None)
-    assert torch.equal(torch.as_strided(got, (tokens, width), (n, 1), got.storage_offset()), g.reshape(tokens, width))
+    got, n, h = _gate_rows(g, g, tokens, heads)
+    D = g.shape[-1]
+    assert (n, h) == ((stride, head) if stride else (heads * D, D)) and (got.data_ptr() == g.data_ptr()) == (stride is not None)
+    assert torch.equal(torch.as_strided(got, (tokens, heads, D), (n, h, 1), got.storage_offset()), g.reshape(tokens, heads, D))
 
 
 def test_reference_gradients():
