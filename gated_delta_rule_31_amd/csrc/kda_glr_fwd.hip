@@ -103,34 +103,63 @@ __global__ __launch_bounds__(64 * WAVES) void glr_fwd_kernel(const GlrArgs a, in
     if constexpr (!OUT) glr_word<VEC>(a, p.tile, p.c, A, h);
 }
 
-// The state in front of every tile: 64 groups of tiles for 16 channels, each group's A and H first, then its tiles from the
-// state that the groups before it leave.
-constexpr int CARRY_C = 16, CARRY_G = 64;
-__global__ __launch_bounds__(CARRY_C * CARRY_G) void glr_carry_kernel(const float *words, float *front, int n, int C, int reverse) {
-    __shared__ float sA[CARRY_G][CARRY_C], sH[CARRY_G][CARRY_C];
-    const int lane = threadIdx.x % CARRY_C, group = threadIdx.x / CARRY_C, c = blockIdx.x * CARRY_C + lane;
-    const int each = (n + CARRY_G - 1) / CARRY_G, lo = group * each, hi = lo + each < n ? lo + each : n;
-    float A = 1.f, H = 0.f;
-    if (c < C) {
-#pragma unroll 4
-        for (int j = lo; j < hi; ++j) {
-            const float *w = words + ((int64_t)(reverse ? n - 1 - j : j) * C + c) * 2;
-            H = join(w[0], w[1], H);
-            A *= w[0];
+// The state in front of every tile: a workgroup takes a few channels, and its groups of lanes a stretch of tiles each: the
+// stretch's A and H, joined over the groups of a wave by shuffles and over the waves through LDS, then its tiles from
+// the state in front of it.  What it takes is the words' way, so 16 of them are on it at a time (four at a time:
+// 22 us for 4096 tiles of 256 channels).  16 channels a workgroup read whole cache lines; where that leaves few
+// workgroups, four.
+constexpr int CARRY_T = 1024, CARRY_U = 16;
+template <int CARRY_C>
+__global__ __launch_bounds__(CARRY_T) void glr_carry_kernel(const float *words, float *front, int n, int C, int reverse) {
+    __shared__ float sA[CARRY_T / 64][CARRY_C], sH[CARRY_T / 64][CARRY_C];
+    const int ch = threadIdx.x % CARRY_C, group = threadIdx.x / CARRY_C, c = blockIdx.x * CARRY_C + ch, lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int groups = CARRY_T / CARRY_C, each = (n + groups - 1) / groups, lo = group * each, end = lo + each < n ? lo + each : n, hi = c < C ? end : lo;
+    float A = 1.f, H = 0.f, a[CARRY_U], h[CARRY_U];
+    auto words_from = [&](int at) {
+#pragma unroll
+        for (int u = 0; u < CARRY_U; ++u) {
+            a[u] = 1.f;
+            h[u] = 0.f;
+            if (at + u < hi) {
+                const float *w = words + ((int64_t)(reverse ? n - 1 - at - u : at + u) * C + c) * 2;
+                a[u] = w[0];
+                h[u] = w[1];
+            }
+        }
+    };
+    for (int at = lo; at < hi; at += CARRY_U) {
+        words_from(at);
+#pragma unroll
+        for (int u = 0; u < CARRY_U; ++u) {
+            H = join(a[u], h[u], H);
+            A *= a[u];
         }
     }
-    sA[group][lane] = A;
-    sH[group][lane] = H;
+#pragma unroll
+    for (int d = CARRY_C; d < 64; d *= 2) {
+        const float pa = __shfl_up(A, d), ph = __shfl_up(H, d);
+        if (lane >= d) {
+            H = join(A, H, ph);
+            A *= pa;
+        }
+    }
+    if (lane >= 64 - CARRY_C) {
+        sA[wave][ch] = A;
+        sH[wave][ch] = H;
+    }
+    float ea = __shfl_up(A, CARRY_C), eh = __shfl_up(H, CARRY_C);
     __syncthreads();
-    if (c >= C || lo >= hi) return;
-    float h = 0.f;
-#pragma unroll 8
-    for (int g = 0; g < group; ++g) h = join(sA[g][lane], sH[g][lane], h);
-#pragma unroll 4
-    for (int j = lo; j < hi; ++j) {
-        const int64_t t = reverse ? n - 1 - j : j;
-        front[t * C + c] = h;
-        h = join(words[(t * C + c) * 2], words[(t * C + c) * 2 + 1], h);
+    float x = 0.f;
+    for (int w = 0; w < wave; ++w) x = join(sA[w][ch], sH[w][ch], x);
+    if (lane >= CARRY_C) x = join(ea, eh, x);
+    for (int at = lo; at < hi; at += CARRY_U) {
+        if (each > CARRY_U) words_from(at);  // otherwise they are still there
+#pragma unroll
+        for (int u = 0; u < CARRY_U; ++u)
+            if (at + u < hi) {
+                front[(int64_t)(reverse ? n - 1 - at - u : at + u) * C + c] = x;
+                x = join(a[u], h[u], x);
+            }
     }
 }
 
@@ -202,16 +231,17 @@ hipError_t step_by_gate(const GlrStepArgs &a, hipStream_t stream) {
 
 hipError_t launch_glr_carry(const GlrArgs &a, bool reverse, hipStream_t stream) {
     if (!a.tiles.front) return hipSuccess;
-    hipLaunchKernelGGL(glr_carry_kernel, dim3((unsigned)((a.C + CARRY_C - 1) / CARRY_C)), dim3(CARRY_C * CARRY_G), 0, stream, a.tiles.words, a.tiles.front,
-                       a.tiles.n, a.C, reverse ? 1 : 0);
+    if (a.C <= 1024) hipLaunchKernelGGL(glr_carry_kernel<4>, dim3((unsigned)((a.C + 3) / 4)), dim3(CARRY_T), 0, stream, a.tiles.words, a.tiles.front, a.tiles.n, a.C, reverse ? 1 : 0);
+    else hipLaunchKernelGGL(glr_carry_kernel<16>, dim3((unsigned)((a.C + 15) / 16)), dim3(CARRY_T), 0, stream, a.tiles.words, a.tiles.front, a.tiles.n, a.C, reverse ? 1 : 0);
     return hipGetLastError();
 }
 
-// Tiles of 64 rows, or shorter ones where those leave compute units idle.
+// Tiles of 64 rows, or shorter ones where those are too few waves to cover their loads: 7957 x 4096 in 109 us with 32 rows
+// (8000 waves), 117 with 64, 125 with 16.
 void glr_plan(GlrArgs &a) {
     const int64_t columns = (a.C + 127) / 128;
     a.tiles.rows = 64;
-    while (a.tiles.rows > 16 && (a.seqs.rows + a.tiles.rows - 1) / a.tiles.rows * columns < 2048) a.tiles.rows /= 2;
+    while (a.tiles.rows > 16 && (a.seqs.rows + a.tiles.rows - 1) / a.tiles.rows * columns < 6000) a.tiles.rows /= 2;
     a.tiles.n = (int)((a.seqs.rows + a.tiles.rows - 1) / a.tiles.rows);
 }
 
