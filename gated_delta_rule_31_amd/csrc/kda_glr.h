@@ -73,11 +73,11 @@ using gate_t = std::conditional_t<LOGITS, T, float>;
 //   1. A and H of every tile (with one tile: not needed)
 //   2. the state in front of every tile (with few tiles their readers join the words themselves)
 //   3. the rows themselves, from the state in front of their tile
-// so the rows are read twice, the second time partly from the last-level cache.  One pass in which a tile
-// waits for what the tiles in front publish was measured: 8192 x 4096 in 97-102 us, of which 63 are
-// the rows' own and the rest the waiting.  These launches wait for nothing.
+// so the rows are read twice, the second time partly from the last-level cache.  Reading them once was measured for 7957
+// x 4096: tiles that wait for what the tiles in front publish, 97-102 us (63 without the waiting) against 108 for these
+// launches, which wait for nothing; and workgroups that take 16 channels through all rows, 109 us at best.
 
-constexpr int GLR_FEW = 16;  // tiles that readers join themselves
+constexpr int GLR_FEW = 16;  // tiles that readers join themselves: a launch less where launches are what a call takes
 constexpr int U = 8;         // rows that a wave has on their way
 
 // A wave's tile: its column of channels, rows and marks.

@@ -91,7 +91,6 @@ struct Raw {
     // `off` bytes behind a row that all lanes share
     __device__ __forceinline__ void load(const char *row, uint32_t off) { v = *reinterpret_cast<const vec *>(row + off); }
     __device__ __forceinline__ void store(char *row, uint32_t off) const { *reinterpret_cast<vec *>(row + off) = v; }
-    __device__ __forceinline__ void stream(T *p) const { __builtin_nontemporal_store(v, reinterpret_cast<vec *>(p)); }
     __device__ __forceinline__ float get(int i) const { return to_f32(v[i]); }
     __device__ __forceinline__ void set(int i, float x) { v[i] = from_f32<T>(x); }
     __device__ __forceinline__ void zero() { v = vec{}; }
@@ -103,7 +102,6 @@ struct Raw<T, 1> {
     __device__ __forceinline__ void store(T *p) const { *p = v; }
     __device__ __forceinline__ void load(const char *row, uint32_t off) { v = *reinterpret_cast<const T *>(row + off); }
     __device__ __forceinline__ void store(char *row, uint32_t off) const { *reinterpret_cast<T *>(row + off) = v; }
-    __device__ __forceinline__ void stream(T *p) const { *p = v; }
     __device__ __forceinline__ float get(int) const { return to_f32(v); }
     __device__ __forceinline__ void set(int, float x) { v = from_f32<T>(x); }
     __device__ __forceinline__ void zero() { v = T{}; }

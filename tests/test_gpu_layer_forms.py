@@ -263,3 +263,48 @@ def test_norm_past_32_bit_offsets():
     ref_ = kda.block_norm_bwd(y[:, -50:].contiguous(), y[:, -50:].contiguous(), d_n=want[1], h=want[0], gate=y[:, -50:].contiguous())
     for k in range(3):
         assert torch.equal(got[k][:, -50:], ref_[k])
+
+
+# --------------------------------------------------------------------------- nothing to do
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("cu", [None, [0], [0, 0, 0]])
+def test_no_rows(dtype, cu):
+    """Batches without a row: states are handed on, their gradients handed back, sums are zeros."""
+    B, N = (1, len(cu) - 1) if cu else (2, 2)
+    off = torch.tensor(cu, dtype=torch.int32, device="cuda") if cu else None
+    r = gen(70)
+    x, w, b, s = torch.zeros(B, 0, 20, dtype=dtype, device="cuda"), gpu(r(20, 3)), gpu(r(20)), gpu(r(N, 2, 20).to(dtype))
+    out, fin = kda.short_conv_fwd(x, w, b, s, cu_seqlens=off)
+    assert out.shape == x.shape and torch.equal(fin, s) and not kda.short_conv_fwd(x, w, b, cu_seqlens=off)[1].any()
+    dx, dw, db, ds = kda.short_conv_bwd(x, w, x, b, s, d_final_state=s, cu_seqlens=off)
+    assert dx.shape == x.shape and not dw.any() and not db.any() and torch.equal(ds, s)
+    X, ls, bi, s0 = x.unflatten(2, (2, 10)), gpu(r(2)), gpu(r(2, 10)), gpu(r(N, 2, 10))
+    out, fin, kept = kda.glr_fwd(X, X, ls, bi, X, initial_state=s0, cu_seqlens=off, keep=True)
+    assert out.shape == X.shape and torch.equal(fin, s0) and not kept.numel()
+    dx, dg, di, da, db, ds = kda.glr_bwd(X, X, X, ls, bi, X, initial_state=s0, d_final_state=s0, cu_seqlens=off, kept=kept)
+    assert not da.any() and not db.any() and torch.equal(ds, s0) and di.shape == X.shape
+    y, wa = torch.zeros(0, 3, 16, dtype=dtype, device="cuda"), torch.ones(16, device="cuda")
+    h, n = kda.block_norm_fwd(y, y, y, wa, wa)
+    assert h.shape == y.shape and n.shape == y.shape
+    got = kda.block_norm_bwd(y, y, y, y, y, wa, wa)
+    assert not got[3].any() and not got[4].any()
+    assert kda.short_conv_step(x, w, s).shape == x.shape if B <= N else True
+
+
+def test_offsets_out_of_order():
+    """Offsets that are out of range or order move boundaries, but every call returns, and what is in order still holds."""
+    lens = [50, 30, 20]
+    x, w, b, s = map(gpu, conv_case(lens, True, 16, 4, F32, True, True, 71))
+    X, z, ls, bi, i, s0 = map(gpu, scan_case(lens, True, 2, 8, F32, True, True, True, 72))
+    for bad in ([0, 50, 80, 130], [0, 50, 80, -5], [0, 70, 40, 100], [5, 50, 80, 100], [-9, 50, 1 << 30, 100], [100, 80, 50, 0]):
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        out, _ = kda.short_conv_fwd(x, w, b, s, cu_seqlens=cu)
+        kda.short_conv_bwd(x, w, x, b, s, d_final_state=s, cu_seqlens=cu)
+        o, _, kept = kda.glr_fwd(X, z, ls, bi, i, initial_state=s0, cu_seqlens=cu, keep=True)
+        kda.glr_bwd(X, z, X, ls, bi, i, initial_state=s0, d_final_state=s0, cu_seqlens=cu, kept=kept)
+        torch.cuda.synchronize()
+        if bad[:2] == [0, 50] and bad[3] >= 50:
+            good = gpu(offsets(lens))
+            assert torch.equal(out[:, :50], kda.short_conv_fwd(x, w, b, s, cu_seqlens=good)[0][:, :50])
+            assert torch.equal(o[:, :50], kda.glr_fwd(X, z, ls, bi, i, initial_state=s0, cu_seqlens=good)[0][:, :50])
