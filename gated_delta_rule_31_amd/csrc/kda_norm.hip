@@ -7,7 +7,7 @@
 // gradients of 131072 of them 37 + 4; gradients between two blocks, 8192 x 7168 with a float32 stream, 261 + 8 us (4.9
 // TB/s); one row of 7168, 3.9 us.  Rows of 7168 by 256, 512 or 1024 lanes: 269, 269 and 274 us.
 //
-// LANES lanes share a row (16, 32 or 64 of a wave, or a whole workgroup), each with NV vectors of
+// LANES lanes share a row (4, 16, 32 or 64 of a wave, or a whole workgroup), each with NV vectors of
 // VEC neighbouring channels, LANES vectors apart.  Workgroups go from row to row and keep the
 // weights in registers, and in the backward pass the weights' sums, which they write once.
 #include "kda_rows.h"
@@ -29,7 +29,12 @@ template <int LANES, int N, int M>
 __device__ __forceinline__ void row_sum(float (&x)[N], RowSum<LANES, M> &lds, int &turn) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        x[j] = row16_sum(x[j]);
+        if constexpr (LANES < 16) {
+#pragma unroll
+            for (int d = 1; d < LANES; d *= 2) x[j] += __shfl_xor(x[j], d);
+        } else {
+            x[j] = row16_sum(x[j]);
+        }
         if constexpr (LANES >= 32) x[j] += __shfl_xor(x[j], 16);
         if constexpr (LANES >= 64) x[j] += __shfl_xor(x[j], 32);
     }
@@ -58,13 +63,69 @@ __device__ __forceinline__ void load_weight(float (&w)[NV][VEC], const float *p,
         for (int i = 0; i < VEC; ++i) w[k][i] = on && p && lane + k * LANES < vecs ? p[(lane + k * LANES) * VEC + i] : 1.f;
 }
 
+// Whether a lane keeps its weights from row to row.  A lane of the widest workgroups has 128 registers; with 16 numbers of
+// a row it reads them again.
+template <int VEC, int LANES, int NV>
+constexpr bool KEEP = LANES < 1024 || VEC * NV <= 8;
+template <int VEC, int LANES, int NV>
+struct Weight {
+    float w[KEEP<VEC, LANES, NV> ? NV : 1][VEC];
+    const float *p;
+    int lane, vecs;
+    __device__ __forceinline__ void begin(const float *weight, bool on, int l, int v) {
+        p = on ? weight : nullptr;
+        lane = l;
+        vecs = v;
+        if constexpr (KEEP<VEC, LANES, NV>) load_weight<VEC, LANES, NV>(w, p, true, lane, vecs);
+    }
+    __device__ __forceinline__ float get(int k, int i) const {
+        if constexpr (KEEP<VEC, LANES, NV>) return w[k][i];
+        else return p && lane + k * LANES < vecs ? p[(lane + k * LANES) * VEC + i] : 1.f;
+    }
+};
+
+// A lane's sums of a weight's gradient: in registers, or, where a lane of the widest workgroups has 16 numbers of a row, in
+// its own places in LDS (1000 rows of 16384: 255 us with registers that spill).
+template <int VEC, int LANES, int NV>
+struct Sums {
+    static constexpr bool LDS = !KEEP<VEC, LANES, NV>;
+    float s[LDS ? 1 : NV][VEC];
+    float *own;
+    __device__ __forceinline__ void begin(float *lds) {
+        own = lds + threadIdx.x;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                if constexpr (LDS) own[(k * VEC + i) * LANES] = 0.f;
+                else s[k][i] = 0.f;
+            }
+    }
+    __device__ __forceinline__ void add(int k, int i, float x, float y) {
+        if constexpr (LDS) own[(k * VEC + i) * LANES] = fmaf(x, y, own[(k * VEC + i) * LANES]);
+        else s[k][i] = fmaf(x, y, s[k][i]);
+    }
+    __device__ __forceinline__ float get(int k, int i) const {
+        if constexpr (LDS) return own[(k * VEC + i) * LANES];
+        else return s[k][i];
+    }
+};
+
+// A row's vectors: the row is the same for all lanes of a workgroup (or a row's own where lanes share a wave), so a lane's
+// address is one offset.
 template <typename T, int VEC, int LANES, int NV>
 __device__ __forceinline__ void load_rows(Raw<T, VEC> (&r)[NV], const void *p, int64_t at, int lane, int vecs) {
+    const char *row = static_cast<const char *>(p) + at * (int64_t)sizeof(T);
+    const uint32_t off = here(lane * (uint32_t)(VEC * sizeof(T)));
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         r[k].zero();
-        if (lane + k * LANES < vecs) r[k].load(static_cast<const T *>(p) + at + (lane + k * LANES) * VEC);
+        if (lane + k * LANES < vecs) r[k].load(row + k * (int)(LANES * VEC * sizeof(T)), off);
     }
+}
+template <int LANES, typename T, int VEC>
+__device__ __forceinline__ void store_row(const Raw<T, VEC> &r, void *p, int64_t at, int k, int lane, int vecs) {
+    if (lane + k * LANES < vecs) r.store(static_cast<char *>(p) + at * (int64_t)sizeof(T) + k * (int)(LANES * VEC * sizeof(T)), here(lane * (uint32_t)(VEC * sizeof(T))));
 }
 
 __device__ __forceinline__ int64_t gate_row(const NormArgs &a, int64_t row) {
@@ -80,10 +141,10 @@ __global__ __launch_bounds__(THREADS<LANES>) void norm_fwd_kernel(const NormArgs
     int turn = 0;
     const int lane = threadIdx.x % LANES, vecs = a.D / VEC;
     const float inv = 1.f / a.D;
-    float wa[NV][VEC], wb[NV][VEC];
-    load_weight<VEC, LANES, NV>(wa, a.wa, a.after, lane, vecs);
-    load_weight<VEC, LANES, NV>(wb, a.wb, a.before, lane, vecs);
-    for (int64_t row = (int64_t)blockIdx.x * EACH + threadIdx.x / LANES; row < a.rows; row += (int64_t)gridDim.x * EACH) {
+    Weight<VEC, LANES, NV> wa, wb;
+    wa.begin(a.wa, a.after, lane, vecs);
+    wb.begin(a.wb, a.before, lane, vecs);
+    for (int64_t row = (int64_t)blockIdx.x * EACH + (EACH > 1 ? threadIdx.x / LANES : 0); row < a.rows; row += (int64_t)gridDim.x * EACH) {
         Raw<T, VEC> y[NV], z[NV];
         Raw<R, VEC> x[NV];
         load_rows<T, VEC, LANES, NV>(y, a.y, row * a.D, lane, vecs);
@@ -105,7 +166,7 @@ __global__ __launch_bounds__(THREADS<LANES>) void norm_fwd_kernel(const NormArgs
             Raw<R, VEC> o;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                float p = y[k].get(i) * r * wa[k][i];
+                float p = y[k].get(i) * r * wa.get(k, i);
                 if (a.gate) {
                     const float g = z[k].get(i), s = sigmoid_f32(g);
                     p *= a.silu ? g * s : s;
@@ -115,7 +176,7 @@ __global__ __launch_bounds__(THREADS<LANES>) void norm_fwd_kernel(const NormArgs
                 q[0] = fmaf(p, p, q[0]);
                 o.set(i, p);
             }
-            if (lane + k * LANES < vecs) o.store(static_cast<R *>(a.h) + row * a.D + (lane + k * LANES) * VEC);
+            store_row<LANES>(o, a.h, row * a.D, k, lane, vecs);
         }
         if (!a.before) continue;
         row_sum<LANES>(q, lds, turn);
@@ -124,8 +185,8 @@ __global__ __launch_bounds__(THREADS<LANES>) void norm_fwd_kernel(const NormArgs
         for (int k = 0; k < NV; ++k) {
             Raw<T, VEC> o;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) o.set(i, h[k][i] * rh * wb[k][i]);
-            if (lane + k * LANES < vecs) o.store(static_cast<T *>(a.n) + row * a.D + (lane + k * LANES) * VEC);
+            for (int i = 0; i < VEC; ++i) o.set(i, h[k][i] * rh * wb.get(k, i));
+            store_row<LANES>(o, a.n, row * a.D, k, lane, vecs);
         }
     }
 }
@@ -141,10 +202,14 @@ __global__ __launch_bounds__(THREADS<LANES>) void norm_bwd_kernel(const NormArgs
     int turn = 0;
     const int lane = threadIdx.x % LANES, vecs = a.D / VEC;
     const float inv = 1.f / a.D;
-    float wa[NV][VEC], wb[NV][VEC], da[NV][VEC] = {}, db[NV][VEC] = {};
-    load_weight<VEC, LANES, NV>(wa, a.wa, a.after, lane, vecs);
-    load_weight<VEC, LANES, NV>(wb, a.wb, a.before, lane, vecs);
-    for (int64_t row = (int64_t)blockIdx.x * EACH + threadIdx.x / LANES; row < a.rows; row += (int64_t)gridDim.x * EACH) {
+    Sums<VEC, LANES, NV> da, db;
+    __shared__ float in_lds[Sums<VEC, LANES, NV>::LDS ? 2 : 1][Sums<VEC, LANES, NV>::LDS ? NV * VEC * LANES : 1];
+    da.begin(in_lds[0]);
+    db.begin(in_lds[Sums<VEC, LANES, NV>::LDS ? 1 : 0]);
+    Weight<VEC, LANES, NV> wa, wb;
+    wa.begin(a.wa, a.after, lane, vecs);
+    wb.begin(a.wb, a.before, lane, vecs);
+    for (int64_t row = (int64_t)blockIdx.x * EACH + (EACH > 1 ? threadIdx.x / LANES : 0); row < a.rows; row += (int64_t)gridDim.x * EACH) {
         const int64_t at = row * a.D;
         Raw<T, VEC> y[NV], z[NV], dn[NV];
         Raw<R, VEC> h[NV], dh[NV];
@@ -164,7 +229,7 @@ __global__ __launch_bounds__(THREADS<LANES>) void norm_bwd_kernel(const NormArgs
                 if (a.before) {
                     const float x = h[k].get(i);
                     s[1] = fmaf(x, x, s[1]);
-                    s[2] = fmaf(dn[k].get(i) * wb[k][i], x, s[2]);
+                    s[2] = fmaf(dn[k].get(i) * wb.get(k, i), x, s[2]);
                 }
             }
         if (a.before || a.after) row_sum<LANES>(s, lds, turn);
@@ -173,7 +238,6 @@ __global__ __launch_bounds__(THREADS<LANES>) void norm_bwd_kernel(const NormArgs
         float dp[NV][VEC], q[1] = {0.f};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const bool on = lane + k * LANES < vecs;
             Raw<R, VEC> ox;
             Raw<T, VEC> oz;
 #pragma unroll
@@ -181,8 +245,8 @@ __global__ __launch_bounds__(THREADS<LANES>) void norm_bwd_kernel(const NormArgs
                 float g = a.d_h ? dh[k].get(i) : 0.f;
                 if (a.before) {
                     const float x = h[k].get(i), d = dn[k].get(i);
-                    g = fmaf(rh, fmaf(d, wb[k][i], -x * mean), g);
-                    db[k][i] = fmaf(d * rh, x, db[k][i]);
+                    g = fmaf(rh, fmaf(d, wb.get(k, i), -x * mean), g);
+                    db.add(k, i, d * rh, x);
                     ox.set(i, g);
                 }
                 g *= a.scale;
@@ -191,17 +255,15 @@ __global__ __launch_bounds__(THREADS<LANES>) void norm_bwd_kernel(const NormArgs
                     const float t = z[k].get(i);
                     float f;  // 1 - e
                     const float e = sigmoid_f32(t, f);
-                    oz.set(i, g * v * wa[k][i] * (a.silu ? e * fmaf(t, f, 1.f) : e * f));
+                    oz.set(i, g * v * wa.get(k, i) * (a.silu ? e * fmaf(t, f, 1.f) : e * f));
                     g *= a.silu ? t * e : e;
                 }
-                da[k][i] = fmaf(g, v, da[k][i]);
-                dp[k][i] = g * wa[k][i];
+                da.add(k, i, g, v);
+                dp[k][i] = g * wa.get(k, i);
                 q[0] = fmaf(dp[k][i], v, q[0]);
             }
-            if (on) {
-                if (a.before && a.d_res) ox.store(static_cast<R *>(a.d_res) + at + (lane + k * LANES) * VEC);
-                if (a.gate) oz.store(static_cast<T *>(a.d_gate) + at + (lane + k * LANES) * VEC);
-            }
+            if (a.before && a.d_res) store_row<LANES>(ox, a.d_res, at, k, lane, vecs);
+            if (a.gate) store_row<LANES>(oz, a.d_gate, at, k, lane, vecs);
         }
         if (a.after) row_sum<LANES>(q, lds, turn);
         const float back = a.after ? q[0] * inv * r : 0.f;
@@ -210,7 +272,7 @@ __global__ __launch_bounds__(THREADS<LANES>) void norm_bwd_kernel(const NormArgs
             Raw<T, VEC> o;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) o.set(i, r * fmaf(-back, y[k].get(i), dp[k][i]));
-            if (lane + k * LANES < vecs) o.store(static_cast<T *>(a.dy) + at + (lane + k * LANES) * VEC);
+            store_row<LANES>(o, a.dy, at, k, lane, vecs);
         }
     }
     if (!a.part) return;
@@ -223,7 +285,7 @@ __global__ __launch_bounds__(THREADS<LANES>) void norm_bwd_kernel(const NormArgs
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) all[group][(lane + k * LANES) * VEC + i] = w ? db[k][i] : da[k][i];
+                for (int i = 0; i < VEC; ++i) all[group][(lane + k * LANES) * VEC + i] = w ? db.get(k, i) : da.get(k, i);
             __syncthreads();
             for (int c = threadIdx.x; c < a.D; c += THREADS<LANES>) {
                 float x = 0.f;
@@ -239,8 +301,8 @@ __global__ __launch_bounds__(THREADS<LANES>) void norm_bwd_kernel(const NormArgs
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     const int64_t at = (int64_t)blockIdx.x * 2 * a.D + (lane + k * LANES) * VEC + i;
-                    a.part[at] = da[k][i];
-                    a.part[at + a.D] = db[k][i];
+                    a.part[at] = da.get(k, i);
+                    a.part[at + a.D] = db.get(k, i);
                 }
     }
 }
@@ -261,7 +323,8 @@ hipError_t launch(NormArgs &a, hipStream_t stream) {
 template <bool BWD, typename T, typename R, int VEC>
 hipError_t by_width(NormArgs &a, hipStream_t stream) {
     const int vecs = a.D / VEC;
-    if constexpr (VEC > 1) {
+    if constexpr (VEC > 2) {
+        if (vecs <= 4) return launch<BWD, T, R, VEC, 4, 1>(a, stream);
         if (vecs <= 16) return launch<BWD, T, R, VEC, 16, 1>(a, stream);
         if (vecs <= 32) return launch<BWD, T, R, VEC, 32, 1>(a, stream);
         if (vecs <= 64) return launch<BWD, T, R, VEC, 64, 1>(a, stream);
@@ -269,33 +332,40 @@ hipError_t by_width(NormArgs &a, hipStream_t stream) {
         if (vecs <= 512) return launch<BWD, T, R, VEC, 512, 1>(a, stream);
         if (vecs <= 1024) return launch<BWD, T, R, VEC, 512, 2>(a, stream);
         if (vecs <= 2048) return launch<BWD, T, R, VEC, 1024, 2>(a, stream);
-        if (vecs <= 4096) return launch<BWD, T, R, VEC, 1024, 4>(a, stream);
-    } else {
-        if (vecs <= 64) return launch<BWD, T, R, VEC, 16, 4>(a, stream);
-        if (vecs <= 512) return launch<BWD, T, R, VEC, 64, 8>(a, stream);
-        if (vecs <= 2048) return launch<BWD, T, R, VEC, 256, 8>(a, stream);
-        if (vecs <= 16384) return launch<BWD, T, R, VEC, 1024, 16>(a, stream);
+        if constexpr (VEC == 4)
+            if (vecs <= 4096) return launch<BWD, T, R, VEC, 1024, 4>(a, stream);
+    } else {  // rows off a 16-byte border: two numbers at a time where the width is even, one where it is odd
+        constexpr int TWO = VEC == 2 ? 1 : 2;
+        if (vecs <= 16 * 2 * TWO) return launch<BWD, T, R, VEC, 16, 2 * TWO>(a, stream);
+        if (vecs <= 64 * 4 * TWO) return launch<BWD, T, R, VEC, 64, 4 * TWO>(a, stream);
+        if (vecs <= 256 * 4 * TWO) return launch<BWD, T, R, VEC, 256, 4 * TWO>(a, stream);
+        if (vecs <= 512 * 8 * TWO) return launch<BWD, T, R, VEC, 512, 8 * TWO>(a, stream);
+        if (vecs <= 1024 * 8 * TWO) return launch<BWD, T, R, VEC, 1024, 8 * TWO>(a, stream);
     }
     return hipErrorNotSupported;
 }
 
 template <bool BWD>
-hipError_t by_type(NormArgs &a, bool fp32, bool h_fp32, bool wide, hipStream_t stream) {
-    if (fp32) return wide ? by_width<BWD, float, float, 4>(a, stream) : by_width<BWD, float, float, 1>(a, stream);
-    if (h_fp32) return wide ? by_width<BWD, __bf16, float, 8>(a, stream) : by_width<BWD, __bf16, float, 1>(a, stream);
-    return wide ? by_width<BWD, __bf16, __bf16, 8>(a, stream) : by_width<BWD, __bf16, __bf16, 1>(a, stream);
+hipError_t by_type(NormArgs &a, bool fp32, bool h_fp32, int vec, hipStream_t stream) {
+    if (fp32) return vec > 2 ? by_width<BWD, float, float, 4>(a, stream) : vec == 2 ? by_width<BWD, float, float, 2>(a, stream) : by_width<BWD, float, float, 1>(a, stream);
+    if (h_fp32) return vec > 2 ? by_width<BWD, __bf16, float, 8>(a, stream) : vec == 2 ? by_width<BWD, __bf16, float, 2>(a, stream) : by_width<BWD, __bf16, float, 1>(a, stream);
+    return vec > 2 ? by_width<BWD, __bf16, __bf16, 8>(a, stream) : vec == 2 ? by_width<BWD, __bf16, __bf16, 2>(a, stream) : by_width<BWD, __bf16, __bf16, 1>(a, stream);
 }
 
 }  // namespace
 
-int norm_groups(int64_t rows, int D) { return (int)(rows < 512 ? rows : 512); }
-
-hipError_t launch_norm_fwd(NormArgs a, bool fp32, bool h_fp32, bool wide, hipStream_t stream) {
-    return by_type<false>(a, fp32, h_fp32, wide, stream);
+// Workgroups of the backward pass, each with sums of its own: two a compute unit, or the one that fits of the widest.
+int norm_groups(int64_t rows, int D) {
+    const int most = D > 8192 ? 256 : 512;
+    return (int)(rows < most ? rows : most);
 }
 
-hipError_t launch_norm_bwd(NormArgs a, bool fp32, bool h_fp32, bool wide, float *d_wa, float *d_wb, hipStream_t stream) {
-    const hipError_t e = by_type<true>(a, fp32, h_fp32, wide, stream);
+hipError_t launch_norm_fwd(NormArgs a, bool fp32, bool h_fp32, int vec, hipStream_t stream) {
+    return by_type<false>(a, fp32, h_fp32, vec, stream);
+}
+
+hipError_t launch_norm_bwd(NormArgs a, bool fp32, bool h_fp32, int vec, float *d_wa, float *d_wb, hipStream_t stream) {
+    const hipError_t e = by_type<true>(a, fp32, h_fp32, vec, stream);
     if (e != hipSuccess || !a.part) return e;
     return launch_column_sums(ColumnSums{a.part, a.groups, 2 * a.D, a.D, 1, d_wa, d_wb}, stream);
 }

@@ -290,7 +290,8 @@ struct NormArgs {
     int groups;                  // rows of `part`: at most norm_groups of them are written
 };
 int norm_groups(int64_t rows, int D);
-hipError_t launch_norm_fwd(NormArgs a, bool fp32, bool h_fp32, bool wide, hipStream_t stream);
-hipError_t launch_norm_bwd(NormArgs a, bool fp32, bool h_fp32, bool wide, float *d_wa, float *d_wb, hipStream_t stream);
+// vec: numbers at a time, 2, 1, or any other number for 16 bytes
+hipError_t launch_norm_fwd(NormArgs a, bool fp32, bool h_fp32, int vec, hipStream_t stream);
+hipError_t launch_norm_bwd(NormArgs a, bool fp32, bool h_fp32, int vec, float *d_wa, float *d_wb, hipStream_t stream);
 
 }  // namespace kda

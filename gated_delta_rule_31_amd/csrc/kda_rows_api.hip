@@ -19,25 +19,12 @@ constexpr int64_t MAX_ROWS = INT32_MAX - 64;    // a row's number, and a tile's 
 constexpr int64_t MAX_CHANNELS = 1 << 20;
 constexpr int64_t MAX_GRID = (int64_t)1 << 31;  // threads of a grid, half of what a launch takes
 
-// Whether rows can be read (and written) 16 bytes at a time: every pointer, and every distance between rows.
-struct Wide {
-    size_t size;  // of an element
-    bool ok = true;
-    Wide &ptr(const void *p) {
-        ok = ok && (uintptr_t)p % 16 == 0;
-        return *this;
-    }
-    Wide &stride(int64_t n) {
-        ok = ok && n % (int64_t)(16 / size) == 0;
-        return *this;
-    }
-};
-// Likewise `unit` channels at a time, for rows `n` numbers of `size` bytes apart.
+// Whether rows can be read (and written) `unit` numbers at a time, at most 16 bytes of them in one load: for rows `n` numbers of `size` bytes apart.
 struct Units {
     int unit;
     bool ok = true;
     Units &rows(const void *p, size_t size, int64_t n) {
-        ok = ok && (!p || ((uintptr_t)p % (unit * size) == 0 && n % unit == 0));
+        ok = ok && (!p || ((uintptr_t)p % (unit * size < 16 ? unit * size : 16) == 0 && n % unit == 0));
         return *this;
     }
 };
@@ -436,11 +423,13 @@ kda_status kda_block_norm_fwd(const void *y, const void *gate, int64_t gate_stri
     a.silu = (flags & KDA_SILU) != 0;
     a.h = h;
     a.n = n;
-    Wide w{e};
-    w.ptr(y).ptr(gate).ptr(residual).ptr(h).stride(D);
-    if (before) w.ptr(n);
-    if (gate) w.stride(gate_stride).stride(a.gate_head);
-    return done(kda::launch_norm_fwd(a, dtype == KDA_F32, h_dtype == KDA_F32, w.ok, stream));
+    auto fits = [&](int unit) {
+        Units w{unit};
+        w.rows(y, e, D).rows(residual, he, D).rows(h, he, D).rows(before ? n : nullptr, e, D).rows(gate, e, gate_stride).rows(gate, e, a.gate_head);
+        return w.ok;
+    };
+    const int vec = fits(16 / (int)e) ? 16 / (int)e : fits(2) ? 2 : 1;
+    return done(kda::launch_norm_fwd(a, dtype == KDA_F32, h_dtype == KDA_F32, vec, stream));
 }
 
 size_t kda_block_norm_bwd_workspace_size(int64_t tokens, int heads, int D) {
@@ -493,11 +482,14 @@ kda_status kda_block_norm_bwd(const void *y, const void *gate, int64_t gate_stri
     a.d_res = d_residual;
     a.part = sums ? static_cast<float *>(workspace) : nullptr;
     a.groups = kda::norm_groups(a.rows, D);
-    Wide w{e};
-    w.ptr(y).ptr(gate).ptr(d_h).ptr(dy).stride(D);
-    if (gate) w.ptr(d_gate).stride(gate_stride).stride(a.gate_head);
-    if (before) w.ptr(h).ptr(d_n).ptr(d_residual);
-    return done(kda::launch_norm_bwd(a, dtype == KDA_F32, h_dtype == KDA_F32, w.ok, d_weight_after, d_weight_before, stream));
+    auto fits = [&](int unit) {
+        Units w{unit};
+        w.rows(y, e, D).rows(d_h, he, D).rows(dy, e, D).rows(gate, e, gate_stride).rows(gate, e, a.gate_head).rows(gate ? d_gate : nullptr, e, D);
+        w.rows(before ? h : nullptr, he, D).rows(before ? d_n : nullptr, e, D).rows(before ? d_residual : nullptr, he, D);
+        return w.ok;
+    };
+    const int vec = fits(16 / (int)e) ? 16 / (int)e : fits(2) ? 2 : 1;
+    return done(kda::launch_norm_bwd(a, dtype == KDA_F32, h_dtype == KDA_F32, vec, d_weight_after, d_weight_before, stream));
 }
 
 }  // extern "C"
