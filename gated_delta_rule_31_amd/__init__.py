@@ -34,6 +34,9 @@ Entry points (same names as the C ABI, minus the ``kda_`` prefix where noted):
 * ``gated_delta_rule`` / ``gdr_chunk_fwd`` / ``gdr_chunk_bwd`` -- the same recurrence with one
   decay per value head and key heads shared by groups of value heads; ``gdr_recurrent_step``
   and ``draft_verify`` -- decoding over a pool of states with drafted tokens (``gdr.py``).
+* ``short_conv`` / ``short_conv_fwd`` / ``_bwd`` / ``_step``, ``gated_linear_recurrence`` / ``glr_fwd`` /
+  ``_bwd`` / ``_step``, ``block_norm`` / ``block_norm_fwd`` / ``_bwd`` and ``gated_norm`` -- what stands
+  around the recurrence in a layer (``layer.py``).
 """
 from __future__ import annotations
 

@@ -430,7 +430,7 @@ def norm_case(shape, dtype, res, gate, wa, wb, seed):
             1 + 0.3 * r(shape[-1]) if wb else None)
 
 
-WIDTHS = [1, 2, 7, 8, 40, 64, 100, 128, 136, 256, 264, 500, 512, 1000, 1032, 2048, 4096, 4104, 7168, 8200, 16383, 16384]
+WIDTHS = [1, 2, 7, 8, 18, 32, 40, 64, 100, 150, 128, 136, 256, 264, 500, 512, 1000, 1032, 2048, 4096, 4104, 5170, 7168, 8200, 9998, 16383, 16384]
 
 
 @pytest.mark.parametrize("D", WIDTHS)
