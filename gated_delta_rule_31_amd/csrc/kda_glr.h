@@ -4,9 +4,10 @@
 //   a_t = e^{g_t},   b_t = f_t i_t x_t,    f = sqrt(1 - e^{2g}) or 1,   i = sigmoid(i_t) or 1
 //   h_t = a_t h_{t-1} + b_t
 // A stretch of rows maps the state in front of it to the one behind it as h -> A h + H; a
-// sequence that begins inside it makes A zero.  Two stretches joined: (A2 A1, A2 H1 + H2).
-// Where A is zero the state in front is not looked at, so nothing of one sequence reaches another,
-// infinities and NaN among it.
+// sequence that begins inside it makes A minus zero.  Two stretches joined: (A2 A1, A2 H1 + H2).
+// Where A is minus zero the state in front is not looked at, so nothing of one sequence reaches another,
+// infinities and NaN among it; where decays alone made it zero (plus zero: they are not negative) it
+// is, so that an infinity or a NaN of a sequence is not forgotten by it.
 #pragma once
 
 #include "kda_rows.h"
@@ -63,7 +64,8 @@ __device__ __forceinline__ Gate make_gate(float z, float in, float scale2, float
     return g;
 }
 
-__device__ __forceinline__ float join(float a, float h, float before) { return a == 0.f ? h : fmaf(a, before, h); }
+constexpr float CUT = -0.f;  // the A of a stretch in which a sequence begins
+__device__ __forceinline__ float join(float a, float h, float before) { return __float_as_uint(a) == 0x80000000u ? h : fmaf(a, before, h); }
 
 // The types of a call: x and the logits are T, log decays float32.
 template <typename T, bool LOGITS>

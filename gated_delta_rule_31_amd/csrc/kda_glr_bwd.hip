@@ -66,7 +66,10 @@ __global__ __launch_bounds__(64 * WAVES) void glr_back_kernel(const GlrArgs a) {
                     if (HERE && r + u >= p.own) continue;
                     if (HERE && last >> u & 1) {
 #pragma unroll
-                        for (int i = 0; i < VEC; ++i) A[i] = Q[i] = 0.f;
+                        for (int i = 0; i < VEC; ++i) {
+                            A[i] = CUT;
+                            Q[i] = 0.f;
+                        }
                         if (a.d_sf) load_f32<VEC>(Q, a.d_sf + (int64_t)a.seqs.of(p.t0 + r + u) * a.C + p.c);
                     }
 #pragma unroll

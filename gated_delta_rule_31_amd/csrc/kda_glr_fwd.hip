@@ -79,7 +79,10 @@ __global__ __launch_bounds__(64 * WAVES) void glr_fwd_kernel(const GlrArgs a, in
                 if (HERE && r + u >= p.count) continue;
                 if (HERE && first >> u & 1) {
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) A[i] = h[i] = 0.f;
+                    for (int i = 0; i < VEC; ++i) {
+                        A[i] = CUT;
+                        h[i] = 0.f;
+                    }
                     if (a.s0) load_f32<VEC>(h, a.s0 + (int64_t)a.seqs.of(p.t0 + r + u) * a.C + p.c);
                 }
                 Raw<T, VEC> y;

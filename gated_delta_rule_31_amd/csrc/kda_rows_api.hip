@@ -111,6 +111,8 @@ bool glr_fits(const kda::Seqs &s, int C) {
     const int64_t tiles = (s.rows + 63) / 64;  // where there are many
     return tiles * ((C + 63) / 64 * 64) < MAX_GRID && (int64_t)s.N * C < MAX_GRID;
 }
+// a workspace of which nothing is used is not empty: 0 says that there is no such call
+size_t some(size_t bytes) { return bytes ? bytes : 256; }
 int64_t glr_kept_rows(int64_t rows) { return (rows + kda::GLR_KEPT - 1) / kda::GLR_KEPT; }
 
 kda_status norm_shape(kda_dtype dtype, kda_dtype h_dtype, int64_t tokens, int heads, int D, float eps, unsigned flags) {
@@ -260,7 +262,7 @@ size_t kda_glr_fwd_workspace_size(int B, int64_t T, int H, int K) {
     bool empty;
     if (H <= 0 || K <= 0 || (int64_t)H * K > MAX_CHANNELS || batch(a.seqs, nullptr, 0, B, T, &empty) != KDA_OK || empty) return 0;
     a.C = H * K;
-    return glr_fits(a.seqs, a.C) ? kda::carve_glr_fwd(a, nullptr) : 0;
+    return glr_fits(a.seqs, a.C) ? some(kda::carve_glr_fwd(a, nullptr)) : 0;
 }
 
 size_t kda_glr_bwd_workspace_size(int B, int64_t T, int H, int K, int logits, int kept) {
@@ -268,10 +270,10 @@ size_t kda_glr_bwd_workspace_size(int B, int64_t T, int H, int K, int logits, in
     bool empty;
     if (H <= 0 || K <= 0 || (int64_t)H * K > MAX_CHANNELS || batch(a.seqs, nullptr, 0, B, T, &empty) != KDA_OK || empty) return 0;
     a.C = H * K;
-    static const float some = 0.f;
-    a.gates.log_scale = logits ? &some : nullptr;
+    static const float one = 0.f;
+    a.gates.log_scale = logits ? &one : nullptr;
     float *sums;
-    return glr_fits(a.seqs, a.C) ? kda::carve_glr_bwd(a, nullptr, kept != 0, sums) : 0;
+    return glr_fits(a.seqs, a.C) ? some(kda::carve_glr_bwd(a, nullptr, kept != 0, sums)) : 0;
 }
 
 kda_status kda_glr_fwd(const void *x, int64_t x_stride, kda_dtype dtype, const void *gate, int64_t gate_stride, const float *log_scale,

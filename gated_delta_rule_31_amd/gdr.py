@@ -32,11 +32,11 @@ def _input(x: Optional[torch.Tensor], name: str, like: Optional[torch.Tensor] = 
         if not x.is_cuda:
             raise ValueError("%s must be on the GPU (got %s)" % (name, x.device))
     elif x.device != like.device:
-        raise ValueError("%s is on %s, but q is on %s" % (name, x.device, like.device))
+        raise ValueError("%s is on %s, but the first input is on %s" % (name, x.device, like.device))
     if dtype is not None and x.dtype != dtype:
         raise ValueError("%s must be %s (got %s)" % (name, dtype, x.dtype))
     if x.requires_grad and torch.is_grad_enabled():
-        raise ValueError("%s requires grad: the raw kernels do not record autograd; use gated_delta_rule, or call gdr_chunk_bwd yourself" % name)
+        raise ValueError("%s requires grad: the raw kernels do not record autograd; use the recorded call (gated_delta_rule, short_conv, gated_linear_recurrence, block_norm), or the call for its gradients yourself" % name)
     if not x.is_contiguous():
         x = x.contiguous()
     return x.clone() if x.data_ptr() % border else x

@@ -325,8 +325,8 @@ def glr_step(x: torch.Tensor, gate: torch.Tensor, states: torch.Tensor, log_scal
     """Up to S tokens for each of B requests over a pool of states: x, gate, in_gate [B,S,H,K] and their
     companions as in ``glr_fwd``, states [pool,H,K] float32 contiguous, updated in place.  ``slots``,
     ``start`` and ``lengths`` as in ``gdr_recurrent_step``.  Returns out [B,S,H,K]."""
-    x, _, gate, _, log_scale, bias, in_gate, _ = _glr_inputs(*(None if y is None else y.contiguous() for y in (x, gate)), log_scale, bias,
-                                                             None if in_gate is None else in_gate.contiguous())
+    x, gate, in_gate = (y.contiguous() if isinstance(y, torch.Tensor) else y for y in (x, gate, in_gate))
+    x, _, gate, _, log_scale, bias, in_gate, _ = _glr_inputs(x, gate, log_scale, bias, in_gate)
     B, S, H, K = x.shape
     if not isinstance(states, torch.Tensor) or states.dim() != 3:
         raise ValueError("states must be [pool, H, K]")
@@ -382,11 +382,11 @@ def gated_linear_recurrence(x, gate, log_scale=None, bias=None, in_gate=None, in
 
 def _tokens_heads(shape):
     """[..., D] as tokens of heads: the dimension before the last is a token's heads where there are three or more."""
-    heads = shape[-2] if len(shape) > 2 else 1
     n = 1
     for s in shape[:-1]:
         n *= s
-    return (n // heads if heads else 0), heads
+    heads = shape[-2] if len(shape) > 2 and n else 1
+    return n // heads, heads
 
 
 def _gate_rows(gate, y, tokens, heads):
@@ -417,7 +417,7 @@ def _norm_inputs(y, gate, weight_after, weight_before, norm_after, norm_before, 
     y = _input(y, "y", None, None, 1)
     if y is None:
         raise TypeError("y must be a torch.Tensor")
-    if y.dim() < 2 or y.shape[-1] < 1 or 0 in y.shape[1:]:
+    if y.dim() < 2 or y.shape[-1] < 1:
         raise ValueError("y must be [tokens, D] or [..., heads, D]")
     tokens, heads = _tokens_heads(y.shape)
     gate, *gate_strides = _gate_rows(gate, y, tokens, heads)
@@ -476,7 +476,6 @@ def block_norm_bwd(y: torch.Tensor, d_h: Optional[torch.Tensor], d_n: Optional[t
         raise ValueError("d_h must be shaped like y, in the type of h")
     made = lambda x: None if x is None else torch.empty(x.shape, dtype=x.dtype, device=dev)  # noqa: E731
     dy, dz, dwa, dwb = made(y), made(gate), made(weight_after), made(weight_before)
-    dz = dz.contiguous() if dz is not None else None
     d_res = torch.empty(y.shape, dtype=like.dtype, device=dev) if norm_before else d_h
     workspace = _workspace(workspace, block_norm_bwd_workspace_size(tokens, heads, D), dev)
     _call(_load().kda_block_norm_bwd, dev, _p(y), _p(gate), *gate_strides, _dtype_code(y.dtype), _p(h) if norm_before else None,

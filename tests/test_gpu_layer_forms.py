@@ -308,3 +308,49 @@ def test_offsets_out_of_order():
             good = gpu(offsets(lens))
             assert torch.equal(out[:, :50], kda.short_conv_fwd(x, w, b, s, cu_seqlens=good)[0][:, :50])
             assert torch.equal(o[:, :50], kda.glr_fwd(X, z, ls, bi, i, initial_state=s0, cu_seqlens=good)[0][:, :50])
+
+
+@pytest.mark.parametrize("shape", [(0, 16), (1, 0, 16), (2, 0, 3, 16), (2, 5, 0, 16)])
+def test_norm_of_no_rows(shape):
+    """A batch without tokens, in every form that has a place for them, recorded and not: empty results, and gradients of the weights that are zeros."""
+    y, r, z = (torch.empty(shape, dtype=BF, device="cuda", requires_grad=True) for _ in range(3))
+    wa, wb = (torch.ones(16, device="cuda", requires_grad=True) for _ in range(2))
+    h, n = kda.block_norm(y, gate=z, residual=r, weight_after=wa, weight_before=wb)
+    assert h.shape == shape and n.shape == shape
+    dy, dz, dr, da, db = torch.autograd.grad([h, n], [y, z, r, wa, wb], [torch.empty_like(h), torch.empty_like(n)])
+    assert dy.shape == shape and dz.shape == shape and dr.shape == shape
+    assert torch.equal(da, torch.zeros_like(wa)) and torch.equal(db, torch.zeros_like(wb))
+    assert kda.gated_norm(y.detach(), z.detach(), wa.detach()).shape == shape
+
+
+def test_refusals_name_what_to_call():
+    x = torch.zeros(2, 3, 1, 8, device="cuda")
+    for call in (lambda: kda.glr_step([1.0], x, x[0]), lambda: kda.glr_step(x, None, x[0]), lambda: kda.glr_step(x, x, x[0], in_gate=1.0)):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(ValueError, match="short_conv"):
+        kda.short_conv_fwd(x[:, :, 0].requires_grad_(), torch.zeros(8, 2, device="cuda"))
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("T", [40, 400, 3000])
+def test_scan_does_not_forget_what_is_not_finite(bad, T):
+    """alpha = e^-5 everywhere: a tile's product of decays leaves float32's range, but inf * alpha stays inf and NaN stays
+    NaN down the sequence (through zero decays at most inf * 0, NaN), as in the recurrence row by row; the next sequence and the other
+    channels have none of it.  Its gradients: the same from the right."""
+    H, K, behind = 2, 8, 30
+    gate = torch.full((1, T + behind, H, K), -5.0, device="cuda")
+    x = torch.ones(1, T + behind, H, K, device="cuda")
+    s0 = torch.zeros(2, H, K, device="cuda")
+    s0[0, 1, 3] = bad
+    cu = gpu(torch.tensor([0, T, T + behind], dtype=torch.int32))
+    out, final, kept = kda.glr_fwd(x, gate, initial_state=s0, cu_seqlens=cu, keep=True)
+    want = torch.ones_like(out, dtype=torch.bool)
+    want[:, :T, 1, 3] = False
+    assert torch.equal(torch.isfinite(out), want)
+    assert not torch.isfinite(final[0, 1, 3]) and torch.isfinite(final).sum() == final.numel() - 1
+    d_final = torch.zeros_like(final)
+    d_final[0, 1, 3] = bad
+    dx, dg, _, _, _, ds = kda.glr_bwd(x, gate, torch.ones_like(x), initial_state=torch.zeros_like(s0), d_final_state=d_final, cu_seqlens=cu)
+    assert torch.equal(torch.isfinite(dx), want) and torch.equal(torch.isfinite(dg), want)
+    assert not torch.isfinite(ds[0, 1, 3]) and torch.isfinite(ds).sum() == ds.numel() - 1

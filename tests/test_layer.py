@@ -141,6 +141,14 @@ def test_where_sequences_begin(tmp_path):
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
 
 
+def test_workspace_of_a_single_tile():
+    """A shape that is served has a workspace to ask for, the smallest among them."""
+    for T in (1, 16, 17):
+        for logits in (True, False):
+            assert kda.glr_fwd_workspace_size(1, T, 1, 8) > 0 and kda.glr_bwd_workspace_size(1, T, 1, 8, logits, True) > 0
+            assert kda.glr_bwd_workspace_size(1, T, 1, 8, logits, False) > 0
+
+
 def test_python_binding_refuses_cpu_tensors():
     z, w = torch.zeros(1, 4, 2, 16), torch.zeros(32, 4)
     for call in (lambda: kda.short_conv_fwd(z.flatten(2), w), lambda: kda.short_conv_step(z.flatten(2), w, torch.zeros(1, 3, 32)), lambda: kda.glr_fwd(z, z),
