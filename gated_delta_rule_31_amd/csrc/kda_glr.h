@@ -4,7 +4,8 @@
 //   a_t = e^{g_t},   b_t = f_t i_t x_t,    f = sqrt(1 - e^{2g}) or 1,   i = sigmoid(i_t) or 1
 //   h_t = a_t h_{t-1} + b_t
 // A stretch of rows maps the state in front of it to the one behind it as h -> A h + H; a
-// sequence that begins inside it makes A minus zero.  Two stretches joined: (A2 A1, A2 H1 + H2).
+// sequence that begins inside it makes A minus zero.  Two stretches joined: (A2 A1, A2 H1 + H2), or, where a sequence
+// begins in either, A minus zero: as a product the mark would be lost to a second one (-0 x -0 = +0) and to a NaN.
 // Where A is minus zero the state in front is not looked at, so nothing of one sequence reaches another,
 // infinities and NaN among it; where decays alone made it zero (plus zero: they are not negative) it
 // is, so that an infinity or a NaN of a sequence is not forgotten by it.
@@ -65,7 +66,10 @@ __device__ __forceinline__ Gate make_gate(float z, float in, float scale2, float
 }
 
 constexpr float CUT = -0.f;  // the A of a stretch in which a sequence begins
-__device__ __forceinline__ float join(float a, float h, float before) { return __float_as_uint(a) == 0x80000000u ? h : fmaf(a, before, h); }
+__host__ __device__ __forceinline__ bool is_cut(float a) { return __builtin_bit_cast(uint32_t, a) == 0x80000000u; }
+// The state behind a stretch from the one in front of it, and the A of two stretches one behind the other.
+__host__ __device__ __forceinline__ float join(float a, float h, float before) { return is_cut(a) ? h : fmaf(a, before, h); }
+__host__ __device__ __forceinline__ float both(float a, float b) { return is_cut(a) || is_cut(b) ? CUT : a * b; }
 
 // The types of a call: x and the logits are T, log decays float32.
 template <typename T, bool LOGITS>

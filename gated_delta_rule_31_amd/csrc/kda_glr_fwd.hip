@@ -138,7 +138,7 @@ __global__ __launch_bounds__(CARRY_T) void glr_carry_kernel(const float *words, 
 #pragma unroll
         for (int u = 0; u < CARRY_U; ++u) {
             H = join(a[u], h[u], H);
-            A *= a[u];
+            A = both(A, a[u]);
         }
     }
 #pragma unroll
@@ -146,7 +146,7 @@ __global__ __launch_bounds__(CARRY_T) void glr_carry_kernel(const float *words, 
         const float pa = __shfl_up(A, d), ph = __shfl_up(H, d);
         if (lane >= d) {
             H = join(A, H, ph);
-            A *= pa;
+            A = both(A, pa);
         }
     }
     if (lane >= 64 - CARRY_C) {

@@ -354,3 +354,45 @@ def test_scan_does_not_forget_what_is_not_finite(bad, T):
     dx, dg, _, _, _, ds = kda.glr_bwd(x, gate, torch.ones_like(x), initial_state=torch.zeros_like(s0), d_final_state=d_final, cu_seqlens=cu)
     assert torch.equal(torch.isfinite(dx), want) and torch.equal(torch.isfinite(dg), want)
     assert not torch.isfinite(ds[0, 1, 3]) and torch.isfinite(ds).sum() == ds.numel() - 1
+
+
+@pytest.mark.parametrize("lens,H,K", [([20] * 6, 2, 4), ([20] * 10, 2, 4), ([12] * 20, 3, 5), ([37] * 70, 1, 8), ([37] * 30, 4, 258)])
+@pytest.mark.parametrize("logits", [True, False])
+def test_no_sequence_reaches_another_over_tiles(lens, H, K, logits):
+    """What is not finite in one input of one sequence changes no bit of any other, forward or backward: several
+    beginnings in tiles of their own on both sides of it, 15 tiles (joined by their readers) and more (joined by a pass over
+    them, some with several tiles to a group of lanes, some with more than 1024 channels)."""
+    N, T = len(lens), sum(lens)
+    x, z, ls, b, i, s = scan_case(lens, True, H, K, F32, logits, True, True, 80)
+    r = gen(81)
+    data = dict(x=x, gate=z, in_gate=i, initial_state=s, d_out=r(*x.shape), d_final_state=r(N, H, K))
+    cu, ls, b = gpu(offsets(lens)), gpu(ls), gpu(b)
+
+    def run(x, gate, in_gate, initial_state, d_out, d_final_state):
+        kw = dict(log_scale=ls, bias=b, in_gate=in_gate, initial_state=initial_state, cu_seqlens=cu)
+        out, final, kept = kda.glr_fwd(x, gate, keep=True, **kw)
+        dx, dg, di, _, _, ds = kda.glr_bwd(x, gate, d_out, d_final_state=d_final_state, kept=kept, **kw)
+        return [out, dx, dg, di], [final, ds]
+
+    data = {k: gpu(v) for k, v in data.items()}
+    rows, states = run(**data)
+    for n in (0, N // 3, N // 2, N - 1):
+        at = offsets(lens)[n].item()
+        mine = torch.zeros(T, dtype=torch.bool, device="cuda")
+        mine[at : at + lens[n]] = True
+        others = torch.arange(N, device="cuda") != n
+        for what, bad in [(k, v) for k in data for v in (float("nan"), float("inf")) if k != "gate" or v != v]:
+            new = {k: v.clone() for k, v in data.items()}
+            if what in ("initial_state", "d_final_state"):
+                new[what][n] = bad
+            else:
+                new[what][0, at + 5] = bad
+            got_rows, got_states = run(**new)
+            for k, (u, v) in enumerate(zip(got_rows, rows)):
+                assert torch.equal(u[:, ~mine], v[:, ~mine]), (n, what, bad, k)
+            for k, (u, v) in enumerate(zip(got_states, states)):
+                assert torch.equal(u[others], v[others]), (n, what, bad, k)
+            # the sigmoid of an infinite input gate is 1
+            back = what in ("d_out", "d_final_state")
+            if (what, bad) != ("in_gate", float("inf")):
+                assert not torch.isfinite((got_rows[1] if back else got_rows[0])[:, mine]).all(), (n, what, bad)

@@ -198,3 +198,12 @@ def test_reference_gradients():
     assert torch.autograd.gradcheck(lambda x, w, b, s: ref.conv(x, w, b, s, lens, True), (r(1, 4, 2), r(2, 3), r(2), r(3, 2, 2)))
     assert torch.autograd.gradcheck(lambda x, z, a, b, i, s: ref.scan(x, z, a, b, i, s, lens, True), (r(1, 4, 2, 2), r(1, 4, 2, 2), r(2), r(2, 2), r(1, 4, 2, 2), r(3, 2, 2)))
     assert torch.autograd.gradcheck(lambda y, z, x, a, b: ref.block_norm(y, z, x, a, b, True, True, 0.5, 1e-6, True), (r(2, 5), r(2, 5), r(2, 5), r(5), r(5)))
+
+
+def test_stretches_of_tiles_keep_their_beginnings(tmp_path):
+    """The device's own joining of tiles, in the order of its pass over them, compiled for the host."""
+    exe = str(tmp_path / "carry")
+    here = os.path.dirname(os.path.abspath(__file__))
+    subprocess.run([HIPCC, "--offload-host-only", "-O1", "-std=c++17", os.path.join(here, "layer_carry_check.hip"), "-o", exe], check=True, capture_output=True, timeout=300)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
