@@ -190,7 +190,9 @@ __global__ __launch_bounds__(64 * WAVES) void glr_bwd_kernel(const GlrArgs a, in
                         const float t = lam * gv[u][i];
                         oz.set(i, t);
                         if constexpr (LOGITS) {
-                            u_sum[i] = fmaf(fmaf(k.scale2[i], rz[u].get(i), k.bias2[i]), t, u_sum[i]);
+                            // u of a logit far out may be infinite, where t is 0 and their product's limit is: held in range
+                            const float far = __builtin_amdgcn_fmed3f(fmaf(k.scale2[i], rz[u].get(i), k.bias2[i]), -3e38f, 3e38f);
+                            u_sum[i] = fmaf(far, t, u_sum[i]);
                             dz_sum[i] += t;
                         }
                     }

@@ -542,7 +542,7 @@ kda_status kda_glr_fwd(const void *x, int64_t x_stride, kda_dtype dtype, const v
  *   d_log_scale [H], d_bias [H K] float32 or NULL, d_initial_state [N, H, K] float32 or NULL
  * from d_out [B, T, H, K] in dtype and d_final_state [N, H, K] float32 or NULL (zeros).  kept: what the
  * forward kept, or NULL (made again from the inputs).  Where alpha is 1 the derivative of
- * sqrt(1 - alpha^2), which has none there, counts as 0.
+ * sqrt(1 - alpha^2), which has none there, counts as 0.  Infinite logits have the gradients of large ones (0).
  */
 size_t kda_glr_bwd_workspace_size(int B, int64_t T, int H, int K, int logits, int kept);
 kda_status kda_glr_bwd(const void *x, int64_t x_stride, kda_dtype dtype, const void *gate, int64_t gate_stride, const float *log_scale,

@@ -396,3 +396,48 @@ def test_no_sequence_reaches_another_over_tiles(lens, H, K, logits):
             back = what in ("d_out", "d_final_state")
             if (what, bad) != ("in_gate", float("inf")):
                 assert not torch.isfinite((got_rows[1] if back else got_rows[0])[:, mine]).all(), (n, what, bad)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("infinite", [False, True])
+def test_scan_masked_logits(dtype, sign, infinite):
+    """Logits at the end of their type's range, or infinite: the sigmoid is 0 or 1, what they add to a gradient 0 (the limit of u du
+    for infinite ones; the 64-bit form has it at the type's largest number).  d log_scale is a sum of 45 x 12 terms, of which those
+    of these logits are 0; tolerances as in test_scan, whose decays these are but for alpha = 1."""
+    lens, H, K = [30, 0, 15], 2, 12
+    x, z, ls, b, i, s = scan_case(lens, True, H, K, dtype, True, True, True, 82)
+    far = sign * torch.finfo(dtype).max
+    for at in (0, 7, 29, 30, 44):
+        z[0, at, at % 2, 3 : 3 + at % 5] = far
+    zs = z.clone()
+    if infinite:
+        zs[z == far] = sign * float("inf")
+    d_out, d_fin = gen(83)(*x.shape).to(dtype), gen(84)(3, H, K)
+    cu = gpu(offsets(lens))
+    kw = dict(log_scale=gpu(ls), bias=gpu(b), in_gate=gpu(i), initial_state=gpu(s), cu_seqlens=cu)
+    out, fin = kda.glr_fwd(gpu(x), gpu(zs), **kw)
+    want, want_fin = ref.scan(f64(x), f64(z), f64(ls), f64(b), f64(i), f64(s), lens, True)
+    close(out, want, 512, "out")
+    close(fin, want_fin, 512, "final")
+    got = kda.glr_bwd(gpu(x), gpu(zs), gpu(d_out), d_final_state=gpu(d_fin), **kw)
+    assert all(torch.isfinite(g).all() for g in got)
+    assert not got[1][gpu(z) == far].any()
+    # the formula's gradient, its own rows with alpha = 1 left out (the root has no derivative there, which counts as 0)
+    g = ref.decay(f64(z), f64(ls), f64(b))
+    a, f, gi = torch.exp(g), torch.sqrt(-torch.expm1(2 * g)), torch.sigmoid(f64(i))
+    lam, before = torch.zeros(45, H, K).double(), torch.zeros(45, H, K).double()
+    for first, last, n in ((0, 30, 0), (30, 45, 2)):
+        h, m = f64(s)[n], f64(d_fin)[n]
+        for t in range(first, last):
+            before[t] = h
+            h = a[0, t] * h + (f * gi * f64(x))[0, t]
+        for t in reversed(range(first, last)):
+            lam[t] = f64(d_out)[0, t] + m
+            m = a[0, t] * lam[t]
+    dg = lam * (a[0] * before - torch.where(f > 0, gi * f64(x) * a * a / f.clamp_min(1e-300), 0 * f)[0])
+    u = torch.exp(f64(ls))[:, None] * (f64(z) + f64(b))
+    du = dg * (-5 * torch.sigmoid(u) * torch.sigmoid(-u))[0]
+    terms = (du * u[0].clamp(-40, 40)).pow(2).sum().sqrt()
+    assert float((f64(got[3]) - (du * u[0]).sum((0, 2))).abs().max()) <= (6 * 1024 + 4 * (45 * K) ** 0.5) * 2.0 ** -24 * max(1.0, float(terms))
+    close(got[4], (du * torch.exp(f64(ls))[:, None]).sum(0), 6 * 1024 + 4 * 45 ** 0.5, "d bias", 1.0)
