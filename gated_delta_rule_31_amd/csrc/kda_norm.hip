@@ -271,7 +271,7 @@ __global__ __launch_bounds__(THREADS<LANES>) void norm_bwd_kernel(const NormArgs
         for (int k = 0; k < NV; ++k) {
             Raw<T, VEC> o;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) o.set(i, r * fmaf(-back, y[k].get(i), dp[k][i]));
+            for (int i = 0; i < VEC; ++i) o.set(i, a.after ? r * fmaf(-back, y[k].get(i), dp[k][i]) : dp[k][i]);  // without the norm no y, which may be infinite
             store_row<LANES>(o, a.dy, at, k, lane, vecs);
         }
     }

@@ -441,3 +441,19 @@ def test_scan_masked_logits(dtype, sign, infinite):
     terms = (du * u[0].clamp(-40, 40)).pow(2).sum().sqrt()
     assert float((f64(got[3]) - (du * u[0]).sum((0, 2))).abs().max()) <= (6 * 1024 + 4 * (45 * K) ** 0.5) * 2.0 ** -24 * max(1.0, float(terms))
     close(got[4], (du * torch.exp(f64(ls))[:, None]).sum(0), 6 * 1024 + 4 * 45 ** 0.5, "d bias", 1.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [8, 33, 264, 4104, 16384])
+@pytest.mark.parametrize("gate", [False, True])
+def test_norm_gradient_without_norm_after_is_not_of_y(dtype, D, gate):
+    """h = scale sigmoid(gate) y: the gradient of y is scale sigmoid(gate) d_h, whatever y holds; each product and the sigmoid's three
+    operations round once, and the result to its type."""
+    r = gen(85)
+    y, z, d = r(6, D).to(dtype), r(6, D).to(dtype) if gate else None, r(6, D).to(dtype)
+    y[1, D // 2], y[3, 0], y[4, D - 1] = float("inf"), -float("inf"), float("nan")
+    dy, dz, dr, _, _ = kda.block_norm_bwd(gpu(y), gpu(d), gate=gpu(z), norm_after=False, norm_before=False, scale=0.5)
+    close(dy, 0.5 * f64(d) * (torch.sigmoid(f64(z)) if gate else 1), 16, "dy")
+    assert torch.equal(dr, gpu(d))
+    if gate:  # of y itself, its own number alone
+        assert torch.equal(torch.isfinite(dz), torch.isfinite(gpu(y)))
