@@ -1,6 +1,8 @@
 // kda_rows_api.hip -- the C entry points of what stands around the recurrence in a layer (the short
 // convolution, the gated linear recurrence, the norms between blocks): argument validation, the
 // empty cases, workspaces.
+#include <initializer_list>
+
 #include "../../include/kda.h"
 #include "kda_rows.h"
 
@@ -28,7 +30,12 @@ struct Units {
         return *this;
     }
 };
-bool misaligned(const void *p, size_t size) { return (uintptr_t)p % size != 0; }
+// Whether any of them is off a border of `size` bytes; looked at before a call without rows returns, which fills outputs too.
+bool misaligned(size_t size, std::initializer_list<const void *> ps) {
+    for (const void *p : ps)
+        if ((uintptr_t)p % size != 0) return true;
+    return false;
+}
 
 // No output may be an input or another output.
 template <int I, int O>
@@ -138,13 +145,12 @@ kda_status kda_short_conv_fwd(const void *x, int64_t x_stride, kda_dtype dtype, 
     if (st != KDA_OK) return st;
     if (x_stride < D) return KDA_ERR_BAD_SHAPE;
     if (final_state && final_state == initial_state) return KDA_ERR_ALIAS;
+    if (misaligned(size_of(dtype), {x, initial_state, final_state, out}) || misaligned(4, {weight, bias, cu_seqlens})) return KDA_ERR_BAD_ARGUMENT;
     if (empty) return fill(final_state, initial_state, (int64_t)a.seqs.N * (W - 1) * D, size_of(dtype), stream);
     if (!conv_fits(a.seqs, D, W)) return KDA_ERR_UNSUPPORTED;
     if (!x || !weight || !out) return KDA_ERR_NULL_POINTER;
     const void *ins[] = {x, weight, bias, initial_state, cu_seqlens}, *outs[] = {out, final_state};
     if (aliased(ins, outs)) return KDA_ERR_ALIAS;
-    for (const void *p : {x, initial_state, (const void *)final_state, (const void *)out})
-        if (misaligned(p, size_of(dtype))) return KDA_ERR_BAD_ARGUMENT;
     a.x = x;
     a.x_stride = x_stride;
     a.weight = weight;
@@ -184,6 +190,9 @@ kda_status kda_short_conv_bwd(const void *x, int64_t x_stride, kda_dtype dtype, 
     if (st != KDA_OK) return st;
     if (x_stride < D) return KDA_ERR_BAD_SHAPE;
     if (d_initial_state && d_initial_state == d_final_state) return KDA_ERR_ALIAS;
+    if (misaligned(size_of(dtype), {x, initial_state, d_out, d_final_state, dx, d_initial_state}) ||
+        misaligned(4, {weight, bias, cu_seqlens, d_weight, d_bias}))
+        return KDA_ERR_BAD_ARGUMENT;
     if (empty) {
         st = fill(d_weight, nullptr, (int64_t)D * W, sizeof(float), stream);
         if (st == KDA_OK) st = fill(d_bias, nullptr, D, sizeof(float), stream);
@@ -196,9 +205,7 @@ kda_status kda_short_conv_bwd(const void *x, int64_t x_stride, kda_dtype dtype, 
     const void *ins[] = {x, weight, bias, initial_state, cu_seqlens, d_out, d_final_state};
     const void *outs[] = {dx, d_weight, d_bias, d_initial_state, workspace};
     if (aliased(ins, outs)) return KDA_ERR_ALIAS;
-    for (const void *p : {x, initial_state, d_out, d_final_state, (const void *)dx, (const void *)d_initial_state})
-        if (misaligned(p, size_of(dtype))) return KDA_ERR_BAD_ARGUMENT;
-    if (sums && (misaligned(workspace, 16) || workspace_bytes < kda_short_conv_bwd_workspace_size(dtype, B, T, D, W))) return KDA_ERR_BAD_ARGUMENT;
+    if (sums && (misaligned(16, {workspace}) || workspace_bytes < kda_short_conv_bwd_workspace_size(dtype, B, T, D, W))) return KDA_ERR_BAD_ARGUMENT;
     a.x = x;
     a.x_stride = x_stride;
     a.weight = weight;
@@ -232,8 +239,7 @@ kda_status kda_short_conv_step(const void *x, kda_dtype dtype, const float *weig
     if (!x || !weight || !states || !out) return KDA_ERR_NULL_POINTER;
     const void *ins[] = {x, weight, bias, slots, start, lengths}, *outs[] = {states, out};
     if (aliased(ins, outs)) return KDA_ERR_ALIAS;
-    for (const void *p : {x, (const void *)states, (const void *)out})
-        if (misaligned(p, size_of(dtype))) return KDA_ERR_BAD_ARGUMENT;
+    if (misaligned(size_of(dtype), {x, states, out}) || misaligned(4, {weight, bias, slots, start, lengths})) return KDA_ERR_BAD_ARGUMENT;
     a.x = x;
     a.weight = weight;
     a.bias = bias;
@@ -290,24 +296,23 @@ kda_status kda_glr_fwd(const void *x, int64_t x_stride, kda_dtype dtype, const v
     const int C = a.C = H * K;
     if (x_stride < C || gate_stride < C || (in_gate && in_stride < C)) return KDA_ERR_BAD_SHAPE;
     if (final_state && final_state == initial_state) return KDA_ERR_ALIAS;
+    const size_t e = size_of(dtype), gate_size = log_scale ? e : 4;
+    if (misaligned(e, {x, in_gate, out}) || misaligned(gate_size, {gate}) ||
+        misaligned(4, {log_scale, bias, initial_state, final_state, cu_seqlens, kept}))
+        return KDA_ERR_BAD_ARGUMENT;
     if (empty) return fill(final_state, initial_state, (int64_t)a.seqs.N * C, sizeof(float), stream);
     if (!glr_fits(a.seqs, C)) return KDA_ERR_UNSUPPORTED;
     if (!x || !gate || !out || !workspace) return KDA_ERR_NULL_POINTER;
     const void *ins[] = {x, gate, log_scale, bias, in_gate, initial_state, cu_seqlens}, *outs[] = {out, final_state, kept, workspace};
     if (aliased(ins, outs)) return KDA_ERR_ALIAS;
-    const size_t gate_size = log_scale ? size_of(dtype) : 4;
-    if (misaligned(x, size_of(dtype)) || misaligned(in_gate, size_of(dtype)) || misaligned(out, size_of(dtype)) || misaligned(gate, gate_size) ||
-        misaligned(workspace, 16))
-        return KDA_ERR_BAD_ARGUMENT;
     a.x = x;
     a.x_stride = x_stride;
     a.s0 = initial_state;
     a.sf = final_state;
     a.out = out;
     a.kept = kept;
-    if (workspace_bytes < kda_glr_fwd_workspace_size(B, T, H, K)) return KDA_ERR_BAD_ARGUMENT;
+    if (misaligned(16, {workspace}) || workspace_bytes < kda_glr_fwd_workspace_size(B, T, H, K)) return KDA_ERR_BAD_ARGUMENT;
     kda::carve_glr_fwd(a, workspace);
-    const size_t e = size_of(dtype);
     Units w{2};
     w.rows(x, e, x_stride).rows(gate, gate_size, gate_stride).rows(in_gate, e, in_stride).rows(out, e, C);
     w.rows(initial_state, 4, C).rows(final_state, 4, C).rows(kept, 4, C);
@@ -331,6 +336,10 @@ kda_status kda_glr_bwd(const void *x, int64_t x_stride, kda_dtype dtype, const v
     if (x_stride < C || gate_stride < C || (in_gate && in_stride < C)) return KDA_ERR_BAD_SHAPE;
     if (!log_scale && (d_log_scale || d_bias)) return KDA_ERR_BAD_ARGUMENT;
     if (d_initial_state && d_initial_state == d_final_state) return KDA_ERR_ALIAS;
+    const size_t e = size_of(dtype), gate_size = log_scale ? e : 4;
+    if (misaligned(e, {x, in_gate, d_out, dx, d_in_gate}) || misaligned(gate_size, {gate, d_gate}) ||
+        misaligned(4, {log_scale, bias, initial_state, cu_seqlens, kept, d_final_state, d_log_scale, d_bias, d_initial_state}))
+        return KDA_ERR_BAD_ARGUMENT;
     if (empty) {
         st = fill(d_log_scale, nullptr, H, sizeof(float), stream);
         if (st == KDA_OK) st = fill(d_bias, nullptr, C, sizeof(float), stream);
@@ -341,10 +350,6 @@ kda_status kda_glr_bwd(const void *x, int64_t x_stride, kda_dtype dtype, const v
     const void *ins[] = {x, gate, log_scale, bias, in_gate, initial_state, cu_seqlens, kept, d_out, d_final_state};
     const void *outs[] = {dx, d_gate, in_gate ? d_in_gate : nullptr, d_log_scale, d_bias, d_initial_state, workspace};
     if (aliased(ins, outs)) return KDA_ERR_ALIAS;
-    const size_t e = size_of(dtype), gate_size = log_scale ? e : 4;
-    for (const void *p : {x, in_gate, d_out, (const void *)dx, (const void *)d_in_gate})
-        if (misaligned(p, e)) return KDA_ERR_BAD_ARGUMENT;
-    if (misaligned(gate, gate_size) || misaligned(d_gate, gate_size) || misaligned(workspace, 16)) return KDA_ERR_BAD_ARGUMENT;
     a.x = x;
     a.x_stride = x_stride;
     a.s0 = initial_state;
@@ -356,7 +361,7 @@ kda_status kda_glr_bwd(const void *x, int64_t x_stride, kda_dtype dtype, const v
     a.d_in = d_in_gate;
     a.ds0 = d_initial_state;
     float *sums;
-    if (workspace_bytes < kda_glr_bwd_workspace_size(B, T, H, K, log_scale != nullptr, kept != nullptr)) return KDA_ERR_BAD_ARGUMENT;
+    if (misaligned(16, {workspace}) || workspace_bytes < kda_glr_bwd_workspace_size(B, T, H, K, log_scale != nullptr, kept != nullptr)) return KDA_ERR_BAD_ARGUMENT;
     kda::carve_glr_bwd(a, workspace, kept != nullptr, sums);
     if (!d_log_scale && !d_bias) a.part = nullptr;
     Units w{2};
@@ -382,7 +387,8 @@ kda_status kda_glr_step(const void *x, kda_dtype dtype, const void *gate, const 
     const void *ins[] = {x, gate, log_scale, bias, in_gate, slots, start, lengths}, *outs[] = {states, out};
     if (aliased(ins, outs)) return KDA_ERR_ALIAS;
     const size_t e = size_of(dtype), gate_size = log_scale ? e : 4;
-    if (misaligned(x, e) || misaligned(in_gate, e) || misaligned(out, e) || misaligned(gate, gate_size)) return KDA_ERR_BAD_ARGUMENT;
+    if (misaligned(e, {x, in_gate, out}) || misaligned(gate_size, {gate}) || misaligned(4, {log_scale, bias, states, slots, start, lengths}))
+        return KDA_ERR_BAD_ARGUMENT;
     a.x = x;
     a.states = states;
     a.B = B;
@@ -401,12 +407,12 @@ kda_status kda_block_norm_fwd(const void *y, const void *gate, int64_t gate_stri
     const bool before = (flags & KDA_NORM_BEFORE) != 0, after = (flags & KDA_NORM_AFTER) != 0;
     if ((weight_after && !after) || (weight_before && !before)) return KDA_ERR_BAD_ARGUMENT;
     if (gate && (gate_stride < D || (heads > 1 && gate_head_stride < D))) return KDA_ERR_BAD_SHAPE;
+    const size_t e = size_of(dtype), he = size_of(h_dtype);
+    if (misaligned(e, {y, gate, before ? n : nullptr}) || misaligned(he, {residual, h}) || misaligned(4, {weight_after, weight_before})) return KDA_ERR_BAD_ARGUMENT;
     if (tokens == 0) return KDA_OK;
     if (!y || !h || (before && !n)) return KDA_ERR_NULL_POINTER;
     const void *ins[] = {y, gate, residual, weight_after, weight_before}, *outs[] = {h, before ? n : nullptr};
     if (aliased(ins, outs)) return KDA_ERR_ALIAS;
-    const size_t e = size_of(dtype), he = size_of(h_dtype);
-    if (misaligned(y, e) || misaligned(gate, e) || misaligned(residual, he) || misaligned(h, he) || (before && misaligned(n, e))) return KDA_ERR_BAD_ARGUMENT;
     kda::NormArgs a{};
     a.y = y;
     a.gate = gate;
@@ -448,6 +454,10 @@ kda_status kda_block_norm_bwd(const void *y, const void *gate, int64_t gate_stri
     const bool before = (flags & KDA_NORM_BEFORE) != 0, after = (flags & KDA_NORM_AFTER) != 0;
     if ((!after && (weight_after || d_weight_after)) || (!before && (weight_before || d_weight_before))) return KDA_ERR_BAD_ARGUMENT;
     if (gate && (gate_stride < D || (heads > 1 && gate_head_stride < D))) return KDA_ERR_BAD_SHAPE;
+    const size_t e = size_of(dtype), he = size_of(h_dtype);
+    if (misaligned(e, {y, gate, dy, gate ? d_gate : nullptr, before ? d_n : nullptr}) || misaligned(he, {d_h, before ? h : nullptr, before ? d_residual : nullptr}) ||
+        misaligned(4, {weight_after, weight_before, d_weight_after, d_weight_before}))
+        return KDA_ERR_BAD_ARGUMENT;
     if (tokens == 0) {
         st = fill(d_weight_after, nullptr, D, sizeof(float), stream);
         return st == KDA_OK ? fill(d_weight_before, nullptr, D, sizeof(float), stream) : st;
@@ -457,10 +467,7 @@ kda_status kda_block_norm_bwd(const void *y, const void *gate, int64_t gate_stri
     const void *ins[] = {y, gate, before ? h : nullptr, weight_after, weight_before, d_h, before ? d_n : nullptr};
     const void *outs[] = {dy, gate ? d_gate : nullptr, before ? d_residual : nullptr, d_weight_after, d_weight_before, workspace};
     if (aliased(ins, outs)) return KDA_ERR_ALIAS;
-    const size_t e = size_of(dtype), he = size_of(h_dtype);
-    if (misaligned(y, e) || misaligned(gate, e) || misaligned(d_h, he) || misaligned(dy, e) || (gate && misaligned(d_gate, e))) return KDA_ERR_BAD_ARGUMENT;
-    if (before && (misaligned(h, he) || misaligned(d_n, e) || misaligned(d_residual, he))) return KDA_ERR_BAD_ARGUMENT;
-    if (sums && (misaligned(workspace, 16) || workspace_bytes < kda_block_norm_bwd_workspace_size(tokens, heads, D))) return KDA_ERR_BAD_ARGUMENT;
+    if (sums && (misaligned(16, {workspace}) || workspace_bytes < kda_block_norm_bwd_workspace_size(tokens, heads, D))) return KDA_ERR_BAD_ARGUMENT;
     kda::NormArgs a{};
     a.y = y;
     a.gate = gate;

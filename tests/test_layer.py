@@ -207,3 +207,42 @@ def test_stretches_of_tiles_keep_their_beginnings(tmp_path):
     subprocess.run([HIPCC, "--offload-host-only", "-O1", "-std=c++17", os.path.join(here, "layer_carry_check.hip"), "-o", exe], check=True, capture_output=True, timeout=300)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
+
+
+# Float32 and int32 pointers off a 4-byte border, in calls with rows and without
+FLOATS = {
+    "conv": (_conv, dict(w=0x2002, b=0x3001, cu=0x902), dict(T=0)), "conv_states": (_conv, dict(s0=0x9002, sf=0xa002), dict(T=0)),
+    "conv_bwd": (_conv_bwd, dict(w=0x2002, b=0x3002, cu=0x901, dw=0x6002, db=0x7002), dict(T=0)),
+    "conv_bwd_states": (_conv_bwd, dict(s0=0x9002, dsf=0xa002, ds0=0xb002), dict(T=0)),
+    "glr": (_glr, dict(ls=0x3002, b=0x4001, s0=0x9002, sf=0xa002, cu=0x902, kept=0xb002), dict(T=0)),
+    "glr_bwd": (_glr_bwd, dict(ls=0x3002, b=0x4002, s0=0x9002, cu=0x902, kept=0x6002, dsf=0xe002, dls=0xb002, db=0xc002, ds0=0xf002), dict(T=0)),
+    "norm": (_norm, dict(wa=0x4002, wb=0x5001), dict(n=0)), "norm_bwd": (_norm_bwd, dict(wa=0x4002, wb=0x5002, dwa=0xb002, dwb=0xc001), dict(n=0))}
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c in FLOATS for n in FLOATS[c][1]])
+def test_float_pointers_off_a_border(lib, call, name):
+    fn, off, empty = FLOATS[call]
+    kw = {name: off[name]}
+    if name == "cu":
+        kw["N"] = 1
+    if call.endswith("states"):
+        kw["dt"] = 0
+    assert fn(lib, **kw) == 5 and fn(lib, **kw, **empty) == 5
+
+
+@pytest.mark.parametrize("which", ["conv", "glr"])
+@pytest.mark.parametrize("kw", [dict(slots=0x902), dict(start=0x802), dict(lens=0x801), dict(st=0x6002, dt=0)])
+def test_step_pointers_off_a_border(lib, which, kw):
+    assert _steps(lib, which, **kw) == 5
+
+
+@pytest.mark.parametrize("kw", [dict(ls=0x3002), dict(b=0x4002), dict(st=0x6002)])
+def test_glr_step_pointers_off_a_border(lib, kw):
+    arg = dict(ls=0x3000, b=0x4000, st=0x6000)
+    arg.update(kw)
+    assert lib.kda_glr_step(0x1000, 1, 0x2000, arg["ls"], arg["b"], -5.0, 0x5000, 1, arg["st"], 8, 0x900, 3, None, None, 2, 3, 1, 32, 0x7000, None) == 5
+
+
+@pytest.mark.parametrize("w,b", [(0x2002, 0x3000), (0x2000, 0x3002)])
+def test_conv_step_pointers_off_a_border(lib, w, b):
+    assert lib.kda_short_conv_step(0x1000, 1, w, b, 0x6000, 8, 0x900, 3, None, None, 2, 3, 32, 4, 8, 0x7000, None) == 5
