@@ -46,6 +46,7 @@ import os
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 __all__ = ["bounded_decay", "chunk_fwd", "recurrent_step", "recurrent_kda", "KDAError", "chunk_fwd_supported",
            "chunk_fwd_fused_gate", "recurrent_step_fused_gate", "recurrent_fwd", "recurrent_fwd_fused_gate",
@@ -235,11 +236,28 @@ def _dtype_code(t: torch.dtype) -> int:
     raise ValueError("unsupported dtype %s (float32 or bfloat16)" % t)
 
 
+class _AnyLevel:
+    _current_level = 0
+
+
+# whether a forward-mode level is open is one attribute, looked at in place: a call has up to ten tensors to check
+_forward = forward_ad if hasattr(forward_ad, "_current_level") else _AnyLevel
+
+
+def _no_tangent(x: torch.Tensor, name: str) -> None:
+    """Forward-mode derivatives are not computed, by no call: a dual tensor would lose its tangent without a word.
+    (Recorded calls never come here with one: torch refuses it, as they have no rule for it.)"""
+    if forward_ad.unpack_dual(x).tangent is not None:
+        raise ValueError("%s carries a forward-mode tangent: forward-mode derivatives are not supported" % name)
+
+
 def _dev(x: Optional[torch.Tensor], name: str, dtype=None) -> Optional[torch.Tensor]:
     if x is None:
         return None
     if not isinstance(x, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
+    if _forward._current_level >= 0:
+        _no_tangent(x, name)
     if x.device.type != "cuda":
         raise ValueError("%s must be on the GPU (got %s)" % (name, x.device))
     if x.requires_grad and torch.is_grad_enabled():
@@ -494,6 +512,8 @@ def _step_common(q, k, v, beta, state, out_dtype, out, state_vk: bool = False):
     if not isinstance(state, torch.Tensor) or state.device.type != "cuda" or state.dtype != torch.float32 \
             or not state.is_contiguous():
         raise ValueError("state must be a contiguous float32 GPU tensor (it is updated in place)")
+    if _forward._current_level >= 0:
+        _no_tangent(state, "state")
     if q.dim() != 3:
         raise ValueError("q must be [B, H, K]")
     B, H, K = q.shape

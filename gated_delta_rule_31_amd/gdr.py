@@ -18,7 +18,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _check, _dtype_code, _load, _needs_grad
+from . import _check, _dtype_code, _forward, _load, _needs_grad, _no_tangent
 
 
 def _input(x: Optional[torch.Tensor], name: str, like: Optional[torch.Tensor] = None, dtype=None, border: int = 16) -> Optional[torch.Tensor]:
@@ -28,6 +28,8 @@ def _input(x: Optional[torch.Tensor], name: str, like: Optional[torch.Tensor] = 
         return None
     if not isinstance(x, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
+    if _forward._current_level >= 0:
+        _no_tangent(x, name)
     if like is None:
         if not x.is_cuda:
             raise ValueError("%s must be on the GPU (got %s)" % (name, x.device))
@@ -66,6 +68,8 @@ def _output(x: torch.Tensor, name: str, shape, dtype, device) -> torch.Tensor:
     if (not isinstance(x, torch.Tensor) or tuple(x.shape) != tuple(shape) or x.dtype != dtype or x.device != device
             or not x.is_contiguous()):
         raise ValueError("%s must be a contiguous %s tensor %s on %s" % (name, dtype, list(shape), device))
+    if _forward._current_level >= 0:
+        _no_tangent(x, name)
     if x.requires_grad and torch.is_grad_enabled():
         raise ValueError("%s requires grad: it is written in place" % name)
     return x

@@ -457,3 +457,23 @@ def test_norm_gradient_without_norm_after_is_not_of_y(dtype, D, gate):
     assert torch.equal(dr, gpu(d))
     if gate:  # of y itself, its own number alone
         assert torch.equal(torch.isfinite(dz), torch.isfinite(gpu(y)))
+
+
+def test_forward_mode_is_refused_by_every_input():
+    """Weights, gates, states and buffers with a tangent, and recorded calls with one beside a leaf that requires grad."""
+    from torch.autograd import forward_ad
+    dual = lambda t: forward_ad.make_dual(t, torch.ones_like(t))  # noqa: E731
+    x, X, w, ls, s = (torch.zeros(*n, device="cuda") for n in ((1, 4, 32), (1, 4, 2, 16), (32, 4), (2,), (1, 2, 16)))
+    leaf, Leaf = x.clone().requires_grad_(), X.clone().requires_grad_()
+    with forward_ad.dual_level():
+        for call in (lambda: kda.short_conv(x, dual(w)), lambda: kda.short_conv_step(x, w, dual(torch.zeros(1, 3, 32, device="cuda"))), lambda: kda.glr_fwd(X, dual(X)),
+                     lambda: kda.glr_fwd(X, X, ls, initial_state=dual(s)), lambda: kda.glr_fwd(X, X, in_gate=dual(X)[..., :8]), lambda: kda.glr_step(X, X, dual(s)),
+                     lambda: kda.block_norm(X, gate=dual(X)), lambda: kda.block_norm(X, residual=dual(X)), lambda: kda.block_norm(X, weight_before=dual(X[0, 0, 0])),
+                     lambda: kda.glr_fwd(X, X, out=dual(X.clone()))):
+            with pytest.raises(ValueError, match="forward-mode tangent"):
+                call()
+        for call in (lambda: kda.short_conv(leaf, dual(w)), lambda: kda.gated_linear_recurrence(Leaf, dual(X)), lambda: kda.block_norm(Leaf, residual=dual(X)),
+                     lambda: kda.gated_norm(dual(Leaf))):
+            with pytest.raises(NotImplementedError):
+                call()
+        assert not kda.short_conv(leaf, w)[0].any() and not kda.block_norm(X)[0].any()  # what has none goes on as before

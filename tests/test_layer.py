@@ -246,3 +246,29 @@ def test_glr_step_pointers_off_a_border(lib, kw):
 @pytest.mark.parametrize("w,b", [(0x2002, 0x3000), (0x2000, 0x3002)])
 def test_conv_step_pointers_off_a_border(lib, w, b):
     assert lib.kda_short_conv_step(0x1000, 1, w, b, 0x6000, 8, 0x900, 3, None, None, 2, 3, 32, 4, 8, 0x7000, None) == 5
+
+
+def test_forward_mode_is_refused():
+    """A dual tensor that does not require grad is refused by every call that would drop its tangent, also without grad mode;
+    outside of its level it is an ordinary tensor."""
+    from torch.autograd import forward_ad
+    plain, w = torch.zeros(1, 4, 2, 16), torch.zeros(32, 4)
+    dual = lambda t: forward_ad.make_dual(t, torch.ones_like(t))  # noqa: E731
+    with forward_ad.dual_level():
+        z = dual(plain)
+        calls = [lambda: kda.short_conv(z.flatten(2), w), lambda: kda.short_conv_fwd(z.flatten(2)[..., 8:24], w), lambda: kda.short_conv_step(z.flatten(2), w, torch.zeros(1, 3, 32)),
+                 lambda: kda.gated_linear_recurrence(z, plain), lambda: kda.glr_fwd(z, plain), lambda: kda.glr_step(z, plain, torch.zeros(1, 2, 16)), lambda: kda.block_norm(z),
+                 lambda: kda.block_norm_fwd(z), lambda: kda.gated_norm(z), lambda: kda.short_conv_bwd(z.flatten(2), w, plain.flatten(2)), lambda: kda.glr_bwd(z, plain, plain),
+                 lambda: kda.block_norm_bwd(z, plain, plain, plain), lambda: kda.gdr_chunk_fwd(z, plain, plain, plain[..., 0], plain[..., 0]),
+                 lambda: kda.gated_delta_rule(z, plain, plain, plain[..., 0], plain[..., 0]), lambda: kda.bounded_decay(z, torch.zeros(2)),
+                 lambda: kda.chunk_fwd(z, plain, plain, plain, plain[..., 0]), lambda: kda.recurrent_fwd(z, plain, plain, plain, plain[..., 0])]
+        for grad in (True, False):
+            with torch.set_grad_enabled(grad):
+                for call in calls:
+                    with pytest.raises(ValueError, match="forward-mode tangent"):
+                        call()
+        for call in (lambda: kda.short_conv_fwd(plain.flatten(2), w), lambda: kda.bounded_decay(plain, torch.zeros(2))):
+            with pytest.raises(ValueError, match="on the GPU"):
+                call()
+    with pytest.raises(ValueError, match="on the GPU"):
+        kda.glr_fwd(z, plain)
