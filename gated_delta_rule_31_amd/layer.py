@@ -183,10 +183,6 @@ def _d(x):
     return None if x is None else x.detach()
 
 
-def _same_type(x, like):
-    return None if x is None else x.to(like.dtype)
-
-
 class _ShortConvFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, initial_state, cu_seqlens, silu):
