@@ -69,6 +69,13 @@ struct Seqs {
             const int u = (int)(b - t0);
             if (u < count) first |= 1ull << u;
             if (u > 0) last |= 1ull << (u - 1);
+            if (cu && at <= N && cu[at] == b) {  // sequences without rows, however many: on to the first offset behind them
+                for (int hi = N + 1; at < hi;) {
+                    const int m = (at + hi) >> 1;
+                    if (cu[m] <= b) at = m + 1;
+                    else hi = m;
+                }
+            }
         }
     }
 };

@@ -477,3 +477,31 @@ def test_forward_mode_is_refused_by_every_input():
             with pytest.raises(NotImplementedError):
                 call()
         assert not kda.short_conv(leaf, w)[0].any() and not kda.block_norm(X)[0].any()  # what has none goes on as before
+
+
+@pytest.mark.parametrize("many", [70, 5000])
+def test_batch_padded_with_empty_sequences(many):
+    """Thousands of sequences without rows, in front, in the middle and at the end, change nothing of the others, and hand their states on."""
+    lens = [37, 100, 1, 62]
+    x, w, b, s = map(gpu, conv_case(lens, True, 20, 4, BF, True, True, 86))
+    X, z, ls, bi, i, s0 = map(gpu, scan_case(lens, True, 2, 10, F32, True, True, True, 87))
+    padded = [0] * many + lens[:2] + [0] * many + lens[2:] + [0] * many
+    real = torch.tensor([k for k, n in enumerate(padded) if n], device="cuda")
+    cu, few = gpu(offsets(padded)), gpu(offsets(lens))
+
+    def spread(t):
+        more = gpu(gen(88)(len(padded), *t.shape[1:]).to(t.dtype))
+        more[real] = t
+        return more
+    s_, s0_ = spread(s), spread(s0)
+    empty = torch.tensor([n == 0 for n in padded], device="cuda")
+    for got, want, handed in (
+            (kda.short_conv_fwd(x, w, b, s_, cu_seqlens=cu), kda.short_conv_fwd(x, w, b, s, cu_seqlens=few), s_),
+            (kda.glr_fwd(X, z, ls, bi, i, initial_state=s0_, cu_seqlens=cu), kda.glr_fwd(X, z, ls, bi, i, initial_state=s0, cu_seqlens=few), s0_)):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1][real], want[1]) and torch.equal(got[1][empty], handed[empty])
+    for got, want, handed in (
+            (kda.short_conv_bwd(x, w, x, b, s_, d_final_state=s_, cu_seqlens=cu), kda.short_conv_bwd(x, w, x, b, s, d_final_state=s, cu_seqlens=few), s_),
+            (kda.glr_bwd(X, z, X, ls, bi, i, initial_state=s0_, d_final_state=s0_, cu_seqlens=cu), kda.glr_bwd(X, z, X, ls, bi, i, initial_state=s0, d_final_state=s0, cu_seqlens=few), s0_)):
+        for u, v in zip(got[:-1], want[:-1]):
+            assert torch.equal(u, v)
+        assert torch.equal(got[-1][real], want[-1]) and torch.equal(got[-1][empty], handed[empty])

@@ -272,3 +272,12 @@ def test_forward_mode_is_refused():
                 call()
     with pytest.raises(ValueError, match="on the GPU"):
         kda.glr_fwd(z, plain)
+
+
+def test_many_sequences_without_rows(tmp_path):
+    """The device's own lookup of where sequences begin, compiled for the host, in batches padded with up to 2^20 empty sequences."""
+    exe = str(tmp_path / "empty")
+    here = os.path.dirname(os.path.abspath(__file__))
+    subprocess.run([HIPCC, "--offload-host-only", "-O1", "-std=c++17", os.path.join(here, "layer_empty_check.hip"), "-o", exe], check=True, capture_output=True, timeout=300)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
