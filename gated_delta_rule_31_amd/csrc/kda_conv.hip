@@ -4,7 +4,7 @@
 // gradients; and decoding over a pool of kept rows.
 //
 // Bound by memory: a row is read and a row written.  A lane owns VEC neighbouring channels (one
-// 16-byte load) and goes through a run of rows with the last W - 1 of them in registers, so a
+// load of a row: two of them forward and in decode, four for gradients, where rows allow it) and goes through a run of rows with the last W - 1 of them in registers, so a
 // row is read once, but for the W - 1 in front of a run.  Where sequences begin and end is the
 // same for all lanes of a wave: two bit masks for a run, looked up once.  W = 4, bf16, a large copy having 5.0 TB/s:
 // 7957 packed rows of 12288 channels 81 us (4.85 TB/s); gradients of 8192 rows of 4096 channels 52 us (0.2 GB and

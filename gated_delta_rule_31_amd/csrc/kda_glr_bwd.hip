@@ -10,7 +10,7 @@
 // the right, U rows at a time: their states again from the one that the forward kept in front of them, then m and
 // the gradients.  Bound by
 // memory: four rows read and three written (a gate and an input gate, bf16: 14 bytes a number).  8192 rows of 4096
-// channels: A and Q 27 us, the pass over the tiles 5, the rows 100 us (0.49 GB with the kept states, 4.9 TB/s; a large copy
+// channels: A and Q 27 us, the pass over the tiles 5, the rows 102 us (0.49 GB with the kept states, 4.8 TB/s; a large copy
 // has 5.0), the sums 9.  With a row's gates kept instead of what its lambda is multiplied by, a wave more than fills half of a
 // SIMD's registers: 184 us.
 #include "kda_glr.h"

@@ -2,7 +2,7 @@
 //
 // Bound by memory and the vector units: a number takes 33 instructions, six of them transcendental, in each of the two
 // launches that read the rows, and the first has them from memory, the second partly from the last-level cache.  7957 packed
-// rows of 4096 channels, bf16, logits and input gate: A and H 53 us (0.2 GB), the pass over the tiles 5, the rows 50 (0.26 GB);
+// rows of 4096 channels, bf16, logits and input gate: A and H 52 us (0.2 GB), the pass over the tiles 5, the rows 52 (0.26 GB);
 // a large copy takes 52 us for 0.26 GB.  131072 rows of 256 channels, log decays as given: 45, 14 and 42 us.
 #include "kda_glr.h"
 

@@ -11,6 +11,9 @@
   the next block in one call; ``block_norm_bwd`` -- its gradients; ``block_norm(...)`` -- recorded;
   ``gated_norm(y, gate, weight)`` -- a recurrence's heads: norm and gate alone, recorded.
 
+Sequences of a packed batch do not reach each other, whatever they hold.  Forward-mode derivatives are refused, as
+everywhere in the library.
+
 The decode calls take ``slots``, ``start`` and ``lengths`` as ``gdr_recurrent_step`` does, so that a
 layer's convolution, recurrence and drafts go by one table.
 """
@@ -292,7 +295,7 @@ def glr_bwd(x: torch.Tensor, gate: torch.Tensor, d_out: torch.Tensor, log_scale:
     d_in_gate, d_log_scale, d_bias, d_initial_state), each like what it is the gradient of (float32
     for the last three; None for what was not given).  ``kept``: the third of what ``glr_fwd(...,
     keep=True)`` returned for the same inputs; without it the states are made again.  Rows behind the
-    last packed sequence get zeros."""
+    last packed sequence get zeros.  Infinite logits have the gradients of large ones (0)."""
     x, x_stride, gate, gate_stride, log_scale, bias, in_gate, in_stride = _glr_inputs(x, gate, log_scale, bias, in_gate)
     B, T, H, K = x.shape
     cu_seqlens, N = _sequences(cu_seqlens, x, B)
@@ -431,7 +434,8 @@ def block_norm_fwd(y: torch.Tensor, gate: Optional[torch.Tensor] = None, residua
     p = y / rms(y) weight_after (``norm_after``; else y), h = residual + scale act(gate) p (act: sigmoid, or
     silu), n = h / rms(h) weight_before (``norm_before``), rms(x) = sqrt(mean x^2 + eps).  y, gate
     float32 or bfloat16 (the gate a slice of a wider tensor without a copy); residual like y or
-    float32; weights [D] float32, None for ones.  Returns (h like the residual, or like y without
+    float32; weights [D] float32, None for ones.  The sums of a row's squares, of y and of h where they are
+    normed, must be finite in float32.  Returns (h like the residual, or like y without
     one; n like y, or None).  ``out``: where h is written."""
     y, gate, gate_strides, weight_after, weight_before, flags, (tokens, heads, D) = _norm_inputs(y, gate, weight_after, weight_before, norm_after,
                                                                                                norm_before, silu)
@@ -456,7 +460,8 @@ def block_norm_bwd(y: torch.Tensor, d_h: Optional[torch.Tensor], d_n: Optional[t
                    eps: float = 1e-6, silu: bool = False, workspace: Optional[torch.Tensor] = None):
     """Gradients of ``block_norm_fwd`` for L = <d_h, h> + <d_n, n>: (dy, d_gate, d_residual, d_weight_after,
     d_weight_before), None for what was not given.  h as the forward returned it, d_h like h (None:
-    zeros) and d_n like y; without ``norm_before`` h and d_n are not used, and d_residual is d_h."""
+    zeros) and d_n like y; without ``norm_before`` h and d_n are not used, and d_residual is d_h; without ``norm_after`` dy does not
+    depend on y."""
     y, gate, gate_strides, weight_after, weight_before, flags, (tokens, heads, D) = _norm_inputs(y, gate, weight_after, weight_before, norm_after,
                                                                                                norm_before, silu)
     dev = y.device

@@ -467,13 +467,18 @@ kda_status kda_draft_verify(const float *target_probs, const int32_t *draft_toke
  *   - Weights, biases and scales are float32.
  *   - cu_seqlens, num_seqs and the empty-sequence rule are those of kda_gdr_chunk_fwd (rows behind
  *     the last sequence are left as they were, their gradients are zeros; offsets out of range or
- *     order move boundaries, never an access).  final_state must not be initial_state.
- *   - Pointers need the alignment of their elements; where all rows begin on 16-byte borders they
- *     are read 16 bytes at a time, otherwise number by number.
+ *     order move boundaries, never an access: the results, states among them, are then unspecified).
+ *     final_state must not be initial_state.  Nothing of one sequence, infinities and NaN among it, reaches another's
+ *     rows, states or their gradients (the weights' gradients are sums over all).
+ *   - Pointers need the alignment of their elements (KDA_ERR_BAD_ARGUMENT otherwise).  Where the rows' borders and
+ *     widths allow it they are read several numbers at a time: two (convolution and recurrence) or four (the
+ *     convolution's gradients), 16 bytes or two numbers (norms).
  *   - Fewer than 2^31 - 64 rows, at most 2^20 channels, fewer than 2^31 numbers in all sequences'
  *     states and as many threads in a grid (KDA_ERR_UNSUPPORTED otherwise).
- *   - Every result is the same bit for bit in every call on the same data.
- *   - Sums, states and gates are float32; outputs are rounded once.
+ *   - Every result is the same bit for bit in every call on the same data in the same layout (how rows are read may
+ *     change the order of a weight's sums).
+ *   - Sums, states and gates are float32; outputs are rounded once.  alpha itself is rounded to float32, so the rate
+ *     1 - alpha = d of a slow channel is off by about 2^-24 / d of itself, as it is token by token.
  */
 
 /* silu(x) = x sigmoid(x) behind the convolution, or as the gate of a norm instead of sigmoid */
