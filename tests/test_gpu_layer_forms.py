@@ -505,3 +505,47 @@ def test_batch_padded_with_empty_sequences(many):
         for u, v in zip(got[:-1], want[:-1]):
             assert torch.equal(u, v)
         assert torch.equal(got[-1][real], want[-1]) and torch.equal(got[-1][empty], handed[empty])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_recorded_block_in_a_graph(dtype):
+    """Forward and backward of the recorded calls, one after another as in a block, captured and replayed with new inputs in place
+    between eager passes: every replay gives the eager results' bits.  Thirty rows behind the last sequence."""
+    lens, H, K = [60, 70, 0, 30], 2, 24
+    T, C, cu = sum(lens) + 30, H * K, gpu(offsets(lens))
+
+    def make(seed):
+        r = gen(seed)
+        rows = [r(1, T, n).to(dtype) for n in (C, C, 4 * C)]
+        return [gpu(t) for t in rows + [r(C, 4) / 2, r(C), 0.2 * r(H), r(H, K), 1 + 0.2 * r(C), 1 + 0.2 * r(K), r(4, 3, C).to(dtype), r(4, H, K)] +
+                [r(1, T, C).to(dtype), r(1, T, C).to(dtype), r(4, 3, C).to(dtype), r(4, H, K)]]
+
+    def turn(data):
+        leaves = [t.detach().requires_grad_() for t in data[:11]]
+        y, x, u, w, b, ls, bias, norm, head, s, s0 = leaves
+        h, n = kda.block_norm(y, residual=x, weight_after=norm, weight_before=norm, scale=0.5, silu=True)
+        v, rows = kda.short_conv(u[..., :C] + n, w, b, s, cu_seqlens=cu)
+        part = lambda k: u[..., k * C : (k + 1) * C].unflatten(-1, (H, K))  # noqa: E731
+        o, state = kda.gated_linear_recurrence(v.unflatten(-1, (H, K)), part(1), ls, bias, part(2), initial_state=s0, cu_seqlens=cu)
+        outs = [h, kda.gated_norm(o, part(3), head).flatten(-2), rows, state]
+        return outs + list(torch.autograd.grad(outs, leaves, data[11:]))
+    static = make(90)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        turn(static)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = turn(static)
+    for seed in (91, 92, 93):
+        new = make(seed)
+        for t, m in zip(static, new):
+            t.copy_(m)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = turn(new)
+        torch.cuda.synchronize()
+        for k, (p, q) in enumerate(zip(got, want)):
+            assert torch.isfinite(p).all() and torch.equal(p, q), k
